@@ -319,6 +319,112 @@ int ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int
              const void* x, const float* dt, const float* A, const void* B, const void* C,
              const float* D, const float* state, float* new_state, void* y, void* stream);
 
+/*
+ * The gated delta rule: a recurrence that corrects its memory instead of adding to it.  Per value
+ * head, with the state H [p, r] and a_t = exp(g_t):
+ *   e_t = v_t - a_t H_{t-1} k_t            (what the decayed state gets wrong about v_t at k_t)
+ *   H_t = a_t H_{t-1} + beta_t e_t k_t^T
+ *   y_t = scale H_t q_t,                   H_{-1} = init
+ * Layouts (b batch, s tokens, hk key heads, h value heads, p headdim, r dstate; value head j reads
+ * key head j / (h / hk)):
+ *   q, k         [b, s, hk, r]  io dtype, strided     v  [b, s, h, p]  io dtype, strided
+ *   g, beta      [b, s, h]      fp32 (g: the log decay, <= 0 for a decay; -inf forgets the state)
+ *   y, dy, d_v   [b, s, h, p]   io dtype, contiguous  d_q, d_k  [b, s, hk, r]  io dtype, contiguous
+ *   init, final_state, d_final, d_init  [b, h, p, r]  fp32;   d_g, d_beta  [b, s, h]  fp32
+ * q, k and v are read through the element strides (batch, token, head) of dims, with their last
+ * axis contiguous, so they may be slices of one projection's output.
+ *   batch >= 0, seq >= 0 (an empty sequence: final = init, d_init = d_final); nheads a multiple of
+ *   kheads; headdim and dstate in {16, 32, 64, 128}; any seq.
+ *   q, k 16-byte aligned with strides of whole 16 bytes; y, dy and the gradients of io dtype
+ *   16-byte (8-byte for bf16) aligned; states 16-byte aligned.
+ *   valid_len    [b]  HOST int64, nullable (NULL = all of seq), each in [0, seq]: tokens at or past
+ *   it are not read, leave the state alone, and give y and gradients of exactly zero.
+ * bf16 io: the products take the bf16 inputs as they are and everything else (states, decays, the
+ * triangular inverse, sums) in fp32; y, d_q, d_k, d_v are rounded to nearest even.  Results are
+ * bitwise reproducible.  No launch exceeds 2^32 work-items: batch * nheads * max(8 * (seq + 63),
+ * 8 * headdim) < 2^32 (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
+ * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,
+ * SSD_ERR_HIP.
+ */
+typedef struct ssd_delta_dims {
+    int64_t batch;   /* b */
+    int64_t seq;     /* s */
+    int64_t kheads;  /* hk */
+    int64_t nheads;  /* h */
+    int64_t headdim; /* p */
+    int64_t dstate;  /* r */
+    int64_t q_stride[3], k_stride[3], v_stride[3]; /* elements: batch, token, head (each >= 0) */
+    float scale;     /* of the outputs; the usual choice is 1 / sqrt(r) */
+    int32_t io_dtype;
+} ssd_delta_dims;
+
+/* Workspace bytes (256-byte aligned buffer) of ssd_delta_fwd (bwd == 0) or ssd_delta_bwd. */
+int ssd_delta_workspace_size(const ssd_delta_dims* dims, int bwd, size_t* bytes);
+
+/*
+ * Outputs of a whole sequence, chunk by chunk.  final_state and init are nullable (not written;
+ * zero initial state).  Nothing is saved for the backward.
+ */
+int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, const void* v,
+                  const float* g, const float* beta, const float* init, const int64_t* valid_len,
+                  void* y, float* final_state, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of <dy, y> + <d_final, final_state> from the leaves (the states are recomputed).
+ * d_final and init nullable (= zero), d_init nullable (not written); the other gradients are
+ * required.  d_q and d_k are summed over the value heads that share a key head.
+ */
+int ssd_delta_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_final, const void* q,
+                  const void* k, const void* v, const float* g, const float* beta,
+                  const float* init, const int64_t* valid_len, void* d_q, void* d_k, void* d_v,
+                  float* d_g, float* d_beta, float* d_init, void* ws, size_t ws_bytes,
+                  void* stream);
+
+/*
+ * One token from cached states, updated in place (decoding).  dims.seq must be 1 (token strides
+ * are not used).
+ *   state [nslots, h, p, r] fp32, the pool the sequences' states live in
+ *   slots [b] DEVICE int32, nullable (NULL: row i has slot i, nslots >= batch): the slot of each
+ *         row of the batch.  A row whose slot is outside [0, nslots) is idle: y = 0 and no state
+ *         is touched (its other inputs may hold anything).  Two rows may not share a slot.
+ *   q, k [b, hk, r], v [b, h, p] strided as above; g, beta [b, h]; y [b, h, p]
+ * No workspace; may be captured into a graph.
+ */
+int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, const void* k,
+                   const void* v, const float* g, const float* beta, float* state,
+                   const int32_t* slots, void* y, void* stream);
+
+/*
+ * Root-mean-square norm over rows, with the residual's addition and an 8-bit output:
+ *   s = x + residual (s = x without one),   n = s / sqrt(mean(s^2) + eps),   y = n weight
+ *   8 bits: per group of `group` values of a row (0: the row), scale = max|y| / 448, or 1 where y
+ *   is all zero, and y8 = y / scale rounded to nearest even in e4m3 (no infinities, largest 448).
+ *   x, residual, s, y  [rows, width] io dtype;   weight [width] fp32
+ *   y8 [rows, width] bytes;   scale [rows, width / group] fp32
+ * residual is nullable; s is required with a residual (it may be the residual itself) and must be
+ * NULL without one; y is nullable if y8 is given; y8 and scale come together or not at all.
+ * rows >= 0, 0 < width <= 32768, group 0 or 32, 64, 128 or 256 and dividing width.  Tensors are
+ * contiguous and 16-byte aligned.  s is rounded to the io dtype where it is stored; the norm is
+ * taken of the fp32 sum, and y and y8 are each rounded once from fp32.
+ * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_HIP.
+ */
+int ssd_rms_norm(int64_t rows, int64_t width, int io_dtype, float eps, const void* x,
+                 const void* residual, const float* weight, int64_t group, void* s, void* y,
+                 void* y8, float* scale, void* stream);
+
+/*
+ * Gradient of <dy, y> + <d_s, s> at the stored s (x where there was no residual); the sum passes
+ * the same gradient to x and to the residual:
+ *   d_x = d_s + (weight dy - n mean(n weight dy)) / sqrt(mean(s^2) + eps)   [rows, width] io dtype
+ *   d_weight = sum over rows of dy n                                        [width] fp32
+ * d_s is nullable (= zero); d_x may be d_s.  The workspace (ssd_rms_norm_workspace_size, 256-byte
+ * aligned) holds partial sums of d_weight, which are added in a fixed order.
+ */
+int ssd_rms_norm_bwd(int64_t rows, int64_t width, int io_dtype, float eps, const void* dy,
+                     const void* s, const void* d_s, const float* weight, void* d_x,
+                     float* d_weight, void* ws, size_t ws_bytes, void* stream);
+int ssd_rms_norm_workspace_size(int64_t rows, int64_t width, size_t* bytes);
+
 /* Message for the last nonzero status returned on this thread ("" if none). */
 const char* ssd_last_error(void);
 

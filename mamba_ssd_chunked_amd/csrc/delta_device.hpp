@@ -1,0 +1,135 @@
+// Device-side building blocks of the gated delta rule (gfx950, wave64).
+//
+// Every product runs on the bf16 matrix cores (16x16x32).  An fp32 operand is cut into
+// three bf16 parts, each the rounded remainder of the ones before it, which together
+// hold all 24 bits; a bf16 input is one part.  A product of an a-part and a b-part
+// operand sums the pairs whose combined weight reaches fp32's last bit: 1 x 3 parts take
+// three MFMAs, 3 x 3 six, and accumulate in fp32.  (An fp32 MFMA takes the time of about
+// sixteen bf16 ones for the same product: v_mfma_f32_16x16x4_f32 issues in 32 cycles for
+// k = 4, v_mfma_f32_16x16x32_bf16 in 16 for k = 32.)
+//
+// Operand and result layout of the 16x16x32 MFMA, for lane L (i = L % 16, g = L / 16):
+// operands hold row / column i and eight k values, results hold D[4g + v][i], v = 0..3.
+// Which k a slot means is free as long as both operands agree, so two results stacked
+// along their row axis serve as the next product's operand without moving between lanes:
+// slots 0..3 are rows 4g..4g+3 of the even tile, slots 4..7 of the odd one.
+#pragma once
+
+#include "ssd_device.hpp"
+
+namespace ssd {
+
+constexpr int DL = 64;         // tokens per chunk of the delta rule
+constexpr int DTRI = 6;        // 16 x 32 operand tiles of a triangular 64 x 64 matrix
+constexpr int DTILE = 64 * 8;  // bf16 values of one operand tile (8 per lane)
+constexpr int DCOEF = 5 * DL;  // floats of a chunk's coefficients: e^G, e^{G_L - G}, beta, G in base 2 (fp64)
+
+// Buffers of the scans, typed.
+template <class T>
+struct DeltaScan {
+    const T *q, *k, *v, *dy;
+    T* y;
+    const int64_t* len;
+    const float *init, *d_final;
+    float *final_state, *d_init;
+    float* coef;
+    uint16_t *M, *P, *NT;
+    float *H, *E, *dH, *dZ;
+};
+
+template <int N>
+struct Parts {
+    b8v p[N];
+};
+
+// Eight fp32 values as N bf16 parts, each rounded to nearest even.
+template <int N>
+__device__ __forceinline__ Parts<N> split8(const float (&x)[8]) {
+    Parts<N> o;
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = f32x2_to_bf16x2(r[2 * e], r[2 * e + 1]);
+            if (n + 1 < N) {
+                r[2 * e] -= __uint_as_float(w[e] << 16);
+                r[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+        o.p[n] = __builtin_bit_cast(b8v, *reinterpret_cast<const uint4*>(w));
+    }
+    return o;
+}
+template <int N>
+__device__ __forceinline__ Parts<N> split44(v4f a, v4f b) {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return split8<N>(x);
+}
+
+template <int NA, int NB>
+__device__ __forceinline__ v4f mma(const Parts<NA>& a, const Parts<NB>& b, v4f c) {
+    constexpr int K = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int s = K; s >= 0; --s)  // the small terms first
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], c, 0, 0, 0);
+    return c;
+}
+
+// The result of a 16x16x32 MFMA may be read by other instructions eight wait states after its
+// issue; the compiler counts them inside a loop body but not across its back edge (clang 22 of
+// ROCm 7.2 read an accumulator two states after the last MFMA of the iteration before: wrong
+// values in the registers written last).  To stand at the end of a loop body that carries
+// accumulators.
+__device__ __forceinline__ void mfma_settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 7\n\ts_nop 3" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Four bf16 of one column out of a row-major LDS matrix: the 16 lanes of a group address
+// four rows x 16 columns, 8 bytes each (lane i: row i / 4, columns 4 (i % 4) .. + 3), and
+// lane i receives column i of the four rows.
+typedef s4 __attribute__((address_space(3))) lds_s4;
+__device__ __forceinline__ s4 lds_col4(const uint16_t* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
+}
+__device__ __forceinline__ b8v join8(s4 a, s4 b) {
+    typedef short s8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(b8v, s8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+}
+
+// Operand tile numbers of a lower (upper) triangular 64 x 64 matrix in row tiles tau of 16
+// and k steps j of 32: the six tiles that are not zero.
+__device__ __forceinline__ constexpr int tri_lower(int tau, int j) { return tau < 2 ? tau : 2 * (tau - 1) + j; }
+__device__ __forceinline__ constexpr int tri_upper(int tau, int j) { return tau < 2 ? 2 * tau + j : tau + 2; }
+
+// Eight consecutive values of a token row as parts, zeros where !on.
+template <class IO>
+__host__ __device__ constexpr int in_parts() { return sizeof(typename IO::T) == 2 ? 1 : 3; }
+
+template <class IO>
+__device__ __forceinline__ Parts<in_parts<IO>()> load_parts8(const typename IO::T* p, bool on) {
+    Parts<in_parts<IO>()> o;
+    if constexpr (in_parts<IO>() == 1) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (on) w = *reinterpret_cast<const uint4*>(p);
+        o.p[0] = __builtin_bit_cast(b8v, w);
+    } else {
+        v4f a = zero4(), b = zero4();
+        if (on) {
+            a = *reinterpret_cast<const v4f*>(p);
+            b = *reinterpret_cast<const v4f*>(p + 4);
+        }
+        o = split44<3>(a, b);
+    }
+    return o;
+}
+
+}  // namespace ssd

@@ -446,6 +446,115 @@ int fwd_impl(const char* who, const ssd_dims* dims, const void* x, const float* 
     return ok();
 }
 
+// ------------------------------------------------------------ gated delta rule, norm
+int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape* d) {
+    if (!dims) return fail(SSD_ERR_NULL, "%s: dims is NULL", who);
+    if (dims->io_dtype != SSD_F32 && dims->io_dtype != SSD_BF16)
+        return fail(SSD_ERR_DTYPE, "%s: io_dtype must be SSD_F32 (0) or SSD_BF16 (1) (got %d)", who, dims->io_dtype);
+    if (dims->batch < 0 || dims->seq < 0 || dims->kheads <= 0 || dims->nheads <= 0 || dims->headdim <= 0 ||
+        dims->dstate <= 0 || dims->nheads % dims->kheads != 0)
+        return fail(SSD_ERR_SHAPE, "%s: need batch, seq >= 0, kheads, headdim, dstate > 0 and nheads a multiple of "
+                    "kheads (got b=%lld s=%lld hk=%lld h=%lld p=%lld r=%lld)", who, (long long)dims->batch,
+                    (long long)dims->seq, (long long)dims->kheads, (long long)dims->nheads,
+                    (long long)dims->headdim, (long long)dims->dstate);
+    if (!pow2_in(dims->headdim, 16, 128) || !pow2_in(dims->dstate, 16, 128))
+        return fail(SSD_ERR_UNSUPPORTED, "%s: headdim and dstate must be 16, 32, 64 or 128 (got %lld, %lld)", who,
+                    (long long)dims->headdim, (long long)dims->dstate);
+    // a workgroup of at most 512 work-items per chunk of 64 tokens and head, and two of 4 per
+    // value column and head
+    const double per_bh = std::max(8.0 * ((double)dims->seq + 63.0), 8.0 * (double)dims->headdim);
+    if (dims->batch > (1 << 30) || dims->seq > (1 << 30) || dims->nheads > (1 << 30) ||
+        (double)dims->batch * dims->nheads * per_bh > ssd::kMaxGridItems)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch would exceed 2^32 work-items "
+                    "(split the batch or the heads)", who);
+    const int64_t unit = dims->io_dtype == SSD_BF16 ? 8 : 4;  // 16 bytes
+    for (int k = 0; k < 3; ++k) {
+        if (dims->q_stride[k] < 0 || dims->k_stride[k] < 0 || dims->v_stride[k] < 0)
+            return fail(SSD_ERR_SHAPE, "%s: strides must not be negative", who);
+        if (dims->q_stride[k] % unit || dims->k_stride[k] % unit)
+            return fail(SSD_ERR_UNSUPPORTED, "%s: strides of q and k must be whole 16 bytes", who);
+        d->qs[k] = dims->q_stride[k];
+        d->ks[k] = dims->k_stride[k];
+        d->vs[k] = dims->v_stride[k];
+    }
+    d->B = (int)dims->batch;
+    d->S = (int)dims->seq;
+    d->HK = (int)dims->kheads;
+    d->H = (int)dims->nheads;
+    d->P = (int)dims->headdim;
+    d->R = (int)dims->dstate;
+    d->io = dims->io_dtype;
+    d->N = (int)((dims->seq + 63) / 64);
+    d->scale = dims->scale;
+    return SSD_OK;
+}
+
+int check_delta_lens(const char* who, const ssd::DeltaShape& d, const int64_t* valid_len) {
+    if (!valid_len) return SSD_OK;
+    for (int b = 0; b < d.B; ++b)
+        if (valid_len[b] < 0 || valid_len[b] > d.S)
+            return fail(SSD_ERR_SHAPE, "%s: valid_len[%d] = %lld is outside [0, %d]", who, b,
+                        (long long)valid_len[b], d.S);
+    return SSD_OK;
+}
+
+// Workspace of the delta rule: the lengths, then per chunk and head the coefficients and the
+// triangular operands (6 tiles of 512 bf16 values a part); the backward adds the other triangular
+// operands, the entry states and the gradients of the leaving states, E and dZ.
+size_t delta_plan(const ssd::DeltaShape& d, bool bwd, void* ws, ssd::DeltaBufs* f) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char* at = static_cast<char*>(ws) + off;
+        off += round_up(bytes);
+        return at;
+    };
+    const size_t n = static_cast<size_t>(d.chunk_heads()), tri = 6 * 512 * 2;
+    const size_t state = 4 * static_cast<size_t>(d.P) * d.R, rows = 4 * static_cast<size_t>(64) * d.P;
+    f->len = reinterpret_cast<int64_t*>(take(8 * static_cast<size_t>(d.B)));
+    f->coef = reinterpret_cast<float*>(take(5 * 64 * 4 * n));
+    f->M = reinterpret_cast<uint16_t*>(take(3 * tri * n));
+    f->P = reinterpret_cast<uint16_t*>(take((bwd || d.io == SSD_F32 ? 3 : 2) * tri * n));
+    if (bwd) {
+        f->NT = reinterpret_cast<uint16_t*>(take(3 * tri * n));
+        f->H = reinterpret_cast<float*>(take(state * n));
+        f->dH = reinterpret_cast<float*>(take(state * n));
+        f->E = reinterpret_cast<float*>(take(rows * n));
+        f->dZ = reinterpret_cast<float*>(take(rows * n));
+    }
+    return off;
+}
+
+int check_delta_ws(const char* who, size_t need, const void* ws, size_t ws_bytes) {
+    if (!ws || ws_bytes < need)
+        return fail(SSD_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu%s)", who, need, ws_bytes,
+                    ws ? "" : ", NULL pointer");
+    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: workspace is not 256-byte aligned", who);
+    return SSD_OK;
+}
+
+int validate_norm(const char* who, int64_t rows, int64_t width, int io_dtype, float eps, ssd::NormShape* n) {
+    if (io_dtype != SSD_F32 && io_dtype != SSD_BF16)
+        return fail(SSD_ERR_DTYPE, "%s: io_dtype must be SSD_F32 (0) or SSD_BF16 (1) (got %d)", who, io_dtype);
+    if (rows < 0 || width <= 0 || !(eps >= 0.0f))
+        return fail(SSD_ERR_SHAPE, "%s: need rows >= 0, width > 0 and eps >= 0 (got %lld, %lld, %g)", who,
+                    (long long)rows, (long long)width, (double)eps);
+    if (width > 32768)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: width must be at most 32768 (got %lld)", who, (long long)width);
+    // a team of at most 1024 work-items per row
+    if (rows > (1 << 22) - 1)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch could exceed 2^32 work-items "
+                    "(split the rows)", who);
+    *n = ssd::NormShape{rows, (int)width, (int)width, io_dtype, eps};
+    return SSD_OK;
+}
+
+int check_aligned16(std::initializer_list<std::pair<const void*, const char*>> ptrs) {
+    for (auto& p : ptrs)
+        if (int rc = check_align(p.first, p.second, 16)) return rc;
+    return SSD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -942,6 +1051,178 @@ int ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int
     ssd::StepShape s{(int)batch, (int)nheads, (int)headdim, (int)dstate, io_dtype};
     hipStream_t st = static_cast<hipStream_t>(stream);
     SSD_HIP(ssd::launch_step(s, x, dt, A, B, C, D, state, new_state, y, st), "k_step");
+    return ok();
+}
+
+int ssd_delta_workspace_size(const ssd_delta_dims* dims, int bwd, size_t* bytes) {
+    ssd::DeltaShape d;
+    if (int rc = validate_delta("ssd_delta_workspace_size", dims, &d)) return rc;
+    if (!bytes) return fail(SSD_ERR_NULL, "ssd_delta_workspace_size: bytes is NULL");
+    ssd::DeltaBufs f{};
+    *bytes = delta_plan(d, bwd != 0, nullptr, &f);
+    return ok();
+}
+
+int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, const void* v, const float* g,
+                  const float* beta, const float* init, const int64_t* valid_len, void* y, float* final_state,
+                  void* ws, size_t ws_bytes, void* stream) {
+    const char* who = "ssd_delta_fwd";
+    ssd::DeltaShape d;
+    if (int rc = validate_delta(who, dims, &d)) return rc;
+    const bool tok = d.B > 0 && d.N > 0;
+    if (tok && (!q || !k || !v || !g || !beta || !y))
+        return fail(SSD_ERR_NULL, "%s: q, k, v, g, beta and y are required", who);
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {init, "init"}, {final_state, "final_state"}})) return rc;
+    if (int rc = check_align(y, "y", d.io == SSD_BF16 ? 8 : 16)) return rc;
+    if (int rc = check_delta_lens(who, d, valid_len)) return rc;
+    ssd::DeltaBufs f{};
+    const size_t need = delta_plan(d, false, ws, &f);
+    if (tok)
+        if (int rc = check_delta_ws(who, need, ws, ws_bytes)) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (!tok) {
+        const int64_t nstate = static_cast<int64_t>(d.B) * d.H * d.P * d.R;
+        if (final_state) SSD_HIP(ssd::launch_copy_or_zero(final_state, init, nstate, st), "copy init");
+        return ok();
+    }
+    if (valid_len)
+        SSD_HIP(ssd::launch_set_i64(const_cast<int64_t*>(f.len), valid_len, d.S, d.B, st), "set_i64");
+    else
+        f.len = nullptr;
+    f.q = q;
+    f.k = k;
+    f.v = v;
+    f.g = g;
+    f.beta = beta;
+    f.init = init;
+    f.y = y;
+    f.final_state = final_state;
+    SSD_HIP(ssd::launch_delta_prep(d, f, false, st), "k_delta_prep");
+    SSD_HIP(ssd::launch_delta_scan(d, f, false, st), "k_delta_scan");
+    return ok();
+}
+
+int ssd_delta_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_final, const void* q, const void* k,
+                  const void* v, const float* g, const float* beta, const float* init, const int64_t* valid_len,
+                  void* d_q, void* d_k, void* d_v, float* d_g, float* d_beta, float* d_init, void* ws,
+                  size_t ws_bytes, void* stream) {
+    const char* who = "ssd_delta_bwd";
+    ssd::DeltaShape d;
+    if (int rc = validate_delta(who, dims, &d)) return rc;
+    const bool tok = d.B > 0 && d.N > 0;
+    if (tok && (!dy || !q || !k || !v || !g || !beta || !d_q || !d_k || !d_v || !d_g || !d_beta))
+        return fail(SSD_ERR_NULL, "%s: dy, q, k, v, g, beta, d_q, d_k, d_v, d_g and d_beta are required", who);
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {init, "init"}, {d_final, "d_final"}, {d_init, "d_init"}}))
+        return rc;
+    const size_t ia = d.io == SSD_BF16 ? 8 : 16;
+    for (auto& p : {std::pair<const void*, const char*>{dy, "dy"}, {d_q, "d_q"}, {d_k, "d_k"}, {d_v, "d_v"}})
+        if (int rc = check_align(p.first, p.second, ia)) return rc;
+    if (int rc = check_delta_lens(who, d, valid_len)) return rc;
+    ssd::DeltaBufs f{};
+    const size_t need = delta_plan(d, true, ws, &f);
+    if (tok)
+        if (int rc = check_delta_ws(who, need, ws, ws_bytes)) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (!tok) {
+        const int64_t nstate = static_cast<int64_t>(d.B) * d.H * d.P * d.R;
+        if (d_init) SSD_HIP(ssd::launch_copy_or_zero(d_init, d_final, nstate, st), "copy d_final");
+        return ok();
+    }
+    if (valid_len)
+        SSD_HIP(ssd::launch_set_i64(const_cast<int64_t*>(f.len), valid_len, d.S, d.B, st), "set_i64");
+    else
+        f.len = nullptr;
+    f.q = q;
+    f.k = k;
+    f.v = v;
+    f.dy = dy;
+    f.g = g;
+    f.beta = beta;
+    f.init = init;
+    f.d_final = d_final;
+    f.d_q = d_q;
+    f.d_k = d_k;
+    f.d_v = d_v;
+    f.d_g = d_g;
+    f.d_beta = d_beta;
+    f.d_init = d_init;
+    SSD_HIP(ssd::launch_delta_prep(d, f, true, st), "k_delta_prep");
+    SSD_HIP(ssd::launch_delta_scan(d, f, true, st), "k_delta_states");
+    SSD_HIP(ssd::launch_delta_grad(d, f, st), "k_delta_grad");
+    return ok();
+}
+
+int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, const void* k, const void* v,
+                   const float* g, const float* beta, float* state, const int32_t* slots, void* y, void* stream) {
+    const char* who = "ssd_delta_step";
+    ssd::DeltaShape d;
+    if (int rc = validate_delta(who, dims, &d)) return rc;
+    if (d.S != 1) return fail(SSD_ERR_SHAPE, "%s: seq must be 1 (got %d)", who, d.S);
+    if (nslots < 0 || nslots > INT32_MAX || (!slots && nslots < d.B))
+        return fail(SSD_ERR_SHAPE, "%s: nslots = %lld: need at least one slot per row without slots", who,
+                    (long long)nslots);
+    // one workgroup of 256 work-items per (b, h)
+    if ((double)d.B * d.H * 256.0 > ssd::kMaxGridItems)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch would exceed 2^32 work-items "
+                    "(split the batch)", who);
+    if (d.B == 0) return ok();
+    if (!q || !k || !v || !g || !beta || !y || (!state && nslots > 0))
+        return fail(SSD_ERR_NULL, "%s: q, k, v, g, beta, state and y are required", who);
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {state, "state"}})) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    SSD_HIP(ssd::launch_delta_step(d, (int)nslots, q, k, v, g, beta, state, slots, y, st), "k_delta_step");
+    return ok();
+}
+
+int ssd_rms_norm(int64_t rows, int64_t width, int io_dtype, float eps, const void* x, const void* residual,
+                 const float* weight, int64_t group, void* s, void* y, void* y8, float* scale, void* stream) {
+    const char* who = "ssd_rms_norm";
+    ssd::NormShape n;
+    if (int rc = validate_norm(who, rows, width, io_dtype, eps, &n)) return rc;
+    if (group != 0 && (!pow2_in(group, 32, 256) || width % group != 0))
+        return fail(SSD_ERR_UNSUPPORTED, "%s: group must be 0, or 32, 64, 128 or 256 and divide width (got %lld for "
+                    "width %lld)", who, (long long)group, (long long)width);
+    if (group != 0) n.group = (int)group;
+    if (rows == 0) return ok();
+    if (!x || !weight || (!y && !y8))
+        return fail(SSD_ERR_NULL, "%s: x, weight and one of y and y8 are required", who);
+    if (!residual != !s) return fail(SSD_ERR_NULL, "%s: residual and s come together or not at all", who);
+    if (!y8 != !scale) return fail(SSD_ERR_NULL, "%s: y8 and scale come together or not at all", who);
+    if (int rc = check_aligned16({{x, "x"}, {residual, "residual"}, {weight, "weight"}, {s, "s"}, {y, "y"},
+                                  {y8, "y8"}, {scale, "scale"}}))
+        return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    SSD_HIP(ssd::launch_rms_norm(n, x, residual, weight, s, y, y8, scale, st), "k_rms_norm");
+    return ok();
+}
+
+int ssd_rms_norm_workspace_size(int64_t rows, int64_t width, size_t* bytes) {
+    ssd::NormShape n;
+    if (int rc = validate_norm("ssd_rms_norm_workspace_size", rows, width, SSD_F32, 0.0f, &n)) return rc;
+    if (!bytes) return fail(SSD_ERR_NULL, "ssd_rms_norm_workspace_size: bytes is NULL");
+    *bytes = round_up(4 * static_cast<size_t>(ssd::rms_norm_parts(rows)) * static_cast<size_t>(width));
+    return ok();
+}
+
+int ssd_rms_norm_bwd(int64_t rows, int64_t width, int io_dtype, float eps, const void* dy, const void* s,
+                     const void* d_s, const float* weight, void* d_x, float* d_weight, void* ws, size_t ws_bytes,
+                     void* stream) {
+    const char* who = "ssd_rms_norm_bwd";
+    ssd::NormShape n;
+    if (int rc = validate_norm(who, rows, width, io_dtype, eps, &n)) return rc;
+    if (!weight || !d_weight || (rows > 0 && (!dy || !s || !d_x)))
+        return fail(SSD_ERR_NULL, "%s: dy, s, weight, d_x and d_weight are required", who);
+    if (int rc = check_aligned16({{dy, "dy"}, {s, "s"}, {d_s, "d_s"}, {weight, "weight"}, {d_x, "d_x"}})) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (rows == 0) {
+        SSD_HIP(ssd::launch_copy_or_zero(d_weight, nullptr, width, st), "zero d_weight");
+        return ok();
+    }
+    const size_t need = round_up(4 * static_cast<size_t>(ssd::rms_norm_parts(rows)) * static_cast<size_t>(width));
+    if (int rc = check_delta_ws(who, need, ws, ws_bytes)) return rc;
+    float* part = at<float>(ws, 0);
+    SSD_HIP(ssd::launch_rms_norm_bwd(n, dy, s, d_s, weight, d_x, part, st), "k_rms_norm_bwd");
+    SSD_HIP(ssd::launch_rms_norm_weight(n, part, d_weight, st), "k_rms_norm_weight");
     return ok();
 }
 

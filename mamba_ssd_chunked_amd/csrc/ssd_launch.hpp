@@ -286,4 +286,55 @@ hipError_t launch_step(const StepShape& s, const void* x, const float* dt, const
                        const void* B, const void* C, const float* D, const float* state,
                        float* new_state, void* y, hipStream_t st);
 
+// ---------------------------------------------------------------- gated delta rule
+struct DeltaShape {
+    int B, S, HK, H, P, R;  // batch, tokens, key heads, value heads, headdim, dstate
+    int io;                 // 0 = fp32, 1 = bf16
+    int N;                  // chunks of 64 tokens
+    float scale;
+    int64_t qs[3], ks[3], vs[3];  // element strides (batch, token, head) of q, k, v
+    int64_t chunk_heads() const { return static_cast<int64_t>(B) * H * N; }
+};
+
+// Everything the delta kernels read and write.  len: device copy of valid_len, or null.
+// Workspace, per (b, h, chunk): coef; M, P (forward and backward), NT (backward) in bf16
+// parts; the backward's entry states H and leaving gradients dH [r, p], E and dZ [64, p].
+struct DeltaBufs {
+    const void *q, *k, *v, *dy;
+    const float *g, *beta, *init, *d_final;
+    const int64_t* len;
+    void *y, *d_q, *d_k, *d_v;
+    float *final_state, *d_g, *d_beta, *d_init;
+    float* coef;
+    uint16_t *M, *P, *NT;
+    float *H, *E, *dH, *dZ;
+};
+
+// Decay factors and triangular operands of every chunk.
+hipError_t launch_delta_prep(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st);
+// The recurrence over chunks: y and the final state, or for the backward H, E, dH, dZ, d_init.
+hipError_t launch_delta_scan(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st);
+// The gradients of every chunk from H, E, dH, dZ.
+hipError_t launch_delta_grad(const DeltaShape& d, const DeltaBufs& f, hipStream_t st);
+
+// One token from the states of a pool of nslots; slots (device, may be null) picks each row's.
+hipError_t launch_delta_step(const DeltaShape& d, int nslots, const void* q, const void* k, const void* v,
+                             const float* g, const float* beta, float* state, const int32_t* slots, void* y,
+                             hipStream_t st);
+
+// ---------------------------------------------------------------- root-mean-square norm
+struct NormShape {
+    int64_t rows;
+    int width, group;  // group: values per 8-bit scale (divides width)
+    int io;
+    float eps;
+};
+hipError_t launch_rms_norm(const NormShape& n, const void* x, const void* residual, const float* weight,
+                           void* s, void* y, void* y8, float* scale, hipStream_t st);
+// Rows per partial sum of the weight gradient, and the number of partial sums.
+int64_t rms_norm_parts(int64_t rows);
+hipError_t launch_rms_norm_bwd(const NormShape& n, const void* dy, const void* s, const void* d_s,
+                               const float* weight, void* d_x, float* part, hipStream_t st);
+hipError_t launch_rms_norm_weight(const NormShape& n, const float* part, float* d_weight, hipStream_t st);
+
 }  // namespace ssd

@@ -14,6 +14,7 @@ raises immediately.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -31,7 +32,9 @@ STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_UNSUPP
 EXPORTS = ("ssd_workspace_size", "ssd_fwd", "ssd_fwd_noalloc", "ssd_bwd", "ssd_state_moments",
            "ssd_state_moments_bwd", "ssd_moments_pr", "ssd_moments_pr_bwd", "ssd_y_diag",
            "ssd_y_diag_bwd", "ssd_quat_scan", "ssd_quat_scan_bwd", "ssd_quat_workspace_size",
-           "ssd_step", "ssd_last_error", "ssd_debug_enable", "ssd_timing_enable",
+           "ssd_step", "ssd_delta_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd",
+           "ssd_delta_step", "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size",
+           "ssd_last_error", "ssd_debug_enable", "ssd_timing_enable",
            "ssd_timing_collect", "ssd_bwd_partial_region", "ssd_stream_probe")
 
 
@@ -45,6 +48,14 @@ class ssd_dims(ctypes.Structure):
         return ("ssd_dims(b=%d, n=%d, l=%d, h=%d, p=%d, r=%d, io=%d, kernel_chunk_len=%d)" %
                 (self.batch, self.nchunks, self.chunk_len, self.nheads, self.headdim,
                  self.dstate, self.io_dtype, self.kernel_chunk_len))
+
+
+class ssd_delta_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seq", ctypes.c_int64), ("kheads", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("scale", ctypes.c_float),
+                ("io_dtype", ctypes.c_int32)]
 
 
 class SsdError(RuntimeError):
@@ -82,6 +93,18 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_quat_scan_bwd.argtypes = [I64] * 4 + [P] * 6 + [ctypes.c_size_t, P]
     lib.ssd_quat_workspace_size.argtypes = [I64] * 4 + [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
     lib.ssd_step.argtypes = [I64] * 4 + [ctypes.c_int] + [P] * 10
+    E = ctypes.POINTER(ssd_delta_dims)
+    SZ, F = ctypes.c_size_t, ctypes.c_float
+    lib.ssd_delta_workspace_size.argtypes = [E, ctypes.c_int, ctypes.POINTER(SZ)]
+    lib.ssd_delta_fwd.argtypes = [E] + [P] * 10 + [SZ, P]
+    lib.ssd_delta_bwd.argtypes = [E] + [P] * 16 + [SZ, P]
+    lib.ssd_delta_step.argtypes = [E, I64] + [P] * 9
+    lib.ssd_rms_norm.argtypes = [I64, I64, ctypes.c_int, F] + [P] * 3 + [I64] + [P] * 5
+    lib.ssd_rms_norm_bwd.argtypes = [I64, I64, ctypes.c_int, F] + [P] * 7 + [SZ, P]
+    lib.ssd_rms_norm_workspace_size.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+    for f in ("ssd_delta_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd", "ssd_delta_step",
+              "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("ssd_workspace_size", "ssd_fwd", "ssd_fwd_noalloc", "ssd_bwd", "ssd_state_moments",
               "ssd_state_moments_bwd", "ssd_moments_pr", "ssd_moments_pr_bwd", "ssd_y_diag",
               "ssd_y_diag_bwd", "ssd_quat_scan", "ssd_quat_scan_bwd", "ssd_quat_workspace_size", "ssd_step"):
@@ -412,7 +435,150 @@ def ssd_step(x, dt, A, B, C, D, state, new_state, y, stream=None) -> int:
     return load_library().ssd_step(b, h, p, r, io, *args, _stream(stream))
 
 
+def _io_of(t: torch.Tensor, name: str) -> int:
+    io = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}.get(t.dtype)
+    if io is None:
+        raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    return io
+
+
+def _strided(t: torch.Tensor, name: str, dtype, shape):
+    """(pointer, element strides of all axes but the last) of a device tensor whose last axis is
+    contiguous; axes of one element get stride 0."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return ctypes.c_void_p(t.data_ptr()), [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape)]
+
+
+def _delta_args(q, k, v, scale):
+    """(dims, pointers of q, k, v) for q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]``."""
+    if q.dim() != 4 or v.dim() != 4 or q.shape[:2] != v.shape[:2]:
+        raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
+    b, s, hk, r = q.shape
+    h, p = v.shape[2:]
+    d = ssd_delta_dims(b, s, hk, h, p, r)
+    d.io_dtype = _io_of(q, "q")
+    d.scale = r ** -0.5 if scale is None else float(scale)
+    ptrs = []
+    for t, name, field, shape in ((q, "q", d.q_stride, q.shape), (k, "k", d.k_stride, q.shape),
+                                  (v, "v", d.v_stride, v.shape)):
+        ptr, strides = _strided(t, name, q.dtype, shape)
+        field[:] = strides
+        ptrs.append(ptr)
+    return d, ptrs
+
+
+def ssd_delta_workspace_size(dims: ssd_delta_dims, bwd: bool) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load_library().ssd_delta_workspace_size(ctypes.byref(dims), int(bool(bwd)), ctypes.byref(n))
+    if rc:
+        raise SsdError(rc, "ssd_delta_workspace_size", ssd_last_error())
+    return int(n.value)
+
+
+def ssd_delta_fwd(q, k, v, g, beta, init, valid_len, y, final_state, ws, scale=None, stream=None) -> int:
+    """q, k ``[b, s, hk, r]``, v ``[b, s, h, p]`` (last axis contiguous), g, beta ``[b, s, h]``;
+    scale None is ``1 / sqrt(r)``."""
+    d, qkv = _delta_args(q, k, v, scale)
+    f, tok, state = torch.float32, v.shape[0] * v.shape[1] * v.shape[2], d.batch * d.nheads * d.headdim * d.dstate
+    args = [_ptr(g, "g", f, tok, True), _ptr(beta, "beta", f, tok, True),
+            _ptr(init, "init", f, state, False),
+            _ptr(valid_len, "valid_len", torch.int64, d.batch, False),
+            _ptr(y, "y", q.dtype, v.numel(), True), _ptr(final_state, "final_state", f, state, False)]
+    wp, wb = _ws(ws)
+    return load_library().ssd_delta_fwd(ctypes.byref(d), *qkv, *args, wp, wb, _stream(stream))
+
+
+def ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, valid_len, d_q, d_k, d_v, d_g, d_beta, d_init, ws,
+                  scale=None, stream=None) -> int:
+    d, qkv = _delta_args(q, k, v, scale)
+    f, tok, state = torch.float32, v.shape[0] * v.shape[1] * v.shape[2], d.batch * d.nheads * d.headdim * d.dstate
+    head = [_ptr(dy, "dy", q.dtype, v.numel(), True), _ptr(d_final, "d_final", f, state, False)]
+    args = [_ptr(g, "g", f, tok, True), _ptr(beta, "beta", f, tok, True),
+            _ptr(init, "init", f, state, False),
+            _ptr(valid_len, "valid_len", torch.int64, d.batch, False),
+            _ptr(d_q, "d_q", q.dtype, q.numel(), True), _ptr(d_k, "d_k", q.dtype, q.numel(), True),
+            _ptr(d_v, "d_v", q.dtype, v.numel(), True), _ptr(d_g, "d_g", f, tok, True),
+            _ptr(d_beta, "d_beta", f, tok, True), _ptr(d_init, "d_init", f, state, False)]
+    wp, wb = _ws(ws)
+    return load_library().ssd_delta_bwd(ctypes.byref(d), *head, *qkv, *args, wp, wb, _stream(stream))
+
+
+def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -> int:
+    """q, k ``[b, hk, r]``, v ``[b, h, p]`` (last axis contiguous), g, beta ``[b, h]``, state
+    ``[nslots, h, p, r]`` updated in place, slots device int32 ``[b]`` or None, y like v."""
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q and k must be [b, hk, r], v [b, h, p] and state [nslots, h, p, r]")
+    d, qkv = _delta_args(q.unsqueeze(1), k.unsqueeze(1) if k.dim() == 3 else k, v.unsqueeze(1), scale)
+    f, n = torch.float32, state.shape[0]
+    if tuple(state.shape[1:]) != (d.nheads, d.headdim, d.dstate):
+        raise ValueError(f"state must be [nslots, {d.nheads}, {d.headdim}, {d.dstate}] (got {list(state.shape)})")
+    if slots is not None and (slots.dtype != torch.int32 or slots.device.type != "cuda"
+                              or not slots.is_contiguous() or slots.numel() != d.batch):
+        raise ValueError(f"slots must be a contiguous device int32 tensor of {d.batch} elements")
+    args = [_ptr(g, "g", f, d.batch * d.nheads, True), _ptr(beta, "beta", f, d.batch * d.nheads, True),
+            _ptr(state, "state", f, state.numel(), True),
+            ctypes.c_void_p(slots.data_ptr()) if slots is not None else None,
+            _ptr(y, "y", q.dtype, v.numel(), True)]
+    return load_library().ssd_delta_step(ctypes.byref(d), n, *qkv, *args, _stream(stream))
+
+
+def ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream=None) -> int:
+    """x, residual, s, y ``[..., width]``, weight fp32 ``[width]``, y8 float8_e4m3fn like x, scale fp32
+    ``[..., width / group]`` (group 0: one per row)."""
+    width = x.shape[-1]
+    n, io = x.numel(), _io_of(x, "x")
+    rows = n // width if width else 0
+    args = [_ptr(x, "x", x.dtype, n, True), _ptr(residual, "residual", x.dtype, n, False),
+            _ptr(weight, "weight", torch.float32, width, True)]
+    groups = width // group if group > 0 else 1
+    outs = [_ptr(s, "s", x.dtype, n, False), _ptr(y, "y", x.dtype, n, False),
+            _ptr(y8, "y8", torch.float8_e4m3fn, n, False),
+            _ptr(scale, "scale", torch.float32, rows * groups, False)]
+    return load_library().ssd_rms_norm(rows, width, io, float(eps), *args, int(group), *outs, _stream(stream))
+
+
+def ssd_rms_norm_workspace_size(rows, width) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load_library().ssd_rms_norm_workspace_size(rows, width, ctypes.byref(n))
+    if rc:
+        raise SsdError(rc, "ssd_rms_norm_workspace_size", ssd_last_error())
+    return int(n.value)
+
+
+def ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream=None) -> int:
+    width = s.shape[-1]
+    n, io = s.numel(), _io_of(s, "s")
+    args = [_ptr(dy, "dy", s.dtype, n, True), _ptr(s, "s", s.dtype, n, True),
+            _ptr(d_s, "d_s", s.dtype, n, False), _ptr(weight, "weight", torch.float32, width, True),
+            _ptr(d_x, "d_x", s.dtype, n, True), _ptr(d_weight, "d_weight", torch.float32, width, True)]
+    wp, wb = _ws(ws)
+    return load_library().ssd_rms_norm_bwd(n // width if width else 0, width, io, float(eps), *args, wp, wb,
+                                           _stream(stream))
+
+
 # ------------------------------------------------------------ allocating helpers
+@contextlib.contextmanager
+def _allocating_on(stream):
+    """Allocate on the stream the work runs on, so that memory freed after the call is reused in
+    that stream's order."""
+    if stream is None:
+        yield
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        yield
+
+
 def _check(rc: int, where: str):
     if rc != 0:
         raise SsdError(rc, where, ssd_last_error())
@@ -567,3 +733,89 @@ def step(x, dt, A, B, C, D, state, in_place=False, stream=None):
     new_state = state if in_place else torch.empty_like(state)
     _check(ssd_step(x, dt, A, B, C, D, state, new_state, y, stream), "ssd_step")
     return y, new_state
+
+
+def _lengths(valid_len):
+    if valid_len is not None and not isinstance(valid_len, torch.Tensor):
+        valid_len = torch.tensor(list(valid_len), dtype=torch.int64)
+    return valid_len
+
+
+def delta_workspace(q, k, v, bwd: bool) -> torch.Tensor:
+    """Workspace of delta_rule (bwd False) or delta_rule_bwd for tensors of these shapes."""
+    n = ssd_delta_workspace_size(_delta_args(q, k, v, None)[0], bwd)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def delta_rule(q, k, v, g, beta, init=None, valid_len=None, scale=None, want_final=True, ws=None,
+               stream=None):
+    """The gated delta rule over a sequence (see ssd_delta_fwd): returns ``(y, final_state)``.
+
+    q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]`` (fp32 or bf16; slices of one projection's output
+    are read in place), log decay g and write strength beta ``[b, s, h]`` fp32, init ``[b, h, p, r]``
+    fp32 or None, valid_len host int64 ``[b]`` (or a list) or None, scale None for ``1 / sqrt(r)``."""
+    with _allocating_on(stream):
+        y = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        final = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), dtype=torch.float32,
+                            device=q.device) if want_final else None
+        ws = delta_workspace(q, k, v, False) if ws is None else ws
+        _check(ssd_delta_fwd(q, k, v, g, beta, init, _lengths(valid_len), y, final, ws, scale, stream),
+               "ssd_delta_fwd")
+    return y, final
+
+
+def delta_rule_bwd(dy, q, k, v, g, beta, init=None, d_final=None, valid_len=None, scale=None,
+                   want_d_init=True, ws=None, stream=None):
+    """Gradients of ``<dy, y> + <d_final, final_state>`` of delta_rule, from its inputs: returns
+    dict(d_q, d_k, d_v, d_g, d_beta, d_init)."""
+    with _allocating_on(stream):
+        new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+        out = dict(d_q=new(q), d_k=new(k), d_v=new(v), d_g=new(g), d_beta=new(beta),
+                   d_init=torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]),
+                                      dtype=torch.float32, device=q.device) if want_d_init else None)
+        ws = delta_workspace(q, k, v, True) if ws is None else ws
+        _check(ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, _lengths(valid_len), out["d_q"],
+                             out["d_k"], out["d_v"], out["d_g"], out["d_beta"], out["d_init"], ws, scale,
+                             stream), "ssd_delta_bwd")
+    return out
+
+
+def delta_step(q, k, v, g, beta, state, slots=None, scale=None, stream=None):
+    """One token of the gated delta rule from cached states (see ssd_delta_step): q, k ``[b, hk, r]``,
+    v ``[b, h, p]``, g, beta ``[b, h]``; state ``[nslots, h, p, r]`` is updated in place; slots (device
+    int32 ``[b]``) names each row's slot, negative for an idle row.  Returns y ``[b, h, p]``."""
+    with _allocating_on(stream):
+        y = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        _check(ssd_delta_step(q, k, v, g, beta, state, slots, y, scale, stream), "ssd_delta_step")
+    return y
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, out8=False, group=0, want_y=None, stream=None):
+    """Root-mean-square norm of x ``[..., width]`` (see ssd_rms_norm).  Returns a dict of: ``s`` = x +
+    residual (with a residual), ``y`` (by default where out8 is false), and with out8 ``y8``
+    (float8_e4m3fn) and ``scale`` (fp32 ``[..., width / group]``, group 0: one per row) with
+    y = y8 * scale."""
+    want_y = not out8 if want_y is None else want_y
+    width = x.shape[-1]
+    with _allocating_on(stream):
+        s = torch.empty_like(x) if residual is not None else None
+        y = torch.empty_like(x) if want_y else None
+        y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if out8 else None
+        groups = width // group if group > 0 else 1
+        scale = torch.empty((*x.shape[:-1], groups), device=x.device) if out8 else None
+        _check(ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream), "ssd_rms_norm")
+    return {k: t for k, t in (("s", s), ("y", y), ("y8", y8), ("scale", scale)) if t is not None}
+
+
+def rms_norm_bwd(dy, s, weight, eps=1e-6, d_s=None, ws=None, stream=None):
+    """Gradient of ``<dy, y> + <d_s, s>`` of rms_norm at its s (x without a residual): returns
+    ``(d_x, d_weight)``; d_x is the gradient of x and of the residual alike."""
+    width = s.shape[-1]
+    with _allocating_on(stream):
+        d_x = torch.empty_like(s)
+        d_weight = torch.empty_like(weight)
+        if ws is None:
+            n = ssd_rms_norm_workspace_size(s.numel() // width if width else 0, width)
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=s.device)
+        _check(ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream), "ssd_rms_norm_bwd")
+    return d_x, d_weight
