@@ -335,8 +335,7 @@ int ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int
  * axis contiguous, so they may be slices of one projection's output.
  *   batch >= 0, seq >= 0 (an empty sequence: final = init, d_init = d_final); nheads a multiple of
  *   kheads; headdim and dstate in {16, 32, 64, 128}; any seq.
- *   q, k 16-byte aligned with strides of whole 16 bytes; y, dy and the gradients of io dtype
- *   16-byte (8-byte for bf16) aligned; states 16-byte aligned.
+ *   q, k, v, y, dy, d_q, d_k, d_v and the states 16-byte aligned; strides of whole 16 bytes.
  *   valid_len    [b]  HOST int64, nullable (NULL = all of seq), each in [0, seq]: tokens at or past
  *   it are not read, leave the state alone, and give y and gradients of exactly zero.
  * bf16 io: the products take the bf16 inputs as they are and everything else (states, decays, the

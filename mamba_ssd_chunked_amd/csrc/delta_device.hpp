@@ -22,7 +22,11 @@ namespace ssd {
 constexpr int DL = 64;         // tokens per chunk of the delta rule
 constexpr int DTRI = 6;        // 16 x 32 operand tiles of a triangular 64 x 64 matrix
 constexpr int DTILE = 64 * 8;  // bf16 values of one operand tile (8 per lane)
-constexpr int DCOEF = 5 * DL;  // floats of a chunk's coefficients: e^G, e^{G_L - G}, beta, G in base 2 (fp64)
+
+// Floats of a chunk's coefficients: e^G (zero past the row's length), e^{G_L - G}, beta, and
+// e^{G_L} in the first of the next 64; then G in base 2 (fp64).
+constexpr int DCF = 4 * DL;
+constexpr int DCOEF = DCF + 2 * DL;
 
 // Buffers of the scans, typed.
 template <class T>
@@ -33,7 +37,7 @@ struct DeltaScan {
     const float *init, *d_final;
     float *final_state, *d_init;
     float* coef;
-    uint16_t *M, *P, *NT;
+    uint16_t *M, *P, *NT, *Kp, *Qp;
     float *H, *E, *dH, *dZ;
 };
 
@@ -70,6 +74,33 @@ __device__ __forceinline__ Parts<N> split44(v4f a, v4f b) {
     return split8<N>(x);
 }
 
+// The same for T results at once, the MFMAs of one result T apart: a dependent MFMA waits for
+// its accumulator.
+template <int NA, int NB, int T>
+__device__ __forceinline__ void mma_a(v4f (&c)[T], const Parts<NA> (&a)[T], const Parts<NB>& b) {
+    constexpr int K = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int s = K; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t].p[i], b.p[s - i], c[t], 0, 0, 0);
+}
+template <int NA, int NB, int T>
+__device__ __forceinline__ void mma_b(v4f (&c)[T], const Parts<NA>& a, const Parts<NB> (&b)[T]) {
+    constexpr int K = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int s = K; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b[t].p[s - i], c[t], 0, 0, 0);
+}
+
 template <int NA, int NB>
 __device__ __forceinline__ v4f mma(const Parts<NA>& a, const Parts<NB>& b, v4f c) {
     constexpr int K = (NA > NB ? NA : NB) - 1;
@@ -104,6 +135,32 @@ __device__ __forceinline__ b8v join8(s4 a, s4 b) {
     typedef short s8 __attribute__((ext_vector_type(8)));
     return __builtin_bit_cast(b8v, s8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 }
+
+// 16 bytes per lane from global memory straight into LDS at lds + 16 lane (a byte address, the
+// same in all lanes).  It counts in vmcnt; the reader waits and passes a barrier
+// (wait_barrier).  Written out because around the builtin the compiler waits for every such
+// load before any LDS read, of whatever array.
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)p));
+}
+__device__ __forceinline__ void load_to_lds(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                 "v"(src)
+                 : "memory", "m0");
+}
+// Wait until at most N of this wave's memory operations are outstanding (they end in order) and
+// its LDS reads have returned, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N < 63 ? N : 63) : "memory");
+}
+
+// LDS order of a 64-token matrix [64, r] of bf16: 16 x 32 tiles (token tile tau, step j), each
+// a kilobyte: the eight values r = 32 j + 8 g .. of token 16 tau + i at 16-byte slot
+// 16 g + (i ^ 4 g).  A tile is then one lane-linear operand read (rows), and the four rows x four
+// column groups that a transposing read (columns) addresses lie in sixteen different slots mod 16.
+__device__ __forceinline__ constexpr int tile_slot(int i, int g) { return 16 * g + (i ^ (4 * g)); }
 
 // Operand tile numbers of a lower (upper) triangular 64 x 64 matrix in row tiles tau of 16
 // and k steps j of 32: the six tiles that are not zero.

@@ -28,6 +28,11 @@ namespace {
 
 constexpr int CS = DL + 4;  // LDS row stride of a 64 x 64 fp32 matrix
 
+// Whether the scans read q and k as bf16 parts that the preparation wrote (fp32 io, or rows
+// shorter than an operand) rather than from the caller's tensors.
+template <class IO, int R>
+__host__ __device__ constexpr bool stage_parts() { return in_parts<IO>() == 3 || R < 32; }
+
 // Below this a log decay counts as this: exp() of either is zero in fp32, and differences of
 // cumulative sums stay finite where g is -inf (a state that is forgotten at once).
 constexpr float kMinLogDecay = -1.0e4f;
@@ -108,7 +113,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
                                                     const float* __restrict__ beta,
                                                     const int64_t* __restrict__ len,
                                                     float* __restrict__ coef, uint16_t* __restrict__ Mo,
-                                                    uint16_t* __restrict__ Po, uint16_t* __restrict__ No) {
+                                                    uint16_t* __restrict__ Po, uint16_t* __restrict__ No,
+                                                    uint16_t* __restrict__ Kp, uint16_t* __restrict__ Qp) {
     constexpr int NP = in_parts<IO>(), KJ = R < 32 ? 1 : R / 32;
     constexpr int NY = BWD ? 3 : (NP == 1 ? 2 : 3);
     __shared__ double sG[DL];
@@ -138,10 +144,11 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
         sG[lane] = G2;
         sBeta[lane] = bv;
         float* cf = coef + ch * DCOEF;
-        cf[lane] = exp2_of(G2);
+        cf[lane] = lane < L ? exp2_of(G2) : 0.0f;
         cf[DL + lane] = exp2_of(tot - G2);
         cf[2 * DL + lane] = bv;
-        reinterpret_cast<double*>(cf + 3 * DL)[lane] = G2;
+        if (lane == 0) cf[3 * DL] = exp2_of(tot);
+        reinterpret_cast<double*>(cf + DCF)[lane] = G2;
     }
     const int hk = h / (d.H / d.HK);
     const typename IO::T* kb = k + b * d.ks[0] + t0 * d.ks[1] + hk * d.ks[2];
@@ -159,6 +166,17 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
     for (int j = 0; j < KJ; ++j) {
         const auto kw = row(kb, d.ks[1], w, j);
         const auto qw = row(qb, d.qs[1], w, j);
+        if constexpr (stage_parts<IO, R>()) {
+            if (h == hk * (d.H / d.HK)) {  // one value head writes the parts of its key head
+                const int64_t at = ((static_cast<int64_t>(b) * d.HK + hk) * d.N + c) * (NP * 4 * KJ * DTILE) +
+                                   (w * KJ + j) * DTILE + tile_slot(i, g) * 8;
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    *reinterpret_cast<b8v*>(Kp + at + n * (4 * KJ * DTILE)) = kw.p[n];
+                    *reinterpret_cast<b8v*>(Qp + at + n * (4 * KJ * DTILE)) = qw.p[n];
+                }
+            }
+        }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             if (s <= w) {
@@ -266,333 +284,427 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
 
 namespace {
 
-// Shared memory of one scan workgroup.
-template <class IO, int R, int NQ>
-struct ScanLds {
-    static constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, LD = RP + 8;
-    uint16_t K[NP][DL * LD];
-    uint16_t Q[NQ ? NP : 1][NQ ? DL * LD : 8];
-    uint16_t M[3][DTRI * DTILE];
-    uint16_t P[NQ ? NQ : 1][NQ ? DTRI * DTILE : 8];
-    float cf[3 * DL];  // e^G, e^{G_L - G}, beta
-};
+enum ScanMode { kOutputs, kRecord, kReverse };
 
-// Rows [0, L) of a chunk's keys or queries as bf16 parts, zeros elsewhere.
-template <class IO, int R, int NTHR>
-__device__ __forceinline__ void stage_parts(uint16_t* dst, int part_stride, const typename IO::T* src,
-                                            int64_t stride, int L) {
-    constexpr int RP = R < 32 ? 32 : R, V = RP / 8;
-#pragma unroll 4
-    for (int idx = threadIdx.x; idx < DL * V; idx += NTHR) {
-        const int t = idx / V, col = 8 * (idx % V);
-        const auto p = load_parts8<IO>(src + t * stride + col, t < L && col < R);
-#pragma unroll
-        for (int n = 0; n < in_parts<IO>(); ++n)
-            *reinterpret_cast<b8v*>(dst + n * part_stride + t * (RP + 8) + col) = p.p[n];
+// One scan workgroup: W waves, each 16 value columns of one head.  What a chunk needs is loaded
+// into LDS without passing registers, a chunk ahead, into the buffer that its predecessor has
+// just left: the phases of a chunk are ordered so that between the last read of a buffer and
+// the first read of its next contents lies another phase's matrix work.
+template <class IO, int R, int W, ScanMode MODE>
+struct Scan {
+    using T = typename IO::T;
+    static constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, KJ = RP / 32, RT = RP / 16;
+    static constexpr bool PARTS = stage_parts<IO, R>();
+    // parts of y's operands: an output rounded to bf16 needs no third part (2^-17 of it)
+    static constexpr int NQ = MODE == kOutputs && NP == 1 ? 2 : 3;
+    static constexpr int QT = 4 * KJ;  // tiles per part
+    // LDS, bytes
+    static constexpr int KBYTES = NP * QT * 1024, KBUFS = MODE == kRecord ? 2 : 1;
+    static constexpr int QBYTES = MODE == kRecord ? 0 : KBYTES;
+    static constexpr int MBYTES = 3 * DTRI * 1024, PBYTES = MODE == kRecord ? 0 : NQ * DTRI * 1024;
+    static constexpr int VBYTES = DL * 16 * W * sizeof(T);
+    static constexpr int oK = 0, oQ = oK + KBUFS * KBYTES, oM = oQ + QBYTES, oP = oM + MBYTES, oV = oP + PBYTES,
+                         oC = oV + VBYTES, LDS = oC + 2 * 4 * DCF;
+    // loads and stores per wave
+    static constexpr int nK = (NP * QT + W - 1) / W, nQ = nK, nM = (3 * DTRI + W - 1) / W,
+                         nP = (NQ * DTRI + W - 1) / W, nV = VBYTES / (1024 * W), nC = 1, nY = 4;
+    static constexpr int nState = RT * 4, nRows = 16;
+
+    char* sm;
+    const DeltaShape& d;
+    const DeltaScan<T>& a;
+    int lane, w, i, g, p0, pw, h, b, hk, chunks, len;
+    int64_t bh;
+
+    __device__ Scan(char* smem, const DeltaShape& dd, const DeltaScan<T>& aa, int64_t blk) : sm(smem), d(dd), a(aa) {
+        lane = threadIdx.x & 63;
+        w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        i = lane & 15;
+        g = lane >> 4;
+        const int pbs = d.P / (16 * W);
+        pw = static_cast<int>(blk % pbs) * 16 * W;  // the workgroup's first column
+        p0 = pw + 16 * w;                           // the wave's
+        bh = blk / pbs;
+        h = static_cast<int>(bh % d.H);
+        b = static_cast<int>(bh / d.H);
+        hk = h / (d.H / d.HK);
+        len = a.len ? static_cast<int>(a.len[b]) : d.S;
+        chunks = (len + DL - 1) / DL;
     }
-}
-template <int N16, int NTHR>
-__device__ __forceinline__ void stage_copy(uint16_t* dst, const uint16_t* src) {
-#pragma unroll 4
-    for (int idx = threadIdx.x; idx < N16 / 8; idx += NTHR)
-        reinterpret_cast<uint4*>(dst)[idx] = reinterpret_cast<const uint4*>(src)[idx];
-}
 
-// A operand: rows t = 16 tau + i of a staged matrix, k = 32 j + 8 g ...
-template <int NP, int LD>
-__device__ __forceinline__ Parts<NP> row_op(const uint16_t (*m)[DL * LD], int tau, int j, int i, int g) {
-    Parts<NP> o;
+    // -------------------------------------------------------------- loads into LDS
+    template <int N>  // N kilobytes, as they are
+    __device__ void copy_tiles(int at, const uint16_t* src) const {
+        const uint32_t dst = lds_addr(sm) + at;
 #pragma unroll
-    for (int n = 0; n < NP; ++n)
-        o.p[n] = *reinterpret_cast<const b8v*>(&m[n][(16 * tau + i) * LD + 32 * j + 8 * g]);
-    return o;
-}
-// A operand: the transposed matrix, rows r = 32 (tau / 2) + 8 (i / 4) + 4 (tau % 2) + i % 4 and
-// k over the tokens 32 j + {4 g + v, 16 + 4 g + v}: result row 4 g + v of state tile tau is
-// then r = 32 (tau / 2) + 8 g + 4 (tau % 2) + v, so that two state tiles hold eight
-// consecutive r per lane.
-template <int NP, int LD>
-__device__ __forceinline__ Parts<NP> col_op(const uint16_t (*m)[DL * LD], int tau, int j, int i, int g) {
-    Parts<NP> o;
-    const int at = (32 * j + 4 * g + (i >> 2)) * LD + 32 * (tau >> 1) + 8 * (i & 3) + 4 * (tau & 1);
-#pragma unroll
-    for (int n = 0; n < NP; ++n) o.p[n] = join8(lds_col4(&m[n][at]), lds_col4(&m[n][at + 16 * LD]));
-    return o;
-}
-template <int N>
-__device__ __forceinline__ Parts<N> tri_op(const uint16_t (*m)[DTRI * DTILE], int tile, int lane) {
-    Parts<N> o;
-#pragma unroll
-    for (int n = 0; n < N; ++n) o.p[n] = *reinterpret_cast<const b8v*>(&m[n][tile * DTILE + lane * 8]);
-    return o;
-}
-
-template <class IO>
-__device__ __forceinline__ float load_or0(const typename IO::T* p, bool on) {
-    return on ? io<IO>::ld(p, 0) : 0.0f;
-}
-
-// State tiles of one wave (16 value rows p, lane i; all r) from / to [p, r] rows.
-template <int R, int RT>
-__device__ __forceinline__ void load_state(v4f (&s)[RT], const float* src, int i, int g) {
-#pragma unroll
-    for (int tau = 0; tau < RT; ++tau) {
-        const int r = 32 * (tau >> 1) + 8 * g + 4 * (tau & 1);
-        s[tau] = src && r < R ? *reinterpret_cast<const v4f*>(src + i * R + r) : zero4();
-    }
-}
-template <int R, int RT>
-__device__ __forceinline__ void store_state(const v4f (&s)[RT], float* dst, int i, int g) {
-#pragma unroll
-    for (int tau = 0; tau < RT; ++tau) {
-        const int r = 32 * (tau >> 1) + 8 * g + 4 * (tau & 1);
-        if (r < R) *reinterpret_cast<v4f*>(dst + i * R + r) = s[tau];
-    }
-}
-// ... and to the [r, P] rows that the gradient kernel reads (dst at the wave's first p).
-template <int R, int RT>
-__device__ __forceinline__ void store_state_t(const v4f (&s)[RT], float* dst, int P, int i, int g) {
-#pragma unroll
-    for (int tau = 0; tau < RT; ++tau) {
-        const int r = 32 * (tau >> 1) + 8 * g + 4 * (tau & 1);
-        if (r < R) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) dst[(r + v) * P + i] = s[tau][v];
+        for (int m = 0; m < (N + W - 1) / W; ++m) {
+            const int t = N % W == 0 || w + m * W < N ? w + m * W : N - 1;  // every wave loads as often
+            load_to_lds(src + t * DTILE + lane * 8, dst + t * 1024);
         }
     }
-}
-
-// The forward recurrence of one workgroup: W waves, each 16 value rows.  NQ > 0: the outputs,
-// with y's intra-chunk operands in NQ parts; NQ = 0: the entry states and E for the backward.
-template <class IO, int R, int W, int NQ>
-__device__ void scan_fwd(ScanLds<IO, R, NQ>& sm, const DeltaShape& d, const DeltaScan<typename IO::T>& a,
-                         int64_t blk) {
-    using LDS = ScanLds<IO, R, NQ>;
-    constexpr int NP = LDS::NP, RP = LDS::RP, LD = LDS::LD, KJ = RP / 32, RT = RP / 16, NTHR = 64 * W;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-    const int pbs = d.P / (16 * W);
-    const int p0 = static_cast<int>(blk % pbs) * 16 * W + 16 * w;
-    const int64_t bh = blk / pbs;
-    const int h = static_cast<int>(bh % d.H), b = static_cast<int>(bh / d.H);
-    const int hk = h / (d.H / d.HK);
-    const int64_t state_at = (bh * d.P + p0) * R;
-    v4f s[RT];
-    load_state<R>(s, a.init ? a.init + state_at : nullptr, i, g);
-    int c = 0;
-    for (; c < d.N; ++c) {
-        const int L = chunk_tokens(a.len, b, d.S, c);
-        if (L == 0) break;
-        const int64_t ch = bh * d.N + c, t0 = static_cast<int64_t>(c) * DL;
-        __syncthreads();
-        stage_parts<IO, R, NTHR>(sm.K[0], DL * LD, a.k + b * d.ks[0] + t0 * d.ks[1] + hk * d.ks[2], d.ks[1], L);
-        stage_copy<3 * DTRI * DTILE, NTHR>(sm.M[0], a.M + ch * (3 * DTRI * DTILE));
-        if constexpr (NQ > 0) {
-            stage_parts<IO, R, NTHR>(sm.Q[0], DL * LD, a.q + b * d.qs[0] + t0 * d.qs[1] + hk * d.qs[2], d.qs[1], L);
-            stage_copy<NQ * DTRI * DTILE, NTHR>(sm.P[0], a.P + ch * (NQ * DTRI * DTILE));
-        }
-        for (int idx = threadIdx.x; idx < 3 * DL; idx += NTHR) sm.cf[idx] = a.coef[ch * DCOEF + idx];
-        __syncthreads();
-        v4f x[4], y[4];
+    // Tokens of chunk c of q or k.  Rows past the length repeat its last row: what they feed is
+    // multiplied by the zeros of beta and e^G there.
+    __device__ void load_qk(int at, const T* x, const uint16_t* parts, const int64_t (&stride)[3], int c) const {
+        if constexpr (PARTS) {
+            copy_tiles<NP * QT>(at, parts + ((static_cast<int64_t>(b) * d.HK + hk) * d.N + c) * (NP * QT * DTILE));
+        } else {
+            const int gs = lane >> 4, is = (lane & 15) ^ (4 * gs);
+            const int last = (len - c * DL < DL ? len - c * DL : DL) - 1;
+            const T* base = x + b * stride[0] + static_cast<int64_t>(c) * DL * stride[1] + hk * stride[2] + 8 * gs;
+            const uint32_t dst = lds_addr(sm) + at;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) x[t] = y[t] = zero4();
-#pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-            const auto sp = split44<3>(s[2 * j], s[2 * j + 1]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) x[t] = mma(row_op<NP, LD>(sm.K, t, j, i, g), sp, x[t]);
-            if constexpr (NQ > 0) {
-                Parts<NQ> sy;
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) sy.p[n] = sp.p[n];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) y[t] = mma(sy, row_op<NP, LD>(sm.Q, t, j, i, g), y[t]);
+            for (int m = 0; m < nK; ++m) {
+                const int t = QT % W == 0 || w + m * W < QT ? w + m * W : QT - 1;
+                const int row = 16 * (t / KJ) + is;
+                load_to_lds(base + (row < last ? row : last) * stride[1] + 32 * (t % KJ), dst + t * 1024);
             }
         }
-        // R = V - e^G X, E = M R, U = beta E (lane: value row p0 + i, tokens 16 tau + 4 g + v)
-        v4f rr[4], u[4];
-        const typename IO::T* vb = a.v + b * d.vs[0] + t0 * d.vs[1] + h * d.vs[2] + p0 + i;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const v4f eg = *reinterpret_cast<const v4f*>(&sm.cf[16 * t + 4 * g]);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int tok = 16 * t + 4 * g + v;
-                rr[t][v] = load_or0<IO>(vb + tok * d.vs[1], tok < L) - eg[v] * x[t][v];
-            }
-            u[t] = zero4();
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const auto rp = split44<3>(rr[2 * j], rr[2 * j + 1]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (j <= t / 2) u[t] = mma(tri_op<3>(sm.M, tri_lower(t, j), lane), rp, u[t]);
-        }
-        if constexpr (NQ == 0) {
-            store_state_t<R>(s, a.H + ch * (R * d.P) + p0, d.P, i, g);
-            float* eo = a.E + ch * (DL * d.P) + p0 + i;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) eo[(16 * t + 4 * g + v) * d.P] = u[t][v];
-        }
-        v4f ut[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            u[t] *= *reinterpret_cast<const v4f*>(&sm.cf[2 * DL + 16 * t + 4 * g]);
-            ut[t] = u[t] * *reinterpret_cast<const v4f*>(&sm.cf[DL + 16 * t + 4 * g]);
-        }
-        const float eL = sm.cf[DL - 1];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) s[t] *= eL;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const auto up = split44<3>(ut[2 * j], ut[2 * j + 1]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) s[t] = mma(col_op<NP, LD>(sm.K, t, j, i, g), up, s[t]);
-        }
-        if constexpr (NQ > 0) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) y[t] *= d.scale * sm.cf[16 * t + i];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const auto up = split44<NQ>(u[2 * j], u[2 * j + 1]);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (j <= t / 2) y[t] = mma(up, tri_op<NQ>(sm.P, tri_lower(t, j), lane), y[t]);
-            }
-            // y holds D[p][t]: lane token 16 tau + i, value rows 4 g + v
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int64_t tok = t0 + 16 * t + i;
-                if (tok < d.S) io<IO>::st4(a.y, ((b * static_cast<int64_t>(d.S) + tok) * d.H + h) * d.P + p0 + 4 * g, y[t]);
-            }
-        }
-        mfma_settle();
     }
-    if (a.final_state) store_state<R>(s, a.final_state + state_at, i, g);
-    if constexpr (NQ > 0) {  // chunks past the row's length
-        for (int64_t tok = static_cast<int64_t>(c) * DL + i; tok < d.S; tok += 16)
-            io<IO>::st4(a.y, ((b * static_cast<int64_t>(d.S) + tok) * d.H + h) * d.P + p0 + 4 * g, zero4());
+    // Tokens of chunk c of v or dy, the workgroup's columns, row-major.
+    __device__ void load_v(const T* x, int64_t sb, int64_t st, int64_t sh, int c) const {
+        constexpr int U = 16 * W * sizeof(T) / 16;  // 16-byte units of a row
+        const int last = (len - c * DL < DL ? len - c * DL : DL) - 1;
+        const T* base = x + b * sb + static_cast<int64_t>(c) * DL * st + h * sh + pw;
+#pragma unroll
+        for (int m = 0; m < nV; ++m) {
+            const int u = (m * W + w) * 64 + lane, row = u / U;
+            load_to_lds(base + (row < last ? row : last) * st + (u % U) * (16 / static_cast<int>(sizeof(T))),
+                        lds_addr(sm) + oV + (m * W + w) * 1024);
+        }
     }
-}
+    __device__ void load_coef(int c, int buf) const {
+        load_to_lds(a.coef + (bh * d.N + c) * DCOEF + 4 * lane, lds_addr(sm) + oC + (buf & 1) * 4 * DCF);
+    }
 
-// The reverse recurrence: writes the gradient of the state leaving each chunk and dZ.
-template <class IO, int R, int W>
-__device__ void scan_rev(ScanLds<IO, R, 3>& sm, const DeltaShape& d, const DeltaScan<typename IO::T>& a,
-                         int64_t blk) {
-    using LDS = ScanLds<IO, R, 3>;
-    constexpr int NP = LDS::NP, RP = LDS::RP, LD = LDS::LD, KJ = RP / 32, RT = RP / 16, NTHR = 64 * W;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-    const int pbs = d.P / (16 * W);
-    const int p0 = static_cast<int>(blk % pbs) * 16 * W + 16 * w;
-    const int64_t bh = blk / pbs;
-    const int h = static_cast<int>(bh % d.H), b = static_cast<int>(bh / d.H);
-    const int hk = h / (d.H / d.HK);
-    const int64_t state_at = (bh * d.P + p0) * R;
-    v4f s[RT];
-    load_state<R>(s, a.d_final ? a.d_final + state_at : nullptr, i, g);
-    for (int c = d.N - 1; c >= 0; --c) {
-        const int L = chunk_tokens(a.len, b, d.S, c);
-        if (L == 0) continue;
-        const int64_t ch = bh * d.N + c, t0 = static_cast<int64_t>(c) * DL;
-        __syncthreads();
-        stage_parts<IO, R, NTHR>(sm.K[0], DL * LD, a.k + b * d.ks[0] + t0 * d.ks[1] + hk * d.ks[2], d.ks[1], L);
-        stage_parts<IO, R, NTHR>(sm.Q[0], DL * LD, a.q + b * d.qs[0] + t0 * d.qs[1] + hk * d.qs[2], d.qs[1], L);
-        stage_copy<3 * DTRI * DTILE, NTHR>(sm.M[0], a.NT + ch * (3 * DTRI * DTILE));
-        stage_copy<3 * DTRI * DTILE, NTHR>(sm.P[0], a.P + ch * (3 * DTRI * DTILE));
-        for (int idx = threadIdx.x; idx < 3 * DL; idx += NTHR) sm.cf[idx] = a.coef[ch * DCOEF + idx];
-        store_state_t<R>(s, a.dH + ch * (R * d.P) + p0, d.P, i, g);
-        __syncthreads();
-        v4f x[4], dy[4];
-        const typename IO::T* yb = a.dy + ((b * static_cast<int64_t>(d.S) + t0) * d.H + h) * d.P + p0 + i;
+    // -------------------------------------------------------------- operands
+    __device__ Parts<NP> row_op(int base, int tau, int j) const {  // rows: tokens 16 tau + i
+        Parts<NP> o;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            x[t] = zero4();
+        for (int n = 0; n < NP; ++n)
+            o.p[n] = *reinterpret_cast<const b8v*>(sm + base + (n * QT + tau * KJ + j) * 1024 + tile_slot(i, g) * 16);
+        return o;
+    }
+    // Rows r = 32 (rho / 2) + 8 (i / 4) + 4 (rho % 2) + i % 4 of the transposed matrix, k over the
+    // tokens 32 j + {4 g + v, 16 + 4 g + v}.  Row 4 g + v of state tile rho is then
+    // r = 32 (rho / 2) + 8 g + 4 (rho % 2) + v: two state tiles hold eight consecutive r per lane.
+    __device__ Parts<NP> col_op(int base, int rho, int j) const {
+        Parts<NP> o;
+        const int at = base + (2 * j * KJ + (rho >> 1)) * 1024 + tile_slot(4 * g + (i >> 2), i & 3) * 16 + (rho & 1) * 8;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int tok = 16 * t + 4 * g + v;
-                dy[t][v] = load_or0<IO>(yb + static_cast<int64_t>(tok) * d.H * d.P, tok < L);
+        for (int n = 0; n < NP; ++n)
+            o.p[n] = join8(lds_col4(reinterpret_cast<const uint16_t*>(sm + at + n * QT * 1024)),
+                           lds_col4(reinterpret_cast<const uint16_t*>(sm + at + (n * QT + KJ) * 1024)));
+        return o;
+    }
+    template <int N>
+    __device__ Parts<N> tri_op(int base, int tile) const {
+        Parts<N> o;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            o.p[n] = *reinterpret_cast<const b8v*>(sm + base + (n * DTRI + tile) * 1024 + lane * 16);
+        return o;
+    }
+    // v or dy in result layout: tokens 16 t + 4 g + v of value column p0 + i
+    __device__ v4f value(int t) const {
+        if constexpr (sizeof(T) == 2) {
+            const s4 x = lds_col4(reinterpret_cast<const uint16_t*>(sm + oV) + (16 * t + 4 * g + (i >> 2)) * (16 * W) +
+                                  16 * w + 4 * (i & 3));
+            return v4f{bf16_to_f32(x[0]), bf16_to_f32(x[1]), bf16_to_f32(x[2]), bf16_to_f32(x[3])};
+        } else {
+            const float* x = reinterpret_cast<const float*>(sm + oV) + (16 * t + 4 * g) * (16 * W) + 16 * w + i;
+            return v4f{x[0], x[16 * W], x[32 * W], x[48 * W]};
+        }
+    }
+    __device__ const float* coef(int c) const { return reinterpret_cast<const float*>(sm + oC + (c & 1) * 4 * DCF); }
+    __device__ static v4f at4(const float* p) { return *reinterpret_cast<const v4f*>(p); }
+
+    // -------------------------------------------------------------- states
+    __device__ void load_state(v4f (&s)[RT], const float* src) const {
+#pragma unroll
+        for (int rho = 0; rho < RT; ++rho) {
+            const int r = 32 * (rho >> 1) + 8 * g + 4 * (rho & 1);
+            s[rho] = src && r < R ? at4(src + (bh * d.P + p0 + i) * R + r) : zero4();
+        }
+    }
+    __device__ void store_state(const v4f (&s)[RT], float* dst) const {
+#pragma unroll
+        for (int rho = 0; rho < RT; ++rho) {
+            const int r = 32 * (rho >> 1) + 8 * g + 4 * (rho & 1);
+            if (dst && r < R) *reinterpret_cast<v4f*>(dst + (bh * d.P + p0 + i) * R + r) = s[rho];
+        }
+    }
+    // A chunk's state for the gradient kernel, [r, P] rows.
+    __device__ void record_state(const v4f (&s)[RT], float* dst, int c) const {
+        float* o = dst + (bh * d.N + c) * (static_cast<int64_t>(R) * d.P) + p0 + i;
+#pragma unroll
+        for (int rho = 0; rho < RT; ++rho) {
+            const int r = 32 * (rho >> 1) + 8 * g + 4 * (rho & 1);
+            if (r < R) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) o[(r + v) * d.P] = s[rho][v];
             }
         }
+    }
+    __device__ void record_rows(const v4f (&x)[4], float* dst, int c) const {
+        float* o = dst + (bh * d.N + c) * (static_cast<int64_t>(DL) * d.P) + p0 + i;
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-            const auto sp = split44<3>(s[2 * j], s[2 * j + 1]);
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) x[t] = mma(row_op<NP, LD>(sm.K, t, j, i, g), sp, x[t]);
-        }
-        v4f z[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            x[t] *= *reinterpret_cast<const v4f*>(&sm.cf[DL + 16 * t + 4 * g]);
-            z[t] = zero4();
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const auto yp = split44<NP>(dy[2 * j], dy[2 * j + 1]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (j >= t / 2) x[t] = mma(tri_op<3>(sm.P, tri_upper(t, j), lane), yp, x[t]);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const auto up = split44<3>(x[2 * j], x[2 * j + 1]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (j >= t / 2) z[t] = mma(tri_op<3>(sm.M, tri_upper(t, j), lane), up, z[t]);
-        }
-        float* zo = a.dZ + ch * (DL * d.P) + p0 + i;
-        const float eL = sm.cf[DL - 1];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const v4f eg = *reinterpret_cast<const v4f*>(&sm.cf[16 * t + 4 * g]);
-            const v4f be = *reinterpret_cast<const v4f*>(&sm.cf[2 * DL + 16 * t + 4 * g]);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                zo[(16 * t + 4 * g + v) * d.P] = z[t][v];
-                z[t][v] *= -eg[v] * be[v];
-                dy[t][v] *= d.scale * eg[v];
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < RT; ++t) s[t] *= eL;
+            for (int v = 0; v < 4; ++v) o[(16 * t + 4 * g + v) * d.P] = x[t][v];
+    }
+    // s <- s + X^T z over the chunk's tokens, X = k or q in LDS, z in result layout
+    __device__ void add_outer(v4f (&s)[RT], int base, const v4f (&z)[4]) const {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const auto zp = split44<3>(z[2 * j], z[2 * j + 1]);
-            const auto yp = split44<3>(dy[2 * j], dy[2 * j + 1]);
+            constexpr int G = RT < 4 ? RT : 4;
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                s[t] = mma(col_op<NP, LD>(sm.K, t, j, i, g), zp, s[t]);
-                s[t] = mma(col_op<NP, LD>(sm.Q, t, j, i, g), yp, s[t]);
+            for (int r0 = 0; r0 < RT; r0 += G) {
+                Parts<NP> op[G];
+#pragma unroll
+                for (int m = 0; m < G; ++m) op[m] = col_op(base, r0 + m, j);
+                mma_a(*reinterpret_cast<v4f(*)[G]>(&s[r0]), op, zp);
             }
         }
-        mfma_settle();
     }
-    if (a.d_init) store_state<R>(s, a.d_init + state_at, i, g);
+    // c <- c + A x for a triangular operand in LDS
+    template <bool LOWER, int N, int NB>
+    __device__ void tri_mul(v4f (&c)[4], int base, int j, const Parts<NB>& x) const {
+        constexpr int all = 4;
+        if (LOWER == (j == 0)) {
+            Parts<N> op[all];
+#pragma unroll
+            for (int t = 0; t < all; ++t) op[t] = tri_op<N>(base, LOWER ? tri_lower(t, j) : tri_upper(t, j));
+            mma_a(c, op, x);
+        } else {
+            constexpr int t0 = LOWER ? 2 : 0;
+            Parts<N> op[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) op[t] = tri_op<N>(base, LOWER ? tri_lower(t0 + t, j) : tri_upper(t0 + t, j));
+            mma_a(*reinterpret_cast<v4f(*)[2]>(&c[t0]), op, x);
+        }
+    }
+
+    // -------------------------------------------------------------- the forward recurrence
+    __device__ void store_y(const v4f (&y)[4], int c) const {  // D[p][t]: token 16 t + i, columns 4 g + v
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t tok = static_cast<int64_t>(c) * DL + 16 * t + i;
+            if (tok < d.S) io<IO>::st4(a.y, ((b * static_cast<int64_t>(d.S) + tok) * d.H + h) * d.P + p0 + 4 * g, y[t]);
+        }
+    }
+
+    __device__ void forward() const {
+        v4f s[RT];
+        load_state(s, a.init);
+        int c = 0;
+        if (chunks > 0) {
+            if constexpr (MODE == kOutputs) load_qk(oQ, a.q, a.Qp, d.qs, 0);
+            load_coef(0, 0);
+            copy_tiles<3 * DTRI>(oM, a.M + bh * d.N * (3 * DTRI * DTILE));
+            load_v(a.v, d.vs[0], d.vs[1], d.vs[2], 0);
+            load_qk(oK, a.k, a.Kp, d.ks, 0);
+            wait_barrier<0>();
+        }
+        for (; c < chunks; ++c) {
+            const int64_t ch = bh * d.N + c;
+            const int nx = c + 1 < chunks ? c + 1 : c;  // the last chunk loads itself again
+            const int kb = oK + (MODE == kRecord ? (c & 1) * KBYTES : 0);
+            v4f x[4], y[4], u[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) x[t] = y[t] = u[t] = zero4();
+            Parts<3> sp[KJ];
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) sp[j] = split44<3>(s[2 * j], s[2 * j + 1]);
+            if constexpr (MODE == kOutputs) {
+                wait_barrier<nM + nV + nK + nY>();  // q and the coefficients are here, P is free
+                copy_tiles<NQ * DTRI>(oP, a.P + ch * (NQ * DTRI * DTILE));
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) {
+                    Parts<NP> op[4];
+                    Parts<NQ> sy;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) sy.p[n] = sp[j].p[n];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) op[t] = row_op(oQ, t, j);
+                    mma_b(y, sy, op);
+                }
+                wait_barrier<nY + nP>();  // M, v and k are here, q is free
+                load_qk(oQ, a.q, a.Qp, d.qs, nx);
+                load_coef(nx, c + 1);
+            } else {
+                wait_barrier<nState + nRows>();  // everything is here, the other k buffer is free
+                load_qk(oK + ((c + 1) & 1) * KBYTES, a.k, a.Kp, d.ks, nx);
+            }
+            const float* cf = coef(c);
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                Parts<NP> op[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) op[t] = row_op(kb, t, j);
+                mma_a(x, op, sp[j]);
+            }
+            // R = v - e^G x, E = M R (value column p0 + i, tokens 16 t + 4 g + v)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) x[t] = value(t) - at4(cf + 16 * t + 4 * g) * x[t];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) tri_mul<true, 3>(u, oM, j, split44<3>(x[2 * j], x[2 * j + 1]));
+            v4f z[4];
+            wait_barrier<63>();  // M and v are free
+            copy_tiles<3 * DTRI>(oM, a.M + (bh * d.N + nx) * (3 * DTRI * DTILE));
+            load_v(a.v, d.vs[0], d.vs[1], d.vs[2], nx);
+            if constexpr (MODE == kRecord) {
+                load_coef(nx, c + 1);
+                record_state(s, a.H, c);
+                record_rows(u, a.E, c);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                u[t] *= at4(cf + 2 * DL + 16 * t + 4 * g);
+                z[t] = u[t] * at4(cf + DL + 16 * t + 4 * g);
+            }
+            const float eL = cf[3 * DL];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) s[r] *= eL;
+            add_outer(s, kb, z);
+            if constexpr (MODE == kOutputs) {
+                wait_barrier<nQ + nC + nM + nV>();  // P is here, k is free
+                load_qk(oK, a.k, a.Kp, d.ks, nx);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[t] *= d.scale * cf[16 * t + i];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const auto up = split44<NQ>(u[2 * j], u[2 * j + 1]);
+                    if (j == 0) {
+                        Parts<NQ> op[4];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) op[t] = tri_op<NQ>(oP, tri_lower(t, 0));
+                        mma_b(y, up, op);
+                    } else {
+                        Parts<NQ> op[2];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) op[t] = tri_op<NQ>(oP, tri_lower(2 + t, 1));
+                        mma_b(*reinterpret_cast<v4f(*)[2]>(&y[2]), up, op);
+                    }
+                }
+                store_y(y, c);
+            }
+            mfma_settle();
+        }
+        wait_barrier<0>();  // no load may land after the workgroup has left
+        if constexpr (MODE == kOutputs) {
+            store_state(s, a.final_state);
+            const v4f zero[4] = {zero4(), zero4(), zero4(), zero4()};
+            for (; c < d.N; ++c) store_y(zero, c);  // chunks past the row's length
+        }
+    }
+
+    // -------------------------------------------------------------- the reverse recurrence
+    __device__ void reverse() const {
+        v4f s[RT];
+        load_state(s, a.d_final);
+        const int64_t tok = static_cast<int64_t>(d.H) * d.P;
+        auto load_front = [&](int c, int buf) {  // what the first two phases read
+            copy_tiles<3 * DTRI>(oP, a.P + (bh * d.N + c) * (3 * DTRI * DTILE));
+            load_qk(oQ, a.q, a.Qp, d.qs, c);
+            load_v(a.dy, d.S * tok, tok, d.P, c);
+            load_coef(c, buf);
+        };
+        if (chunks > 0) {
+            load_front(chunks - 1, chunks - 1);
+            copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + chunks - 1) * (3 * DTRI * DTILE));
+            load_qk(oK, a.k, a.Kp, d.ks, chunks - 1);
+            wait_barrier<0>();
+        }
+        for (int c = chunks - 1; c >= 0; --c) {
+            const int nx = c > 0 ? c - 1 : 0;
+            v4f u[4], dy[4], x[4], gq[RT];
+            wait_barrier<nM + nRows + nK>();  // P^T, q, dy and the coefficients are here
+            const float* cf = coef(c);
+            record_state(s, a.dH, c);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                dy[t] = value(t);
+                u[t] = x[t] = zero4();
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) gq[r] = zero4();
+            // dU = P^T dy + tail (K dH^T)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) tri_mul<false, 3>(u, oP, j, split44<NP>(dy[2 * j], dy[2 * j + 1]));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dy[t] *= d.scale * at4(cf + 16 * t + 4 * g);
+            add_outer(gq, oQ, dy);
+            v4f eg[4], tail[4], be[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                eg[t] = at4(cf + 16 * t + 4 * g);
+                tail[t] = at4(cf + DL + 16 * t + 4 * g);
+                be[t] = at4(cf + 2 * DL + 16 * t + 4 * g);
+            }
+            const float eL = cf[3 * DL];
+            wait_barrier<nState>();  // N^T and k are here, P^T, q and dy are free
+            load_front(nx, c - 1);
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                const auto sp = split44<3>(s[2 * j], s[2 * j + 1]);
+                Parts<NP> op[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) op[t] = row_op(oK, t, j);
+                mma_a(x, op, sp);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                u[t] += tail[t] * x[t];
+                x[t] = zero4();
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) tri_mul<false, 3>(x, oM, j, split44<3>(u[2 * j], u[2 * j + 1]));
+            wait_barrier<63>();  // N^T is free
+            copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + nx) * (3 * DTRI * DTILE));
+            record_rows(x, a.dZ, c);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) x[t] *= -eg[t] * be[t];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) s[r] = eL * s[r] + gq[r];
+            add_outer(s, oK, x);
+            wait_barrier<63>();  // k is free
+            load_qk(oK, a.k, a.Kp, d.ks, nx);
+            mfma_settle();
+        }
+        wait_barrier<0>();
+        store_state(s, a.d_init);
+    }
+};
+
+// The eight XCDs take workgroups in turn and each has its own L2: give each a consecutive run of
+// the work, so that the columns and value heads that read the same keys meet in one.
+__device__ __forceinline__ int64_t xcd_order(int64_t blk, int64_t n) {
+    const int64_t x = blk % 8, q = n / 8, rem = n % 8;
+    return x * q + (x < rem ? x : rem) + blk / 8;
 }
 
 }  // namespace
 
 template <class IO, int R, int W>
 __global__ __launch_bounds__(64 * W) void k_delta_scan(DeltaShape d, DeltaScan<typename IO::T> a) {
-    constexpr int NQ = in_parts<IO>() == 1 ? 2 : 3;
-    __shared__ __align__(16) ScanLds<IO, R, NQ> sm;
-    scan_fwd<IO, R, W, NQ>(sm, d, a, blockIdx.x);
+    using S = Scan<IO, R, W, kOutputs>;
+    __shared__ __align__(16) char sm[S::LDS];
+    S(sm, d, a, xcd_order(blockIdx.x, gridDim.x)).forward();
 }
 
-// Both recurrences of the backward: the first half of the grid recomputes the entry states,
-// the second half runs the reverse.
+// Both recurrences of the backward, in alternating workgroups: one recomputes the entry states
+// and E, the other runs the reverse.
 template <class IO, int R, int W>
 __global__ __launch_bounds__(64 * W) void k_delta_states(DeltaShape d, DeltaScan<typename IO::T> a) {
-    __shared__ __align__(16) union Lds {
-        ScanLds<IO, R, 0> f;
-        ScanLds<IO, R, 3> r;
-    } sm;
-    const int64_t half = gridDim.x / 2;
-    if (blockIdx.x < half)
-        scan_fwd<IO, R, W, 0>(sm.f, d, a, blockIdx.x);
+    using F = Scan<IO, R, W, kRecord>;
+    using B = Scan<IO, R, W, kReverse>;
+    __shared__ __align__(16) char sm[F::LDS > B::LDS ? F::LDS : B::LDS];
+    const int64_t blk = xcd_order(blockIdx.x, gridDim.x);
+    if (blk & 1)
+        B(sm, d, a, blk >> 1).reverse();
     else
-        scan_rev<IO, R, W>(sm.r, d, a, blockIdx.x - half);
+        F(sm, d, a, blk >> 1).forward();
 }
 
 namespace {
@@ -615,6 +727,8 @@ DeltaScan<typename IO::T> typed(const DeltaBufs& f) {
     a.M = f.M;
     a.P = f.P;
     a.NT = f.NT;
+    a.Kp = f.Kp;
+    a.Qp = f.Qp;
     a.H = f.H;
     a.E = f.E;
     a.dH = f.dH;
@@ -627,9 +741,11 @@ hipError_t prep_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t
     const auto a = typed<IO>(f);
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * d.N));
     if (bwd)
-        k_delta_prep<IO, R, true><<<grid, 256, 0, st>>>(d, a.q, a.k, f.g, f.beta, a.len, a.coef, a.M, a.P, a.NT);
+        k_delta_prep<IO, R, true><<<grid, 256, 0, st>>>(d, a.q, a.k, f.g, f.beta, a.len, a.coef, a.M, a.P, a.NT,
+                                                    a.Kp, a.Qp);
     else
-        k_delta_prep<IO, R, false><<<grid, 256, 0, st>>>(d, a.q, a.k, f.g, f.beta, a.len, a.coef, a.M, a.P, nullptr);
+        k_delta_prep<IO, R, false><<<grid, 256, 0, st>>>(d, a.q, a.k, f.g, f.beta, a.len, a.coef, a.M, a.P,
+                                                     nullptr, a.Kp, a.Qp);
     return hipGetLastError();
 }
 

@@ -85,7 +85,7 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
         } v;
         uint16_t S[3 * SP];
     } sm;
-    __shared__ float sCf[3 * DL];
+    __shared__ float sCf[3 * DL + 1];  // e^G, e^{G_L - G}, beta, e^{G_L}
     __shared__ double sG[DL];
     __shared__ float sLoc[RT][DL], sWr[RT][DL], sRow[4][DL], sCol[4][DL], sDot[8];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
@@ -141,8 +141,8 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
         const int64_t ch = (static_cast<int64_t>(b) * d.H + h) * d.N + c;
         const float* cf = a.coef + ch * DCOEF;
         __syncthreads();
-        if (tid < 3 * DL) sCf[tid] = cf[tid];
-        if (tid < DL) sG[tid] = reinterpret_cast<const double*>(cf + 3 * DL)[tid];
+        if (tid <= 3 * DL) sCf[tid] = cf[tid];
+        if (tid < DL) sG[tid] = reinterpret_cast<const double*>(cf + DCF)[tid];
         v4f aq[ITEMS], akr[ITEMS], akw[ITEMS], dP[2], dA[2];
 #pragma unroll
         for (int m = 0; m < ITEMS; ++m) aq[m] = akr[m] = akw[m] = zero4();
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
         }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) db += __shfl_xor(db, o);
-        if ((tid & 7) == 0 && (tid >> 3) < all) d_beta[(row0 + (tid >> 3)) * d.H + h] = db;
+        if ((tid & 7) == 0 && (tid >> 3) < all) d_beta[(row0 + (tid >> 3)) * d.H + h] = (tid >> 3) < L ? db : 0.0f;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {  // dS, then dKK
             __syncthreads();
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
                 }
                 pre = __shfl_up(pre, 1);
                 if (lane == 0) pre = 0.0;
-                const double out = suf + pre + static_cast<double>(sCf[DL - 1]) * hd;
+                const double out = suf + pre + static_cast<double>(sCf[3 * DL]) * hd;
                 if (lane < all) d_g[(row0 + lane) * d.H + h] = lane < L ? static_cast<float>(out) : 0.0f;
             }
             if (act) {

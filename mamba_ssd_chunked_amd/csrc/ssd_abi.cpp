@@ -471,8 +471,8 @@ int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape*
     for (int k = 0; k < 3; ++k) {
         if (dims->q_stride[k] < 0 || dims->k_stride[k] < 0 || dims->v_stride[k] < 0)
             return fail(SSD_ERR_SHAPE, "%s: strides must not be negative", who);
-        if (dims->q_stride[k] % unit || dims->k_stride[k] % unit)
-            return fail(SSD_ERR_UNSUPPORTED, "%s: strides of q and k must be whole 16 bytes", who);
+        if (dims->q_stride[k] % unit || dims->k_stride[k] % unit || dims->v_stride[k] % unit)
+            return fail(SSD_ERR_UNSUPPORTED, "%s: strides of q, k and v must be whole 16 bytes", who);
         d->qs[k] = dims->q_stride[k];
         d->ks[k] = dims->k_stride[k];
         d->vs[k] = dims->v_stride[k];
@@ -511,9 +511,11 @@ size_t delta_plan(const ssd::DeltaShape& d, bool bwd, void* ws, ssd::DeltaBufs* 
     const size_t n = static_cast<size_t>(d.chunk_heads()), tri = 6 * 512 * 2;
     const size_t state = 4 * static_cast<size_t>(d.P) * d.R, rows = 4 * static_cast<size_t>(64) * d.P;
     f->len = reinterpret_cast<int64_t*>(take(8 * static_cast<size_t>(d.B)));
-    f->coef = reinterpret_cast<float*>(take(5 * 64 * 4 * n));
+    f->coef = reinterpret_cast<float*>(take(6 * 64 * 4 * n));
     f->M = reinterpret_cast<uint16_t*>(take(3 * tri * n));
     f->P = reinterpret_cast<uint16_t*>(take((bwd || d.io == SSD_F32 ? 3 : 2) * tri * n));
+    f->Kp = reinterpret_cast<uint16_t*>(take(ssd::delta_parts_bytes(d)));
+    f->Qp = reinterpret_cast<uint16_t*>(take(ssd::delta_parts_bytes(d)));
     if (bwd) {
         f->NT = reinterpret_cast<uint16_t*>(take(3 * tri * n));
         f->H = reinterpret_cast<float*>(take(state * n));
@@ -1072,8 +1074,7 @@ int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, cons
     const bool tok = d.B > 0 && d.N > 0;
     if (tok && (!q || !k || !v || !g || !beta || !y))
         return fail(SSD_ERR_NULL, "%s: q, k, v, g, beta and y are required", who);
-    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {init, "init"}, {final_state, "final_state"}})) return rc;
-    if (int rc = check_align(y, "y", d.io == SSD_BF16 ? 8 : 16)) return rc;
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {y, "y"}, {init, "init"}, {final_state, "final_state"}})) return rc;
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
     ssd::DeltaBufs f{};
     const size_t need = delta_plan(d, false, ws, &f);
@@ -1112,11 +1113,9 @@ int ssd_delta_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fin
     const bool tok = d.B > 0 && d.N > 0;
     if (tok && (!dy || !q || !k || !v || !g || !beta || !d_q || !d_k || !d_v || !d_g || !d_beta))
         return fail(SSD_ERR_NULL, "%s: dy, q, k, v, g, beta, d_q, d_k, d_v, d_g and d_beta are required", who);
-    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {init, "init"}, {d_final, "d_final"}, {d_init, "d_init"}}))
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {dy, "dy"}, {d_q, "d_q"}, {d_k, "d_k"}, {d_v, "d_v"}, {init, "init"},
+                                  {d_final, "d_final"}, {d_init, "d_init"}}))
         return rc;
-    const size_t ia = d.io == SSD_BF16 ? 8 : 16;
-    for (auto& p : {std::pair<const void*, const char*>{dy, "dy"}, {d_q, "d_q"}, {d_k, "d_k"}, {d_v, "d_v"}})
-        if (int rc = check_align(p.first, p.second, ia)) return rc;
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
     ssd::DeltaBufs f{};
     const size_t need = delta_plan(d, true, ws, &f);
@@ -1168,7 +1167,7 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
     if (d.B == 0) return ok();
     if (!q || !k || !v || !g || !beta || !y || (!state && nslots > 0))
         return fail(SSD_ERR_NULL, "%s: q, k, v, g, beta, state and y are required", who);
-    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {state, "state"}})) return rc;
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {state, "state"}})) return rc;
     hipStream_t st = static_cast<hipStream_t>(stream);
     SSD_HIP(ssd::launch_delta_step(d, (int)nslots, q, k, v, g, beta, state, slots, y, st), "k_delta_step");
     return ok();

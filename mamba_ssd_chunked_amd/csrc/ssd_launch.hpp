@@ -298,7 +298,7 @@ struct DeltaShape {
 
 // Everything the delta kernels read and write.  len: device copy of valid_len, or null.
 // Workspace, per (b, h, chunk): coef; M, P (forward and backward), NT (backward) in bf16
-// parts; the backward's entry states H and leaving gradients dH [r, p], E and dZ [64, p].
+// parts; Kp, Qp; the backward's entry states H and leaving gradients dH [r, p], E and dZ [64, p].
 struct DeltaBufs {
     const void *q, *k, *v, *dy;
     const float *g, *beta, *init, *d_final;
@@ -306,9 +306,16 @@ struct DeltaBufs {
     void *y, *d_q, *d_k, *d_v;
     float *final_state, *d_g, *d_beta, *d_init;
     float* coef;
-    uint16_t *M, *P, *NT;
+    uint16_t *M, *P, *NT, *Kp, *Qp;
     float *H, *E, *dH, *dZ;
 };
+
+// Bytes of Kp and Qp each (the bf16 parts of k and q per (b, key head, chunk)); 0 where the scans
+// read the tensors themselves.
+inline size_t delta_parts_bytes(const DeltaShape& d) {
+    if (d.io == 1 && d.R >= 32) return 0;
+    return static_cast<size_t>(d.B) * d.HK * d.N * (d.io == 1 ? 1 : 3) * 64 * (d.R < 32 ? 32 : d.R) * 2;
+}
 
 // Decay factors and triangular operands of every chunk.
 hipError_t launch_delta_prep(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st);
