@@ -286,10 +286,16 @@ namespace {
 
 enum ScanMode { kOutputs, kRecord, kReverse };
 
-// One scan workgroup: W waves, each 16 value columns of one head.  What a chunk needs is loaded
-// into LDS without passing registers, a chunk ahead, into the buffer that its predecessor has
-// just left: the phases of a chunk are ordered so that between the last read of a buffer and
-// the first read of its next contents lies another phase's matrix work.
+// Loading waves of a scan workgroup: a wave has at most 63 loads under way, and a chunk of fp32
+// operands is twice that.
+template <class IO>
+__host__ __device__ constexpr int scan_loaders() { return in_parts<IO>() == 1 ? 1 : 2; }
+
+// One scan workgroup: W waves that compute, each 16 value columns of one head, and NL that load.
+// The loading waves bring what a chunk needs into LDS without passing registers, a chunk ahead,
+// into the buffer that its predecessor has just left: the phases of a chunk are ordered so that
+// between the last read of a buffer and the first read of its next contents lies another phase's
+// matrix work.  They count their own loads; the computing waves meet them at barriers only.
 template <class IO, int R, int W, ScanMode MODE>
 struct Scan {
     using T = typename IO::T;
@@ -298,6 +304,7 @@ struct Scan {
     // parts of y's operands: an output rounded to bf16 needs no third part (2^-17 of it)
     static constexpr int NQ = MODE == kOutputs && NP == 1 ? 2 : 3;
     static constexpr int QT = 4 * KJ;  // tiles per part
+    static constexpr int NL = scan_loaders<IO>();
     // LDS, bytes
     static constexpr int KBYTES = NP * QT * 1024, KBUFS = MODE == kRecord ? 2 : 1;
     static constexpr int QBYTES = MODE == kRecord ? 0 : KBYTES;
@@ -305,10 +312,10 @@ struct Scan {
     static constexpr int VBYTES = DL * 16 * W * sizeof(T);
     static constexpr int oK = 0, oQ = oK + KBUFS * KBYTES, oM = oQ + QBYTES, oP = oM + MBYTES, oV = oP + PBYTES,
                          oC = oV + VBYTES, LDS = oC + 2 * 4 * DCF;
-    // loads and stores per wave
-    static constexpr int nK = (NP * QT + W - 1) / W, nQ = nK, nM = (3 * DTRI + W - 1) / W,
-                         nP = (NQ * DTRI + W - 1) / W, nV = VBYTES / (1024 * W), nC = 1, nY = 4;
-    static constexpr int nState = RT * 4, nRows = 16;
+    // loads of one loading wave
+    static constexpr int per(int n) { return (n + NL - 1) / NL; }
+    static constexpr int nK = per(NP * QT), nQ = nK, nM = per(3 * DTRI), nP = per(NQ * DTRI), nV = per(VBYTES / 1024),
+                         nC = 1;
 
     char* sm;
     const DeltaShape& d;
@@ -333,14 +340,15 @@ struct Scan {
     }
 
     // -------------------------------------------------------------- loads into LDS
+    __device__ int unit(int m, int n) const {  // this loading wave's m-th of n: each loads as often
+        const int t = w - W + m * NL;
+        return n % NL == 0 || t < n ? t : n - 1;
+    }
     template <int N>  // N kilobytes, as they are
     __device__ void copy_tiles(int at, const uint16_t* src) const {
         const uint32_t dst = lds_addr(sm) + at;
 #pragma unroll
-        for (int m = 0; m < (N + W - 1) / W; ++m) {
-            const int t = N % W == 0 || w + m * W < N ? w + m * W : N - 1;  // every wave loads as often
-            load_to_lds(src + t * DTILE + lane * 8, dst + t * 1024);
-        }
+        for (int m = 0; m < per(N); ++m) load_to_lds(src + unit(m, N) * DTILE + lane * 8, dst + unit(m, N) * 1024);
     }
     // Tokens of chunk c of q or k.  Rows past the length repeat its last row: what they feed is
     // multiplied by the zeros of beta and e^G there.
@@ -353,10 +361,12 @@ struct Scan {
             const T* base = x + b * stride[0] + static_cast<int64_t>(c) * DL * stride[1] + hk * stride[2] + 8 * gs;
             const uint32_t dst = lds_addr(sm) + at;
 #pragma unroll
-            for (int m = 0; m < nK; ++m) {
-                const int t = QT % W == 0 || w + m * W < QT ? w + m * W : QT - 1;
-                const int row = 16 * (t / KJ) + is;
-                load_to_lds(base + (row < last ? row : last) * stride[1] + 32 * (t % KJ), dst + t * 1024);
+            for (int tau = 0; tau < 4; ++tau) {
+                const int row = 16 * tau + is;
+                const T* src = base + (row < last ? row : last) * stride[1];
+#pragma unroll
+                for (int j = 0; j < KJ; ++j)
+                    if (NL == 1 || (tau * KJ + j) % NL == w - W) load_to_lds(src + 32 * j, dst + (tau * KJ + j) * 1024);
             }
         }
     }
@@ -367,9 +377,9 @@ struct Scan {
         const T* base = x + b * sb + static_cast<int64_t>(c) * DL * st + h * sh + pw;
 #pragma unroll
         for (int m = 0; m < nV; ++m) {
-            const int u = (m * W + w) * 64 + lane, row = u / U;
+            const int n = unit(m, VBYTES / 1024), u = n * 64 + lane, row = u / U;
             load_to_lds(base + (row < last ? row : last) * st + (u % U) * (16 / static_cast<int>(sizeof(T))),
-                        lds_addr(sm) + oV + (m * W + w) * 1024);
+                        lds_addr(sm) + oV + n * 1024);
         }
     }
     __device__ void load_coef(int c, int buf) const {
@@ -494,21 +504,60 @@ struct Scan {
         }
     }
 
+    __device__ void load_forward() const {
+        auto m = [&](int c) {
+            copy_tiles<3 * DTRI>(oM, a.M + (bh * d.N + c) * (3 * DTRI * DTILE));
+            load_v(a.v, d.vs[0], d.vs[1], d.vs[2], c);
+        };
+        if constexpr (MODE == kOutputs) {
+            load_qk(oQ, a.q, a.Qp, d.qs, 0);
+            load_coef(0, 0);
+            m(0);
+            load_qk(oK, a.k, a.Kp, d.ks, 0);
+            for (int c = 0; c < chunks; ++c) {
+                const bool more = c + 1 < chunks;
+                wait_barrier<nM + nV + nK>();  // q and the coefficients
+                copy_tiles<NQ * DTRI>(oP, a.P + (bh * d.N + c) * (NQ * DTRI * DTILE));
+                wait_barrier<nP>();  // M, v and k
+                if (more) {
+                    load_qk(oQ, a.q, a.Qp, d.qs, c + 1);
+                    load_coef(c + 1, c + 1);
+                }
+                wait_barrier<63>();
+                if (more) {
+                    m(c + 1);
+                    wait_barrier<nQ + nC + nM + nV>();  // P
+                    load_qk(oK, a.k, a.Kp, d.ks, c + 1);
+                } else {
+                    wait_barrier<0>();
+                }
+            }
+        } else {
+            load_qk(oK, a.k, a.Kp, d.ks, 0);
+            load_coef(0, 0);
+            m(0);
+            for (int c = 0; c < chunks; ++c) {
+                const bool more = c + 1 < chunks;
+                wait_barrier<0>();
+                if (more) load_qk(oK + ((c + 1) & 1) * KBYTES, a.k, a.Kp, d.ks, c + 1);
+                wait_barrier<63>();
+                if (more) {
+                    m(c + 1);
+                    load_coef(c + 1, c + 1);
+                }
+            }
+        }
+    }
+
     __device__ void forward() const {
+        if (w >= W) {
+            if (chunks > 0) load_forward();
+            return;
+        }
         v4f s[RT];
         load_state(s, a.init);
         int c = 0;
-        if (chunks > 0) {
-            if constexpr (MODE == kOutputs) load_qk(oQ, a.q, a.Qp, d.qs, 0);
-            load_coef(0, 0);
-            copy_tiles<3 * DTRI>(oM, a.M + bh * d.N * (3 * DTRI * DTILE));
-            load_v(a.v, d.vs[0], d.vs[1], d.vs[2], 0);
-            load_qk(oK, a.k, a.Kp, d.ks, 0);
-            wait_barrier<0>();
-        }
         for (; c < chunks; ++c) {
-            const int64_t ch = bh * d.N + c;
-            const int nx = c + 1 < chunks ? c + 1 : c;  // the last chunk loads itself again
             const int kb = oK + (MODE == kRecord ? (c & 1) * KBYTES : 0);
             v4f x[4], y[4], u[4];
 #pragma unroll
@@ -516,9 +565,8 @@ struct Scan {
             Parts<3> sp[KJ];
 #pragma unroll
             for (int j = 0; j < KJ; ++j) sp[j] = split44<3>(s[2 * j], s[2 * j + 1]);
+            meet();  // outputs: q and the coefficients are here, P is free; else everything is here
             if constexpr (MODE == kOutputs) {
-                wait_barrier<nM + nV + nK + nY>();  // q and the coefficients are here, P is free
-                copy_tiles<NQ * DTRI>(oP, a.P + ch * (NQ * DTRI * DTILE));
 #pragma unroll
                 for (int j = 0; j < KJ; ++j) {
                     Parts<NP> op[4];
@@ -529,12 +577,7 @@ struct Scan {
                     for (int t = 0; t < 4; ++t) op[t] = row_op(oQ, t, j);
                     mma_b(y, sy, op);
                 }
-                wait_barrier<nY + nP>();  // M, v and k are here, q is free
-                load_qk(oQ, a.q, a.Qp, d.qs, nx);
-                load_coef(nx, c + 1);
-            } else {
-                wait_barrier<nState + nRows>();  // everything is here, the other k buffer is free
-                load_qk(oK + ((c + 1) & 1) * KBYTES, a.k, a.Kp, d.ks, nx);
+                meet();  // M, v and k are here, q is free
             }
             const float* cf = coef(c);
 #pragma unroll
@@ -550,11 +593,8 @@ struct Scan {
 #pragma unroll
             for (int j = 0; j < 2; ++j) tri_mul<true, 3>(u, oM, j, split44<3>(x[2 * j], x[2 * j + 1]));
             v4f z[4];
-            wait_barrier<63>();  // M and v are free
-            copy_tiles<3 * DTRI>(oM, a.M + (bh * d.N + nx) * (3 * DTRI * DTILE));
-            load_v(a.v, d.vs[0], d.vs[1], d.vs[2], nx);
+            meet();  // M and v are free
             if constexpr (MODE == kRecord) {
-                load_coef(nx, c + 1);
                 record_state(s, a.H, c);
                 record_rows(u, a.E, c);
             }
@@ -568,8 +608,7 @@ struct Scan {
             for (int r = 0; r < RT; ++r) s[r] *= eL;
             add_outer(s, kb, z);
             if constexpr (MODE == kOutputs) {
-                wait_barrier<nQ + nC + nM + nV>();  // P is here, k is free
-                load_qk(oK, a.k, a.Kp, d.ks, nx);
+                meet();  // P is here, k is free
 #pragma unroll
                 for (int t = 0; t < 4; ++t) y[t] *= d.scale * cf[16 * t + i];
 #pragma unroll
@@ -591,7 +630,6 @@ struct Scan {
             }
             mfma_settle();
         }
-        wait_barrier<0>();  // no load may land after the workgroup has left
         if constexpr (MODE == kOutputs) {
             store_state(s, a.final_state);
             const v4f zero[4] = {zero4(), zero4(), zero4(), zero4()};
@@ -600,26 +638,38 @@ struct Scan {
     }
 
     // -------------------------------------------------------------- the reverse recurrence
-    __device__ void reverse() const {
-        v4f s[RT];
-        load_state(s, a.d_final);
+    __device__ void load_reverse() const {
         const int64_t tok = static_cast<int64_t>(d.H) * d.P;
-        auto load_front = [&](int c, int buf) {  // what the first two phases read
+        auto front = [&](int c) {  // what the first two phases read
             copy_tiles<3 * DTRI>(oP, a.P + (bh * d.N + c) * (3 * DTRI * DTILE));
             load_qk(oQ, a.q, a.Qp, d.qs, c);
             load_v(a.dy, d.S * tok, tok, d.P, c);
-            load_coef(c, buf);
+            load_coef(c, c);
         };
-        if (chunks > 0) {
-            load_front(chunks - 1, chunks - 1);
-            copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + chunks - 1) * (3 * DTRI * DTILE));
-            load_qk(oK, a.k, a.Kp, d.ks, chunks - 1);
-            wait_barrier<0>();
-        }
+        front(chunks - 1);
+        copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + chunks - 1) * (3 * DTRI * DTILE));
+        load_qk(oK, a.k, a.Kp, d.ks, chunks - 1);
         for (int c = chunks - 1; c >= 0; --c) {
-            const int nx = c > 0 ? c - 1 : 0;
+            wait_barrier<nM + nK>();  // P^T, q, dy and the coefficients
+            wait_barrier<0>();        // N^T and k
+            if (c > 0) front(c - 1);
+            wait_barrier<63>();
+            if (c > 0) copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + c - 1) * (3 * DTRI * DTILE));
+            wait_barrier<63>();
+            if (c > 0) load_qk(oK, a.k, a.Kp, d.ks, c - 1);
+        }
+    }
+
+    __device__ void reverse() const {
+        if (w >= W) {
+            if (chunks > 0) load_reverse();
+            return;
+        }
+        v4f s[RT];
+        load_state(s, a.d_final);
+        for (int c = chunks - 1; c >= 0; --c) {
             v4f u[4], dy[4], x[4], gq[RT];
-            wait_barrier<nM + nRows + nK>();  // P^T, q, dy and the coefficients are here
+            meet();  // P^T, q, dy and the coefficients are here
             const float* cf = coef(c);
             record_state(s, a.dH, c);
 #pragma unroll
@@ -635,16 +685,7 @@ struct Scan {
 #pragma unroll
             for (int t = 0; t < 4; ++t) dy[t] *= d.scale * at4(cf + 16 * t + 4 * g);
             add_outer(gq, oQ, dy);
-            v4f eg[4], tail[4], be[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                eg[t] = at4(cf + 16 * t + 4 * g);
-                tail[t] = at4(cf + DL + 16 * t + 4 * g);
-                be[t] = at4(cf + 2 * DL + 16 * t + 4 * g);
-            }
-            const float eL = cf[3 * DL];
-            wait_barrier<nState>();  // N^T and k are here, P^T, q and dy are free
-            load_front(nx, c - 1);
+            meet();  // N^T and k are here, P^T, q and dy are free
 #pragma unroll
             for (int j = 0; j < KJ; ++j) {
                 const auto sp = split44<3>(s[2 * j], s[2 * j + 1]);
@@ -655,26 +696,27 @@ struct Scan {
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                u[t] += tail[t] * x[t];
+                u[t] += at4(cf + DL + 16 * t + 4 * g) * x[t];
                 x[t] = zero4();
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) tri_mul<false, 3>(x, oM, j, split44<3>(u[2 * j], u[2 * j + 1]));
-            wait_barrier<63>();  // N^T is free
-            copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + nx) * (3 * DTRI * DTILE));
+            meet();  // N^T is free
             record_rows(x, a.dZ, c);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) x[t] *= -eg[t] * be[t];
+            for (int t = 0; t < 4; ++t) x[t] *= -at4(cf + 16 * t + 4 * g) * at4(cf + 2 * DL + 16 * t + 4 * g);
+            const float eL = cf[3 * DL];
 #pragma unroll
             for (int r = 0; r < RT; ++r) s[r] = eL * s[r] + gq[r];
             add_outer(s, oK, x);
-            wait_barrier<63>();  // k is free
-            load_qk(oK, a.k, a.Kp, d.ks, nx);
+            meet();  // k is free
             mfma_settle();
         }
-        wait_barrier<0>();
         store_state(s, a.d_init);
     }
+
+    // A computing wave's side of a barrier: its LDS reads have returned.
+    __device__ static void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 };
 
 // The eight XCDs take workgroups in turn and each has its own L2: give each a consecutive run of
@@ -687,7 +729,7 @@ __device__ __forceinline__ int64_t xcd_order(int64_t blk, int64_t n) {
 }  // namespace
 
 template <class IO, int R, int W>
-__global__ __launch_bounds__(64 * W) void k_delta_scan(DeltaShape d, DeltaScan<typename IO::T> a) {
+__global__ __launch_bounds__(64 * (W + scan_loaders<IO>()), 2) void k_delta_scan(DeltaShape d, DeltaScan<typename IO::T> a) {
     using S = Scan<IO, R, W, kOutputs>;
     __shared__ __align__(16) char sm[S::LDS];
     S(sm, d, a, xcd_order(blockIdx.x, gridDim.x)).forward();
@@ -696,7 +738,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_scan(DeltaShape d, DeltaScan<t
 // Both recurrences of the backward, in alternating workgroups: one recomputes the entry states
 // and E, the other runs the reverse.
 template <class IO, int R, int W>
-__global__ __launch_bounds__(64 * W) void k_delta_states(DeltaShape d, DeltaScan<typename IO::T> a) {
+__global__ __launch_bounds__(64 * (W + scan_loaders<IO>()), 2) void k_delta_states(DeltaShape d, DeltaScan<typename IO::T> a) {
     using F = Scan<IO, R, W, kRecord>;
     using B = Scan<IO, R, W, kReverse>;
     __shared__ __align__(16) char sm[F::LDS > B::LDS ? F::LDS : B::LDS];
@@ -751,12 +793,13 @@ hipError_t prep_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t
 
 template <class IO, int R, int W>
 hipError_t scan_w(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
+    constexpr int NTHR = 64 * (W + scan_loaders<IO>());
     const auto a = typed<IO>(f);
     const int64_t wgs = static_cast<int64_t>(d.B) * d.H * (d.P / (16 * W));
     if (bwd)
-        k_delta_states<IO, R, W><<<dim3(static_cast<unsigned>(2 * wgs)), 64 * W, 0, st>>>(d, a);
+        k_delta_states<IO, R, W><<<dim3(static_cast<unsigned>(2 * wgs)), NTHR, 0, st>>>(d, a);
     else
-        k_delta_scan<IO, R, W><<<dim3(static_cast<unsigned>(wgs)), 64 * W, 0, st>>>(d, a);
+        k_delta_scan<IO, R, W><<<dim3(static_cast<unsigned>(wgs)), NTHR, 0, st>>>(d, a);
     return hipGetLastError();
 }
 
