@@ -42,6 +42,44 @@ __device__ __forceinline__ int chunk_tokens(const int64_t* len, int b, int S, in
     return n < 0 ? 0 : (n > DL ? DL : n);
 }
 
+// The eight XCDs take workgroups in turn and each has its own L2: give each a consecutive run of
+// the work, so that the columns and value heads that read the same keys meet in one.
+__device__ __forceinline__ int64_t xcd_order(int64_t blk, int64_t n) {
+    const int64_t x = blk % 8, q = n / 8, rem = n % 8;
+    return x * q + (x < rem ? x : rem) + blk / 8;
+}
+
+// Eight io values as bf16 parts, zeros where !on.
+template <class IO, class V>
+__device__ __forceinline__ Parts<in_parts<IO>()> parts_of(const V& x, bool on) {
+    Parts<in_parts<IO>()> o;
+    if constexpr (in_parts<IO>() == 1) {
+        uint4 w = __builtin_bit_cast(uint4, x);
+        if (!on) w = make_uint4(0, 0, 0, 0);
+        o.p[0] = __builtin_bit_cast(b8v, w);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = on ? x[e] : 0.0f;
+        o = split8<3>(f);
+    }
+    return o;
+}
+// Half a lane's slots of an operand tile (four values) as N parts.
+template <int N>
+__device__ __forceinline__ void put_half(uint16_t* dst, int tile, int lane, int half, v4f x) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        uint2 w;
+        w.x = f32x2_to_bf16x2(x[0], x[1]);
+        w.y = f32x2_to_bf16x2(x[2], x[3]);
+        *reinterpret_cast<uint2*>(dst + (n * DTRI + tile) * DTILE + lane * 8 + 4 * half) = w;
+        if (n + 1 < N)
+            x -= v4f{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+    }
+}
+
 // One 16 x 16 tile of a product of fp32 LDS matrices (row stride CS): A rows, B columns.
 __device__ __forceinline__ v4f tile_mul(const float* A, const float* B, int i, int g, v4f c) {
 #pragma unroll
@@ -65,15 +103,19 @@ __device__ __forceinline__ void tile_store_neg(float* X, v4f y, int i, int g) {
 __device__ __forceinline__ void invert_lower(const float* C, float* X) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
     const int d = 16 * w * CS + 16 * w;
-    {  // diagonal blocks: lane i solves column i
+    {  // diagonal blocks: lane i solves column i, each solved row at once taken off those below
+        v4f cr[16][4];
+#pragma unroll
+        for (int t = 1; t < 16; ++t)
+#pragma unroll
+            for (int q = 0; q < (t + 3) / 4; ++q) cr[t][q] = *reinterpret_cast<const v4f*>(C + d + t * CS + 4 * q);
         float x[16];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            float acc = t == i ? 1.0f : 0.0f;
+        for (int t = 0; t < 16; ++t) x[t] = t == i ? 1.0f : 0.0f;
 #pragma unroll
-            for (int s = 0; s < t; ++s) acc -= C[d + t * CS + s] * x[s];
-            x[t] = acc;
-        }
+        for (int s = 0; s < 15; ++s)
+#pragma unroll
+            for (int t = s + 1; t < 16; ++t) x[t] -= cr[t][s / 4][s % 4] * x[s];
         if (g == 0) {
 #pragma unroll
             for (int t = 0; t < 16; ++t) X[d + t * CS + i] = x[t];
@@ -103,9 +145,11 @@ __device__ __forceinline__ void invert_lower(const float* C, float* X) {
 }  // namespace
 
 // Per (b, h, chunk): the chunk's decay factors (coef: e^G, e^{G_L - G}, beta, and G in base 2
-// and fp64) and its
-// triangular matrices as bf16 parts in operand order.  Forward: M and P (rows t, k over s);
-// backward: M, and N^T and P^T (rows s, k over t).
+// and fp64) and its triangular matrices as bf16 parts in operand order.  Forward: M and P (rows
+// t, k over s); backward: M, and N^T and P^T (rows s, k over t).
+//
+// Wave w has the tokens 16 w .. + 15: their rows of K and Q stay in its registers as operands, and
+// the key rows of the others come through LDS, which the fp32 matrices take over afterwards.
 template <class IO, int R, bool BWD>
 __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename IO::T* __restrict__ q,
                                                     const typename IO::T* __restrict__ k,
@@ -115,14 +159,18 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
                                                     float* __restrict__ coef, uint16_t* __restrict__ Mo,
                                                     uint16_t* __restrict__ Po, uint16_t* __restrict__ No,
                                                     uint16_t* __restrict__ Kp, uint16_t* __restrict__ Qp) {
+    using T = typename IO::T;
     constexpr int NP = in_parts<IO>(), KJ = R < 32 ? 1 : R / 32;
     constexpr int NY = BWD ? 3 : (NP == 1 ? 2 : 3);
+    constexpr int MAT = DL * CS;
+    constexpr int KB = NP * 4 * KJ * 1024, MB = (BWD ? 3 : 2) * MAT * 4;
+    __shared__ __align__(16) char sm[KB > MB ? KB : MB];
     __shared__ double sG[DL];
     __shared__ float sBeta[DL];
-    __shared__ __align__(16) float sC[DL * CS];
-    __shared__ __align__(16) float sX[DL * CS];
-    __shared__ __align__(16) float sAb[BWD ? DL * CS : 4];
-    const int64_t ch = blockIdx.x;
+    float* sC = reinterpret_cast<float*>(sm);
+    float* sX = sC + MAT;
+    float* sAb = sX + MAT;
+    const int64_t ch = xcd_order(blockIdx.x, gridDim.x);
     const int c = static_cast<int>(ch % d.N);
     const int64_t bh = ch / d.N;
     const int h = static_cast<int>(bh % d.H), b = static_cast<int>(bh / d.H);
@@ -130,10 +178,24 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
     if (L == 0) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
     const int64_t t0 = static_cast<int64_t>(c) * DL;
+    const int hk = h / (d.H / d.HK);
+    // this wave's rows of k and q; rows past the length are read as the last one, then zeroed
+    typedef T raw8 __attribute__((ext_vector_type(8)));
+    raw8 kr[KJ], qr[KJ];
+    {
+        const int t = 16 * w + i, row = t < L ? t : L - 1;
+        const T* kb = k + b * d.ks[0] + (t0 + row) * d.ks[1] + hk * d.ks[2] + (R < 32 ? 8 * (g & 1) : 8 * g);
+        const T* qb = q + b * d.qs[0] + (t0 + row) * d.qs[1] + hk * d.qs[2] + (R < 32 ? 8 * (g & 1) : 8 * g);
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+            kr[j] = *reinterpret_cast<const raw8*>(kb + 32 * j);
+            qr[j] = *reinterpret_cast<const raw8*>(qb + 32 * j);
+        }
+    }
     if (w == 0) {
-        const int64_t at = (static_cast<int64_t>(b) * d.S + t0 + lane) * d.H + h;
-        const float gv = lane < L ? gate[at] : 0.0f;
-        const float bv = lane < L ? beta[at] : 0.0f;
+        const int64_t at = (static_cast<int64_t>(b) * d.S + t0 + (lane < L ? lane : L - 1)) * d.H + h;
+        const float gl = gate[at], bl = beta[at];
+        const float gv = lane < L ? gl : 0.0f, bv = lane < L ? bl : 0.0f;
         double G = gv < kMinLogDecay ? kMinLogDecay : gv;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -150,85 +212,84 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
         if (lane == 0) cf[3 * DL] = exp2_of(tot);
         reinterpret_cast<double*>(cf + DCF)[lane] = G2;
     }
-    const int hk = h / (d.H / d.HK);
-    const typename IO::T* kb = k + b * d.ks[0] + t0 * d.ks[1] + hk * d.ks[2];
-    const typename IO::T* qb = q + b * d.qs[0] + t0 * d.qs[1] + hk * d.qs[2];
-    auto row = [&](const typename IO::T* base, int64_t stride, int tile, int j) {
-        const int t = 16 * tile + i, col = 32 * j + 8 * g;
-        return load_parts8<IO>(base + t * stride + col, t < L && (R >= 32 || col < R));
-    };
-    // wave w: row tile w of K K^T and Q K^T as D[s][t] (lane t = 16 w + i, s = 16 sg + 4 g + v),
-    // or for the backward Q K^T as D[t][s] (lane s = 16 w + i)
-    v4f kk[4], qk[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) kk[s] = qk[s] = zero4();
+    Parts<NP> kw[KJ], qw[KJ];
+    const bool on = 16 * w + i < L && (R >= 32 || g < 2);
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
-        const auto kw = row(kb, d.ks[1], w, j);
-        const auto qw = row(qb, d.qs[1], w, j);
+        kw[j] = parts_of<IO>(kr[j], on);
+        qw[j] = parts_of<IO>(qr[j], on);
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            *reinterpret_cast<b8v*>(sm + ((n * 4 + w) * KJ + j) * 1024 + lane * 16) = kw[j].p[n];
         if constexpr (stage_parts<IO, R>()) {
             if (h == hk * (d.H / d.HK)) {  // one value head writes the parts of its key head
                 const int64_t at = ((static_cast<int64_t>(b) * d.HK + hk) * d.N + c) * (NP * 4 * KJ * DTILE) +
                                    (w * KJ + j) * DTILE + tile_slot(i, g) * 8;
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
-                    *reinterpret_cast<b8v*>(Kp + at + n * (4 * KJ * DTILE)) = kw.p[n];
-                    *reinterpret_cast<b8v*>(Qp + at + n * (4 * KJ * DTILE)) = qw.p[n];
+                    *reinterpret_cast<b8v*>(Kp + at + n * (4 * KJ * DTILE)) = kw[j].p[n];
+                    *reinterpret_cast<b8v*>(Qp + at + n * (4 * KJ * DTILE)) = qw[j].p[n];
                 }
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (s <= w) {
-                const auto ks = row(kb, d.ks[1], s, j);
-                kk[s] = mma(ks, kw, kk[s]);
-                if constexpr (!BWD) qk[s] = mma(ks, qw, qk[s]);
-            }
-            if constexpr (BWD) {
-                if (s >= w) qk[s] = mma(row(qb, d.qs[1], s, j), kw, qk[s]);
             }
         }
     }
     __syncthreads();
-    {
-        const int t = 16 * w + i;
-        const double Gt = sG[t];
-        v4f p[4];
+    // K K^T as D[s][t] (lane token 16 w + i, sources 16 sg + 4 g + v), Q K^T the same way or, for
+    // the backward's transposed operand, as D[t][s] (lane source 16 sg + i)
+    v4f kk[4], qk[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            p[s] = zero4();
-            if (s <= w) {
-                v4f cc, ab;
+    for (int s = 0; s < 4; ++s) kk[s] = qk[s] = zero4();
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int src = 16 * s + 4 * g + v;
-                    const float e = exp2_of(src <= t ? Gt - sG[src] : 0.0);
-                    ab[v] = src < t ? kk[s][v] * e : 0.0f;
-                    cc[v] = ab[v] * sBeta[src];
-                    if constexpr (!BWD) p[s][v] = src <= t ? d.scale * qk[s][v] * e : 0.0f;
-                }
-                *reinterpret_cast<v4f*>(sC + t * CS + 16 * s + 4 * g) = cc;
-                if constexpr (BWD) *reinterpret_cast<v4f*>(sAb + t * CS + 16 * s + 4 * g) = ab;
-            }
-            if constexpr (BWD) {
-                if (s >= w) {
+    for (int s = 0; s < 4; ++s) {
+        if (s <= w) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const int tt = 16 * s + 4 * g + v;  // lane's token t is the source here
-                        p[s][v] = tt >= t ? d.scale * qk[s][v] * exp2_of(sG[tt] - Gt) : 0.0f;
-                    }
-                }
+            for (int j = 0; j < KJ; ++j) {
+                Parts<NP> ks;
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    ks.p[n] = *reinterpret_cast<const b8v*>(sm + ((n * 4 + s) * KJ + j) * 1024 + lane * 16);
+                kk[s] = mma(ks, kw[j], kk[s]);
+                qk[s] = BWD ? mma(qw[j], ks, qk[s]) : mma(ks, qw[j], qk[s]);
             }
         }
-        uint16_t* po = Po + ch * (NY * DTRI * DTILE);
+    }
+    __syncthreads();
+    const int t = 16 * w + i;
+    uint16_t* po = Po + ch * (NY * DTRI * DTILE);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        if (s <= w) {
+            v4f cc, ab;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int src = 16 * s + 4 * g + v;
+                const float e = exp2_of(src <= t ? sG[t] - sG[src] : 0.0);
+                ab[v] = src < t ? kk[s][v] * e : 0.0f;
+                cc[v] = ab[v] * sBeta[src];
+                if constexpr (!BWD) qk[s][v] = src <= t ? d.scale * qk[s][v] * e : 0.0f;
+            }
+            *reinterpret_cast<v4f*>(sC + t * CS + 16 * s + 4 * g) = cc;
+            if constexpr (BWD) {
+                *reinterpret_cast<v4f*>(sAb + t * CS + 16 * s + 4 * g) = ab;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int tt = 16 * w + 4 * g + v, src = 16 * s + i;
+                    qk[s][v] = src <= tt ? d.scale * qk[s][v] * exp2_of(sG[tt] - sG[src]) : 0.0f;
+                }
+                put_half<NY>(po, tri_upper(s, w / 2), lane, w & 1, qk[s]);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if ((w & 1) == 0) put_half<NY>(po, tri_upper(w + 1, w / 2), lane, 0, zero4());  // above the diagonal
+    } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            if (BWD ? j >= w / 2 : j <= w / 2) {
-                const auto pp = split44<NY>(p[2 * j], p[2 * j + 1]);
-                const int tile = BWD ? tri_upper(w, j) : tri_lower(w, j);
+            if (j <= w / 2) {
+                const auto pp = split44<NY>(qk[2 * j], qk[2 * j + 1]);
 #pragma unroll
                 for (int n = 0; n < NY; ++n)
-                    *reinterpret_cast<b8v*>(po + (n * DTRI + tile) * DTILE + lane * 8) = pp.p[n];
+                    *reinterpret_cast<b8v*>(po + (n * DTRI + tri_lower(w, j)) * DTILE + lane * 8) = pp.p[n];
             }
         }
     }
@@ -243,7 +304,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
                 m[hf] = 2 * j + hf <= w
-                            ? *reinterpret_cast<const v4f*>(sX + (16 * w + i) * CS + 32 * j + 16 * hf + 4 * g)
+                            ? *reinterpret_cast<const v4f*>(sX + t * CS + 32 * j + 16 * hf + 4 * g)
                             : zero4();
             const auto mp = split44<3>(m[0], m[1]);
 #pragma unroll
@@ -265,8 +326,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
                         y = tile_mul(sX + 16 * a * CS + 16 * u, sAb + 16 * u * CS + 16 * w, i, g, y);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const int t = 16 * a + 4 * g + v;
-                    nt[a][v] = (t == 16 * w + i ? 1.0f : 0.0f) - sBeta[t] * y[v];
+                    const int row = 16 * a + 4 * g + v;
+                    nt[a][v] = (row == t ? 1.0f : 0.0f) - sBeta[row] * y[v];
                 }
             }
         }
@@ -289,29 +350,38 @@ enum ScanMode { kOutputs, kRecord, kReverse };
 // Loading waves of a scan workgroup: a wave has at most 63 loads under way, and a chunk of fp32
 // operands is twice that.
 template <class IO>
-__host__ __device__ constexpr int scan_loaders() { return in_parts<IO>() == 1 ? 1 : 2; }
+__host__ __device__ constexpr int scan_loaders() { return in_parts<IO>() == 1 ? 2 : 4; }
 
-// One scan workgroup: W waves that compute, each 16 value columns of one head, and NL that load.
+// One scan workgroup: W tiles of 16 value columns of one head, each computed by a team of T waves
+// that share out the state's r axis, and NL waves that load.
+//
+// The chain of products from one chunk's state to the next bounds the scan, not their number: a
+// team shortens it.  Each of its waves keeps r / T of the state, multiplies that part of K and Q,
+// and the team adds the parts of K H^T through LDS, in the same order in every wave, so that all
+// of them continue with the same R, E and U.
+//
 // The loading waves bring what a chunk needs into LDS without passing registers, a chunk ahead,
 // into the buffer that its predecessor has just left: the phases of a chunk are ordered so that
 // between the last read of a buffer and the first read of its next contents lies another phase's
 // matrix work.  They count their own loads; the computing waves meet them at barriers only.
-template <class IO, int R, int W, ScanMode MODE>
+template <class IO, int R, int W, int TM, ScanMode MODE>
 struct Scan {
     using T = typename IO::T;
-    static constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, KJ = RP / 32, RT = RP / 16;
+    static constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, KJ = RP / 32;
+    static constexpr int JW = KJ / TM, RT = RP / 16 / TM;  // steps of r and state tiles of one wave
     static constexpr bool PARTS = stage_parts<IO, R>();
     // parts of y's operands: an output rounded to bf16 needs no third part (2^-17 of it)
     static constexpr int NQ = MODE == kOutputs && NP == 1 ? 2 : 3;
     static constexpr int QT = 4 * KJ;  // tiles per part
-    static constexpr int NL = scan_loaders<IO>();
+    static constexpr int NL = scan_loaders<IO>(), CW = W * TM;
+    static constexpr int TT = 4 / TM;  // token tiles that a wave finishes for its team
     // LDS, bytes
     static constexpr int KBYTES = NP * QT * 1024, KBUFS = MODE == kRecord ? 2 : 1;
     static constexpr int QBYTES = MODE == kRecord ? 0 : KBYTES;
     static constexpr int MBYTES = 3 * DTRI * 1024, PBYTES = MODE == kRecord ? 0 : NQ * DTRI * 1024;
     static constexpr int VBYTES = DL * 16 * W * sizeof(T);
     static constexpr int oK = 0, oQ = oK + KBUFS * KBYTES, oM = oQ + QBYTES, oP = oM + MBYTES, oV = oP + PBYTES,
-                         oC = oV + VBYTES, LDS = oC + 2 * 4 * DCF;
+                         oC = oV + VBYTES, oX = oC + 2 * 4 * DCF, LDS = oX + (TM > 1 ? CW * 4096 : 0);
     // loads of one loading wave
     static constexpr int per(int n) { return (n + NL - 1) / NL; }
     static constexpr int nK = per(NP * QT), nQ = nK, nM = per(3 * DTRI), nP = per(NQ * DTRI), nV = per(VBYTES / 1024),
@@ -320,7 +390,7 @@ struct Scan {
     char* sm;
     const DeltaShape& d;
     const DeltaScan<T>& a;
-    int lane, w, i, g, p0, pw, h, b, hk, chunks, len;
+    int lane, w, tm, i, g, pt, p0, pw, h, b, hk, chunks, len;
     int64_t bh;
 
     __device__ Scan(char* smem, const DeltaShape& dd, const DeltaScan<T>& aa, int64_t blk) : sm(smem), d(dd), a(aa) {
@@ -328,9 +398,11 @@ struct Scan {
         w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         i = lane & 15;
         g = lane >> 4;
+        pt = w / TM;  // tile of the workgroup
+        tm = w % TM;  // place in its team
         const int pbs = d.P / (16 * W);
         pw = static_cast<int>(blk % pbs) * 16 * W;  // the workgroup's first column
-        p0 = pw + 16 * w;                           // the wave's
+        p0 = pw + 16 * pt;                          // the team's
         bh = blk / pbs;
         h = static_cast<int>(bh % d.H);
         b = static_cast<int>(bh / d.H);
@@ -341,7 +413,7 @@ struct Scan {
 
     // -------------------------------------------------------------- loads into LDS
     __device__ int unit(int m, int n) const {  // this loading wave's m-th of n: each loads as often
-        const int t = w - W + m * NL;
+        const int t = w - CW + m * NL;
         return n % NL == 0 || t < n ? t : n - 1;
     }
     template <int N>  // N kilobytes, as they are
@@ -366,7 +438,7 @@ struct Scan {
                 const T* src = base + (row < last ? row : last) * stride[1];
 #pragma unroll
                 for (int j = 0; j < KJ; ++j)
-                    if (NL == 1 || (tau * KJ + j) % NL == w - W) load_to_lds(src + 32 * j, dst + (tau * KJ + j) * 1024);
+                    if (NL == 1 || (tau * KJ + j) % NL == w - CW) load_to_lds(src + 32 * j, dst + (tau * KJ + j) * 1024);
             }
         }
     }
@@ -387,11 +459,13 @@ struct Scan {
     }
 
     // -------------------------------------------------------------- operands
+    // j, rho: of this wave's share of r
     __device__ Parts<NP> row_op(int base, int tau, int j) const {  // rows: tokens 16 tau + i
         Parts<NP> o;
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-            o.p[n] = *reinterpret_cast<const b8v*>(sm + base + (n * QT + tau * KJ + j) * 1024 + tile_slot(i, g) * 16);
+            o.p[n] = *reinterpret_cast<const b8v*>(sm + base + (n * QT + tau * KJ + tm * JW + j) * 1024 +
+                                                    tile_slot(i, g) * 16);
         return o;
     }
     // Rows r = 32 (rho / 2) + 8 (i / 4) + 4 (rho % 2) + i % 4 of the transposed matrix, k over the
@@ -399,7 +473,7 @@ struct Scan {
     // r = 32 (rho / 2) + 8 g + 4 (rho % 2) + v: two state tiles hold eight consecutive r per lane.
     __device__ Parts<NP> col_op(int base, int rho, int j) const {
         Parts<NP> o;
-        const int at = base + (2 * j * KJ + (rho >> 1)) * 1024 + tile_slot(4 * g + (i >> 2), i & 3) * 16 + (rho & 1) * 8;
+        const int at = base + (2 * j * KJ + tm * JW + (rho >> 1)) * 1024 + tile_slot(4 * g + (i >> 2), i & 3) * 16 + (rho & 1) * 8;
 #pragma unroll
         for (int n = 0; n < NP; ++n)
             o.p[n] = join8(lds_col4(reinterpret_cast<const uint16_t*>(sm + at + n * QT * 1024)),
@@ -414,14 +488,17 @@ struct Scan {
             o.p[n] = *reinterpret_cast<const b8v*>(sm + base + (n * DTRI + tile) * 1024 + lane * 16);
         return o;
     }
+    __device__ b8v tri_part(int base, int n, int tile) const {
+        return *reinterpret_cast<const b8v*>(sm + base + (n * DTRI + tile) * 1024 + lane * 16);
+    }
     // v or dy in result layout: tokens 16 t + 4 g + v of value column p0 + i
     __device__ v4f value(int t) const {
         if constexpr (sizeof(T) == 2) {
             const s4 x = lds_col4(reinterpret_cast<const uint16_t*>(sm + oV) + (16 * t + 4 * g + (i >> 2)) * (16 * W) +
-                                  16 * w + 4 * (i & 3));
+                                  16 * pt + 4 * (i & 3));
             return v4f{bf16_to_f32(x[0]), bf16_to_f32(x[1]), bf16_to_f32(x[2]), bf16_to_f32(x[3])};
         } else {
-            const float* x = reinterpret_cast<const float*>(sm + oV) + (16 * t + 4 * g) * (16 * W) + 16 * w + i;
+            const float* x = reinterpret_cast<const float*>(sm + oV) + (16 * t + 4 * g) * (16 * W) + 16 * pt + i;
             return v4f{x[0], x[16 * W], x[32 * W], x[48 * W]};
         }
     }
@@ -429,17 +506,18 @@ struct Scan {
     __device__ static v4f at4(const float* p) { return *reinterpret_cast<const v4f*>(p); }
 
     // -------------------------------------------------------------- states
+    __device__ int row_of(int rho) const { return 32 * (tm * JW + (rho >> 1)) + 8 * g + 4 * (rho & 1); }
     __device__ void load_state(v4f (&s)[RT], const float* src) const {
 #pragma unroll
         for (int rho = 0; rho < RT; ++rho) {
-            const int r = 32 * (rho >> 1) + 8 * g + 4 * (rho & 1);
+            const int r = row_of(rho);
             s[rho] = src && r < R ? at4(src + (bh * d.P + p0 + i) * R + r) : zero4();
         }
     }
     __device__ void store_state(const v4f (&s)[RT], float* dst) const {
 #pragma unroll
         for (int rho = 0; rho < RT; ++rho) {
-            const int r = 32 * (rho >> 1) + 8 * g + 4 * (rho & 1);
+            const int r = row_of(rho);
             if (dst && r < R) *reinterpret_cast<v4f*>(dst + (bh * d.P + p0 + i) * R + r) = s[rho];
         }
     }
@@ -448,58 +526,166 @@ struct Scan {
         float* o = dst + (bh * d.N + c) * (static_cast<int64_t>(R) * d.P) + p0 + i;
 #pragma unroll
         for (int rho = 0; rho < RT; ++rho) {
-            const int r = 32 * (rho >> 1) + 8 * g + 4 * (rho & 1);
+            const int r = row_of(rho);
             if (r < R) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) o[(r + v) * d.P] = s[rho][v];
             }
         }
     }
-    __device__ void record_rows(const v4f (&x)[4], float* dst, int c) const {
-        float* o = dst + (bh * d.N + c) * (static_cast<int64_t>(DL) * d.P) + p0 + i;
+    __device__ v4f own(const v4f (&x)[4], int t) const {  // x[tm TT + t]
+        v4f o = x[t];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int m = 1; m < TM; ++m)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) o[(16 * t + 4 * g + v) * d.P] = x[t][v];
+            for (int v = 0; v < 4; ++v) o[v] = tm == m ? x[m * TT + t][v] : o[v];
+        return o;
+    }
+    __device__ void record_rows(const v4f (&x)[4], float* dst, int c) const {  // this wave's token tiles
+        float* o = dst + ((bh * d.N + c) * DL + 16 * tm * TT) * static_cast<int64_t>(d.P) + p0 + i;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const v4f r = own(x, t);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[(16 * t + 4 * g + v) * d.P] = r[v];
+        }
+    }
+    // c <- c + X s^T (SWAP: its transpose) over this wave's share of r, X = k or q in LDS, from the
+    // state's parts, or parts made on the way (MAKE): a step's operands are read, and the next
+    // step's parts made, while the matrix cores are at the step before.
+    template <bool SWAP, int N, bool MAKE>
+    __device__ void rows_product(v4f (&c)[4], int base, Parts<3> (&sp)[JW], const v4f (&s)[RT]) const {
+        Parts<NP> op[2][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) op[0][t] = row_op(base, t, 0);
+        if constexpr (MAKE) sp[0] = split44<3>(s[0], s[1]);
+#pragma unroll
+        for (int j = 0; j < JW; ++j) {
+            if (j + 1 < JW) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) op[(j + 1) & 1][t] = row_op(base, t, j + 1);
+            }
+            fence();
+            Parts<N> sn;
+#pragma unroll
+            for (int n = 0; n < N; ++n) sn.p[n] = sp[j].p[n];
+            if constexpr (SWAP)
+                mma_b(c, sn, op[j & 1]);
+            else
+                mma_a(c, op[j & 1], sn);
+            if (MAKE && j + 1 < JW) {
+                sp[j + 1] = split44<3>(s[2 * j + 2], s[2 * j + 3]);
+                mix<4 * terms(NP, N), 176 / (4 * terms(NP, N)) / 4 + 1>();
+            }
+            fence();
+        }
+    }
+    static constexpr int terms(int na, int nb) {
+        int n = 0;
+        for (int s = 0; s < (na > nb ? na : nb); ++s)
+            for (int k = 0; k < na; ++k) n += s - k >= 0 && s - k < nb;
+        return n;
+    }
+    // Instructions do not move across; one MFMA, then VN others of the vector unit, N times.
+    __device__ static void fence() { __builtin_amdgcn_sched_barrier(0); }
+    template <int N, int VN>
+    __device__ static void mix() {
+#pragma unroll
+        for (int m = 0; m < N; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, VN, 0);
+        }
     }
     // s <- s + X^T z over the chunk's tokens, X = k or q in LDS, z in result layout
+    static constexpr int G = RT < 4 ? RT : 4;  // state tiles at a time
+    __device__ void col_ops(Parts<NP> (&op)[G], int base, int step) const {  // step: j, then tiles
+#pragma unroll
+        for (int m = 0; m < G; ++m) op[m] = col_op(base, step % (RT / G) * G + m, step / (RT / G));
+    }
     __device__ void add_outer(v4f (&s)[RT], int base, const v4f (&z)[4]) const {
+        constexpr int STEPS = 2 * (RT / G);
+        Parts<NP> op[2][G];
+        col_ops(op[0], base, 0);
+        Parts<3> zp[2];
+        zp[0] = split44<3>(z[0], z[1]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const auto zp = split44<3>(z[2 * j], z[2 * j + 1]);
-            constexpr int G = RT < 4 ? RT : 4;
+        for (int k = 0; k < STEPS; ++k) {
+            if (k + 1 < STEPS) col_ops(op[(k + 1) & 1], base, k + 1);
+            fence();
+            mma_a(*reinterpret_cast<v4f(*)[G]>(&s[k % (RT / G) * G]), op[k & 1], zp[k / (RT / G)]);
+            if (k == 0) {
+                zp[1] = split44<3>(z[2], z[3]);
+                mix<G * terms(NP, 3), 48 / (G * terms(NP, 3)) + 1>();
+            }
+            fence();
+        }
+    }
+    // c <- c + A x for a triangular operand in LDS, x in result layout
+    template <bool LOWER>
+    __device__ void tri_product(v4f (&c)[4], int base, const v4f (&x)[4]) const {
+        constexpr int jf = LOWER ? 0 : 1, js = 1 - jf, t0 = LOWER ? 2 : 0;  // the full step, the half one
+        Parts<3> a4[4], a2[2];
 #pragma unroll
-            for (int r0 = 0; r0 < RT; r0 += G) {
-                Parts<NP> op[G];
+        for (int t = 0; t < 4; ++t) a4[t] = tri_op<3>(base, LOWER ? tri_lower(t, jf) : tri_upper(t, jf));
+        const auto x0 = split44<3>(x[2 * jf], x[2 * jf + 1]);
 #pragma unroll
-                for (int m = 0; m < G; ++m) op[m] = col_op(base, r0 + m, j);
-                mma_a(*reinterpret_cast<v4f(*)[G]>(&s[r0]), op, zp);
+        for (int t = 0; t < 2; ++t) a2[t] = tri_op<3>(base, LOWER ? tri_lower(t0 + t, js) : tri_upper(t0 + t, js));
+        fence();
+        mma_a(c, a4, x0);
+        const auto x1 = split44<3>(x[2 * js], x[2 * js + 1]);
+        mix<16, 3>();
+        fence();
+        mma_a(*reinterpret_cast<v4f(*)[2]>(&c[t0]), a2, x1);
+    }
+
+    // -------------------------------------------------------------- a team's sums
+    __device__ v4f* share(int member, int t) const {
+        return reinterpret_cast<v4f*>(sm + oX + (pt * TM + member) * 4096 + t * 1024) + lane;
+    }
+    __device__ void team_sum(v4f (&x)[4]) const {  // the sum of the members' x, in all of them
+        if constexpr (TM > 1) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) *share(tm, t) = x[t];
+            meet();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                x[t] = *share(0, t);
+#pragma unroll
+                for (int m = 1; m < TM; ++m) x[t] += *share(m, t);
             }
         }
     }
-    // c <- c + A x for a triangular operand in LDS
-    template <bool LOWER, int N, int NB>
-    __device__ void tri_mul(v4f (&c)[4], int base, int j, const Parts<NB>& x) const {
-        constexpr int all = 4;
-        if (LOWER == (j == 0)) {
-            Parts<N> op[all];
+
+    // y <- y + P u for this wave's token tiles
+    __device__ void intra(v4f (&y)[TT], const v4f (&u)[4]) const {
+        Parts<NQ> op[2][TT];
+        const bool two = TM == 1 || tm >= TM / 2;  // tiles whose rows reach the second step
 #pragma unroll
-            for (int t = 0; t < all; ++t) op[t] = tri_op<N>(base, LOWER ? tri_lower(t, j) : tri_upper(t, j));
-            mma_a(c, op, x);
-        } else {
-            constexpr int t0 = LOWER ? 2 : 0;
-            Parts<N> op[2];
+        for (int t = 0; t < TT; ++t) op[0][t] = tri_op<NQ>(oP, tri_lower(tm * TT + t, 0));
+        if (two) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) op[t] = tri_op<N>(base, LOWER ? tri_lower(t0 + t, j) : tri_upper(t0 + t, j));
-            mma_a(*reinterpret_cast<v4f(*)[2]>(&c[t0]), op, x);
+            for (int t = TM == 1 ? 2 : 0; t < TT; ++t) op[1][t] = tri_op<NQ>(oP, tri_lower(tm * TT + t, 1));
+        }
+        const auto u0 = split44<NQ>(u[0], u[1]);
+        fence();
+        mma_b(y, u0, op[0]);
+        if (two) {
+            const auto u1 = split44<NQ>(u[2], u[3]);
+            if constexpr (TM == 1) {
+                mix<4 * terms(NQ, NQ), 3>();
+                fence();
+                mma_b(*reinterpret_cast<v4f(*)[2]>(&y[TT / 2]), u1, *reinterpret_cast<const Parts<NQ>(*)[2]>(&op[1][TT / 2]));
+            } else {
+                mma_b(y, u1, op[1]);
+            }
         }
     }
 
     // -------------------------------------------------------------- the forward recurrence
-    __device__ void store_y(const v4f (&y)[4], int c) const {  // D[p][t]: token 16 t + i, columns 4 g + v
+    __device__ void store_y(const v4f (&y)[TT], int c) const {  // D[p][t]: token 16 t + i, columns 4 g + v
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int64_t tok = static_cast<int64_t>(c) * DL + 16 * t + i;
+        for (int t = 0; t < TT; ++t) {
+            const int64_t tok = static_cast<int64_t>(c) * DL + 16 * (tm * TT + t) + i;
             if (tok < d.S) io<IO>::st4(a.y, ((b * static_cast<int64_t>(d.S) + tok) * d.H + h) * d.P + p0 + 4 * g, y[t]);
         }
     }
@@ -523,6 +709,7 @@ struct Scan {
                     load_qk(oQ, a.q, a.Qp, d.qs, c + 1);
                     load_coef(c + 1, c + 1);
                 }
+                if constexpr (TM > 1) wait_barrier<63>();
                 wait_barrier<63>();
                 if (more) {
                     m(c + 1);
@@ -540,6 +727,7 @@ struct Scan {
                 const bool more = c + 1 < chunks;
                 wait_barrier<0>();
                 if (more) load_qk(oK + ((c + 1) & 1) * KBYTES, a.k, a.Kp, d.ks, c + 1);
+                if constexpr (TM > 1) wait_barrier<63>();
                 wait_barrier<63>();
                 if (more) {
                     m(c + 1);
@@ -550,7 +738,7 @@ struct Scan {
     }
 
     __device__ void forward() const {
-        if (w >= W) {
+        if (w >= CW) {
             if (chunks > 0) load_forward();
             return;
         }
@@ -562,36 +750,21 @@ struct Scan {
             v4f x[4], y[4], u[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) x[t] = y[t] = u[t] = zero4();
-            Parts<3> sp[KJ];
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) sp[j] = split44<3>(s[2 * j], s[2 * j + 1]);
+            Parts<3> sp[JW];
             meet();  // outputs: q and the coefficients are here, P is free; else everything is here
-            if constexpr (MODE == kOutputs) {
-#pragma unroll
-                for (int j = 0; j < KJ; ++j) {
-                    Parts<NP> op[4];
-                    Parts<NQ> sy;
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) sy.p[n] = sp[j].p[n];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) op[t] = row_op(oQ, t, j);
-                    mma_b(y, sy, op);
-                }
-                meet();  // M, v and k are here, q is free
-            }
             const float* cf = coef(c);
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) {
-                Parts<NP> op[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) op[t] = row_op(kb, t, j);
-                mma_a(x, op, sp[j]);
+            if constexpr (MODE == kOutputs) {
+                rows_product<true, NQ, true>(y, oQ, sp, s);
+                meet();  // M, v and k are here, q is free
+                rows_product<false, 3, false>(x, kb, sp, s);
+            } else {
+                rows_product<false, 3, true>(x, kb, sp, s);
             }
+            team_sum(x);
             // R = v - e^G x, E = M R (value column p0 + i, tokens 16 t + 4 g + v)
 #pragma unroll
             for (int t = 0; t < 4; ++t) x[t] = value(t) - at4(cf + 16 * t + 4 * g) * x[t];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) tri_mul<true, 3>(u, oM, j, split44<3>(x[2 * j], x[2 * j + 1]));
+            tri_product<true>(u, oM, x);
             v4f z[4];
             meet();  // M and v are free
             if constexpr (MODE == kRecord) {
@@ -606,35 +779,52 @@ struct Scan {
             const float eL = cf[3 * DL];
 #pragma unroll
             for (int r = 0; r < RT; ++r) s[r] *= eL;
+            if constexpr (MODE == kOutputs && TM > 1) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) *share(tm, t) = y[t];
+            }
             add_outer(s, kb, z);
             if constexpr (MODE == kOutputs) {
-                meet();  // P is here, k is free
+                meet();  // P is here, k is free, the team's parts of q H are written
+                v4f yo[TT];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) y[t] *= d.scale * cf[16 * t + i];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const auto up = split44<NQ>(u[2 * j], u[2 * j + 1]);
-                    if (j == 0) {
-                        Parts<NQ> op[4];
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) op[t] = tri_op<NQ>(oP, tri_lower(t, 0));
-                        mma_b(y, up, op);
+                for (int t = 0; t < TT; ++t) {
+                    if constexpr (TM == 1) {
+                        yo[t] = y[t];
                     } else {
-                        Parts<NQ> op[2];
+                        yo[t] = *share(0, tm * TT + t);
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) op[t] = tri_op<NQ>(oP, tri_lower(2 + t, 1));
-                        mma_b(*reinterpret_cast<v4f(*)[2]>(&y[2]), up, op);
+                        for (int m = 1; m < TM; ++m) yo[t] += *share(m, tm * TT + t);
                     }
+                    yo[t] *= d.scale * cf[16 * (tm * TT + t) + i];
                 }
-                store_y(y, c);
+                intra(yo, u);
+                store_y(yo, c);
             }
             mfma_settle();
         }
         if constexpr (MODE == kOutputs) {
             store_state(s, a.final_state);
-            const v4f zero[4] = {zero4(), zero4(), zero4(), zero4()};
+            v4f zero[TT];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) zero[t] = zero4();
             for (; c < d.N; ++c) store_y(zero, c);  // chunks past the row's length
         }
+    }
+
+    // u <- u + P^T dy for step j of this wave's token tiles
+    __device__ void intra_t(v4f (&u)[TT], const Parts<NP>& y, int j) const {
+#pragma unroll
+        for (int s0 = 2; s0 >= 0; --s0)
+#pragma unroll
+            for (int n = 0; n <= s0; ++n)
+                if (s0 - n < NP)
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        if (TM == 1 && j < t / 2) continue;
+                        const int tile = tri_upper(tm * TT + t, j);
+                        u[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tri_part(oP, n, tile), y.p[s0 - n], u[t], 0, 0, 0);
+                    }
     }
 
     // -------------------------------------------------------------- the reverse recurrence
@@ -653,6 +843,7 @@ struct Scan {
             wait_barrier<nM + nK>();  // P^T, q, dy and the coefficients
             wait_barrier<0>();        // N^T and k
             if (c > 0) front(c - 1);
+            if constexpr (TM > 1) wait_barrier<63>();
             wait_barrier<63>();
             if (c > 0) copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + c - 1) * (3 * DTRI * DTILE));
             wait_barrier<63>();
@@ -661,7 +852,7 @@ struct Scan {
     }
 
     __device__ void reverse() const {
-        if (w >= W) {
+        if (w >= CW) {
             if (chunks > 0) load_reverse();
             return;
         }
@@ -675,32 +866,35 @@ struct Scan {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 dy[t] = value(t);
-                u[t] = x[t] = zero4();
+                x[t] = zero4();
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r) gq[r] = zero4();
-            // dU = P^T dy + tail (K dH^T)
+            // dU = P^T dy + tail (K dH^T): of the first term, this wave's token tiles
+            v4f pu[TT];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) tri_mul<false, 3>(u, oP, j, split44<NP>(dy[2 * j], dy[2 * j + 1]));
+            for (int t = 0; t < TT; ++t) pu[t] = zero4();
+            if (TM == 1 || tm < (TM + 1) / 2) intra_t(pu, split44<NP>(dy[0], dy[1]), 0);
+            intra_t(pu, split44<NP>(dy[2], dy[3]), 1);
 #pragma unroll
             for (int t = 0; t < 4; ++t) dy[t] *= d.scale * at4(cf + 16 * t + 4 * g);
             add_outer(gq, oQ, dy);
             meet();  // N^T and k are here, P^T, q and dy are free
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) {
-                const auto sp = split44<3>(s[2 * j], s[2 * j + 1]);
-                Parts<NP> op[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) op[t] = row_op(oK, t, j);
-                mma_a(x, op, sp);
-            }
+            Parts<3> sp[JW];
+            rows_product<false, 3, true>(x, oK, sp, s);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                u[t] += at4(cf + DL + 16 * t + 4 * g) * x[t];
+                u[t] = at4(cf + DL + 16 * t + 4 * g) * x[t];
+                if (TM == 1) {
+                    u[t] += pu[t % TT];
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) u[t][v] += t / TT == tm ? pu[t % TT][v] : 0.0f;
+                }
                 x[t] = zero4();
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) tri_mul<false, 3>(x, oM, j, split44<3>(u[2 * j], u[2 * j + 1]));
+            team_sum(u);
+            tri_product<false>(x, oM, u);
             meet();  // N^T is free
             record_rows(x, a.dZ, c);
 #pragma unroll
@@ -719,28 +913,23 @@ struct Scan {
     __device__ static void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 };
 
-// The eight XCDs take workgroups in turn and each has its own L2: give each a consecutive run of
-// the work, so that the columns and value heads that read the same keys meet in one.
-__device__ __forceinline__ int64_t xcd_order(int64_t blk, int64_t n) {
-    const int64_t x = blk % 8, q = n / 8, rem = n % 8;
-    return x * q + (x < rem ? x : rem) + blk / 8;
-}
-
 }  // namespace
 
-template <class IO, int R, int W>
-__global__ __launch_bounds__(64 * (W + scan_loaders<IO>()), 2) void k_delta_scan(DeltaShape d, DeltaScan<typename IO::T> a) {
-    using S = Scan<IO, R, W, kOutputs>;
+template <class IO, int R, int W, int TM>
+__global__ __launch_bounds__(64 * (W * TM + scan_loaders<IO>()), 2) void k_delta_scan(DeltaShape d,
+                                                                                   DeltaScan<typename IO::T> a) {
+    using S = Scan<IO, R, W, TM, kOutputs>;
     __shared__ __align__(16) char sm[S::LDS];
     S(sm, d, a, xcd_order(blockIdx.x, gridDim.x)).forward();
 }
 
 // Both recurrences of the backward, in alternating workgroups: one recomputes the entry states
 // and E, the other runs the reverse.
-template <class IO, int R, int W>
-__global__ __launch_bounds__(64 * (W + scan_loaders<IO>()), 2) void k_delta_states(DeltaShape d, DeltaScan<typename IO::T> a) {
-    using F = Scan<IO, R, W, kRecord>;
-    using B = Scan<IO, R, W, kReverse>;
+template <class IO, int R, int W, int TM>
+__global__ __launch_bounds__(64 * (W * TM + scan_loaders<IO>()), 2) void k_delta_states(DeltaShape d,
+                                                                                     DeltaScan<typename IO::T> a) {
+    using F = Scan<IO, R, W, TM, kRecord>;
+    using B = Scan<IO, R, W, TM, kReverse>;
     __shared__ __align__(16) char sm[F::LDS > B::LDS ? F::LDS : B::LDS];
     const int64_t blk = xcd_order(blockIdx.x, gridDim.x);
     if (blk & 1)
@@ -791,27 +980,34 @@ hipError_t prep_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t
     return hipGetLastError();
 }
 
-template <class IO, int R, int W>
+template <class IO, int R, int W, int TM>
 hipError_t scan_w(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
-    constexpr int NTHR = 64 * (W + scan_loaders<IO>());
+    constexpr int NTHR = 64 * (W * TM + scan_loaders<IO>());
     const auto a = typed<IO>(f);
     const int64_t wgs = static_cast<int64_t>(d.B) * d.H * (d.P / (16 * W));
     if (bwd)
-        k_delta_states<IO, R, W><<<dim3(static_cast<unsigned>(2 * wgs)), NTHR, 0, st>>>(d, a);
+        k_delta_states<IO, R, W, TM><<<dim3(static_cast<unsigned>(2 * wgs)), NTHR, 0, st>>>(d, a);
     else
-        k_delta_scan<IO, R, W><<<dim3(static_cast<unsigned>(wgs)), NTHR, 0, st>>>(d, a);
+        k_delta_scan<IO, R, W, TM><<<dim3(static_cast<unsigned>(wgs)), NTHR, 0, st>>>(d, a);
     return hipGetLastError();
 }
 
 template <class IO, int R>
 hipError_t scan_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
-    switch (d.P) {
-        case 16: return scan_w<IO, R, 1>(d, f, bwd, st);
-        case 32: return scan_w<IO, R, 2>(d, f, bwd, st);
-        case 64:
-        case 128: return scan_w<IO, R, 4>(d, f, bwd, st);
-        default: return hipErrorInvalidValue;
+    constexpr int KJ = R < 32 ? 1 : R / 32;
+    const int64_t tiles = static_cast<int64_t>(d.B) * d.H * (d.P / 16) * (bwd ? 2 : 1);
+    int W = tiles <= 256 || d.P < 32 ? 1 : tiles <= 512 || d.P < 64 ? 2 : 4, TM = W <= 2 && KJ >= 2 ? 2 : 1;
+    // scan config
+    if constexpr (KJ >= 2) switch (10 * W + TM) {
+        case 12: return scan_w<IO, R, 1, 2>(d, f, bwd, st);
+        case 22: return scan_w<IO, R, 2, 2>(d, f, bwd, st);
+        case 41: return scan_w<IO, R, 4, 1>(d, f, bwd, st);
+    } else switch (W) {
+        case 1: return scan_w<IO, R, 1, 1>(d, f, bwd, st);
+        case 2: return scan_w<IO, R, 2, 1>(d, f, bwd, st);
+        case 4: return scan_w<IO, R, 4, 1>(d, f, bwd, st);
     }
+    return hipErrorInvalidValue;
 }
 
 template <class IO>
