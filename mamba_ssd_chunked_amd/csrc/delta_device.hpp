@@ -189,4 +189,20 @@ __device__ __forceinline__ Parts<in_parts<IO>()> load_parts8(const typename IO::
     return o;
 }
 
+// Eight io values as bf16 parts, zeros where !on.
+template <class IO, class V>
+__device__ __forceinline__ Parts<in_parts<IO>()> parts_of(const V& x, bool on) {
+    Parts<in_parts<IO>()> o;
+    if constexpr (in_parts<IO>() == 1) {
+        uint4 w = __builtin_bit_cast(uint4, x);
+        if (!on) w = make_uint4(0, 0, 0, 0);
+        o.p[0] = __builtin_bit_cast(b8v, w);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = on ? x[e] : 0.0f;
+        o = split8<3>(f);
+    }
+    return o;
+}
 }  // namespace ssd

@@ -49,22 +49,6 @@ __device__ __forceinline__ int64_t xcd_order(int64_t blk, int64_t n) {
     return x * q + (x < rem ? x : rem) + blk / 8;
 }
 
-// Eight io values as bf16 parts, zeros where !on.
-template <class IO, class V>
-__device__ __forceinline__ Parts<in_parts<IO>()> parts_of(const V& x, bool on) {
-    Parts<in_parts<IO>()> o;
-    if constexpr (in_parts<IO>() == 1) {
-        uint4 w = __builtin_bit_cast(uint4, x);
-        if (!on) w = make_uint4(0, 0, 0, 0);
-        o.p[0] = __builtin_bit_cast(b8v, w);
-    } else {
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = on ? x[e] : 0.0f;
-        o = split8<3>(f);
-    }
-    return o;
-}
 // Half a lane's slots of an operand tile (four values) as N parts.
 template <int N>
 __device__ __forceinline__ void put_half(uint16_t* dst, int tile, int lane, int half, v4f x) {
@@ -923,19 +907,20 @@ __global__ __launch_bounds__(64 * (W * TM + scan_loaders<IO>()), 2) void k_delta
     S(sm, d, a, xcd_order(blockIdx.x, gridDim.x)).forward();
 }
 
-// Both recurrences of the backward, in alternating workgroups: one recomputes the entry states
-// and E, the other runs the reverse.
+// Both recurrences of the backward: the first half of the workgroups run the reverse, which takes
+// about twice as long, the second half recompute the entry states and E.  Started last, the short
+// ones fill in where the chip does not hold all of them at once.
 template <class IO, int R, int W, int TM>
 __global__ __launch_bounds__(64 * (W * TM + scan_loaders<IO>()), 2) void k_delta_states(DeltaShape d,
                                                                                      DeltaScan<typename IO::T> a) {
     using F = Scan<IO, R, W, TM, kRecord>;
     using B = Scan<IO, R, W, TM, kReverse>;
     __shared__ __align__(16) char sm[F::LDS > B::LDS ? F::LDS : B::LDS];
-    const int64_t blk = xcd_order(blockIdx.x, gridDim.x);
-    if (blk & 1)
-        B(sm, d, a, blk >> 1).reverse();
+    const int64_t half = gridDim.x / 2;
+    if (blockIdx.x < half)
+        B(sm, d, a, xcd_order(blockIdx.x, half)).reverse();
     else
-        F(sm, d, a, blk >> 1).forward();
+        F(sm, d, a, xcd_order(blockIdx.x - half, half)).forward();
 }
 
 namespace {
@@ -995,8 +980,11 @@ hipError_t scan_w(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t
 template <class IO, int R>
 hipError_t scan_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
     constexpr int KJ = R < 32 ? 1 : R / 32;
-    const int64_t tiles = static_cast<int64_t>(d.B) * d.H * (d.P / 16) * (bwd ? 2 : 1);
-    int W = tiles <= 256 || d.P < 32 ? 1 : tiles <= 512 || d.P < 64 ? 2 : 4, TM = W <= 2 && KJ >= 2 ? 2 : 1;
+    // the fewest columns per workgroup with which the workgroups still find a CU each; in fp32,
+    // where a chunk is mostly matrix work, two rounds of teams of two also beat one of single waves
+    const int64_t tiles = static_cast<int64_t>(d.B) * d.H * (d.P / 16), all = bwd ? 2 * tiles : tiles;
+    const int W = all <= 256 || d.P < 32 ? 1 : (in_parts<IO>() == 3 ? tiles : all) <= 512 || d.P < 64 ? 2 : 4;
+    const int TM = W <= 2 && KJ >= 2 ? 2 : 1;
     // scan config
     if constexpr (KJ >= 2) switch (10 * W + TM) {
         case 12: return scan_w<IO, R, 1, 2>(d, f, bwd, st);

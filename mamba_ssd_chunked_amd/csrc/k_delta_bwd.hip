@@ -16,6 +16,8 @@
 // head are added up in its registers, in order.  Value columns go through LDS 32 at a time; a
 // wave owns one 16-row tile of r and its tiles of tokens, so H and dH are read once, straight
 // into operand registers.
+#include <type_traits>
+
 #include "delta_device.hpp"
 #include "ssd_launch.hpp"
 
@@ -39,6 +41,66 @@ __device__ __forceinline__ void store_parts4(uint16_t* dst, int part_stride, v4f
             x -= v4f{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
     }
+}
+template <int N, int C>
+__device__ __forceinline__ void store_parts(uint16_t* dst, int part_stride, const float (&x)[C]) {
+    if constexpr (C == 4) {
+        store_parts4<N>(dst, part_stride, v4f{x[0], x[1], x[2], x[3]});
+    } else {
+        float a = x[0], b = x[1];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint32_t w = f32x2_to_bf16x2(a, b);
+            *reinterpret_cast<uint32_t*>(dst + n * part_stride) = w;
+            if (n + 1 < N) {
+                a -= __uint_as_float(w << 16);
+                b -= __uint_as_float(w & 0xffff0000u);
+            }
+        }
+    }
+}
+// C (2 or 4) consecutive values.
+template <int C, class V>
+__device__ __forceinline__ void load_row(const V* p, float (&x)[C]) {
+    typedef V vec __attribute__((ext_vector_type(C)));
+    const vec v = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+        if constexpr (sizeof(V) == 2)
+            x[e] = bf16_to_f32(v[e]);
+        else
+            x[e] = v[e];
+    }
+}
+template <int C, class V>
+__device__ __forceinline__ void store_row(V* p, const float (&x)[C]) {
+    if constexpr (sizeof(V) == 2) {
+#pragma unroll
+        for (int e = 0; e < C; e += 2) *reinterpret_cast<uint32_t*>(p + e) = f32x2_to_bf16x2(x[e], x[e + 1]);
+    } else {
+        typedef float vec __attribute__((ext_vector_type(C)));
+        vec v;
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[e] = x[e];
+        *reinterpret_cast<vec*>(p) = v;
+    }
+}
+// Sum over the sixteen lanes of a row, in all of them: rotations inside the row.
+template <int CTRL>
+__device__ __forceinline__ float row_rotated(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum_over_row(float x) {
+    x += row_rotated<0x128>(x);
+    x += row_rotated<0x124>(x);
+    x += row_rotated<0x122>(x);
+    return x + row_rotated<0x121>(x);
+}
+// The same over each half of a row (mirrored within it, then swapped in fours, pairs, ones).
+__device__ __forceinline__ float sum_over_half_row(float x) {
+    x += row_rotated<0x141>(x);  // lane 7 - i of the half
+    x += row_rotated<0x4e>(x);   // lane i ^ 2
+    return x + row_rotated<0xb1>(x);  // lane i ^ 1
 }
 template <int N>
 __device__ __forceinline__ v4f sum_parts4(const uint16_t* src, int part_stride) {
@@ -68,16 +130,22 @@ __device__ __forceinline__ Parts<N> cols8(const uint16_t* m, int part_stride, in
 
 }  // namespace
 
-template <class IO, int R>
-__global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<typename IO::T> a,
-                                                    typename IO::T* __restrict__ d_q,
-                                                    typename IO::T* __restrict__ d_k,
-                                                    typename IO::T* __restrict__ d_v,
-                                                    float* __restrict__ d_g, float* __restrict__ d_beta) {
+template <class IO, int R, bool SHARED, int GW>
+__global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) void k_delta_grad(DeltaShape d, DeltaScan<typename IO::T> a,
+                                                        typename IO::T* __restrict__ d_q,
+                                                        typename IO::T* __restrict__ d_k,
+                                                        typename IO::T* __restrict__ d_v, float* __restrict__ d_g,
+                                                        float* __restrict__ d_beta) {
     using T = typename IO::T;
-    constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, LD = RP + 8, KJ = RP / 32;
-    constexpr int RT = R / 16, ITEMS = RT < 2 ? 1 : RT / 2, V = RP / 8;
-    constexpr int KQ = DL * LD, UP = DL * LP, SP = DL * LS;
+    constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, KJ = RP / 32;
+    constexpr int RT = R / 16, ITEMS = RT * 4 < GW ? 1 : RT * 4 / GW, V = RP / 8, NTHR = GW * 64;
+    // Loading a block ahead takes the registers of a second workgroup on the CU, which hides the
+    // loads better (160 heads of 64 chunks, bf16, p = 64, r = 128: 655 against 857 us), except where
+    // a workgroup goes through several value heads (16 heads in 8, 777 tokens: 45 against 38 us).
+    constexpr bool AHEAD = SHARED;
+    constexpr int CT = PB / GW;             // value columns of one thread's piece of a token row
+    constexpr int PAIRS = GW < 10 ? 2 : 1;  // pair tiles of one wave
+    constexpr int KQ = 4 * KJ * DTILE, UP = DL * LP, SP = DL * LS;
     __shared__ __align__(16) uint16_t sK[NP * KQ], sQ[NP * KQ];
     __shared__ __align__(16) union {
         struct {
@@ -87,107 +155,165 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
     } sm;
     __shared__ float sCf[3 * DL + 1];  // e^G, e^{G_L - G}, beta, e^{G_L}
     __shared__ double sG[DL];
-    __shared__ float sLoc[RT][DL], sWr[RT][DL], sRow[4][DL], sCol[4][DL], sDot[8];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
-    const int64_t blk = blockIdx.x;
-    const int c = static_cast<int>(blk % d.N);
-    const int hk = static_cast<int>((blk / d.N) % d.HK), b = static_cast<int>(blk / d.N / d.HK);
-    const int64_t t0 = static_cast<int64_t>(c) * DL;
-    const int grp = d.H / d.HK;
+    __shared__ float sLoc[RT][DL], sWr[RT][DL], sRow[4][DL], sCol[4][DL], sDot[GW];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // The lane's place, made anew in each phase from a value the compiler cannot see through: kept
+    // over the phases, the addresses it derives from them would take every register.
+    int tid, lane, i, g, vt, vp;
+    auto here = [&]() {
+        tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        lane = tid & 63;
+        i = lane & 15;
+        g = lane >> 4;
+        vt = tid / GW;
+        vp = CT * (tid % GW);
+    };
+    here();
+    const unsigned blk = blockIdx.x, n_chunks = d.N, n_heads = d.HK;
+    const int c = blk % n_chunks, hk = blk / n_chunks % n_heads, b = blk / n_chunks / n_heads;
+    const int64_t t0 = static_cast<int64_t>(c) * DL, row0 = static_cast<int64_t>(b) * d.S + t0;
+    const int grp = SHARED ? d.H / d.HK : 1;
     const int all = static_cast<int>(d.S - t0 < DL ? d.S - t0 : DL);  // rows of the tensors
-    int64_t n = (a.len ? a.len[b] : d.S) - t0;
-    const int L = n < 0 ? 0 : (n > DL ? DL : static_cast<int>(n));
-    const int64_t row0 = static_cast<int64_t>(b) * d.S + t0;
+    const int64_t left = (a.len ? a.len[b] : d.S) - t0;
+    const int L = left < 0 ? 0 : (left > DL ? DL : static_cast<int>(left));
     if (L == 0) {  // past the row's length
-        for (int idx = tid; idx < all * (R / 4); idx += 512) {
-            const int64_t at = ((row0 + idx / (R / 4)) * d.HK + hk) * R + 4 * (idx % (R / 4));
+        for (int x = tid; x < all * (R / 4); x += NTHR) {
+            const int64_t at = ((row0 + x / (R / 4)) * d.HK + hk) * R + 4 * (x % (R / 4));
             io<IO>::st4(d_q, at, zero4());
             io<IO>::st4(d_k, at, zero4());
         }
         for (int hh = 0; hh < grp; ++hh) {
             const int h = hk * grp + hh;
-            for (int idx = tid; idx < all * (d.P / 4); idx += 512)
-                io<IO>::st4(d_v, ((row0 + idx / (d.P / 4)) * d.H + h) * d.P + 4 * (idx % (d.P / 4)), zero4());
+            for (int x = tid; x < all * (d.P / 4); x += NTHR)
+                io<IO>::st4(d_v, ((row0 + x / (d.P / 4)) * d.H + h) * d.P + 4 * (x % (d.P / 4)), zero4());
             if (tid < all) d_g[(row0 + tid) * d.H + h] = d_beta[(row0 + tid) * d.H + h] = 0.0f;
         }
         return;
     }
-    {
-        const T* kb = a.k + b * d.ks[0] + t0 * d.ks[1] + hk * d.ks[2];
-        const T* qb = a.q + b * d.qs[0] + t0 * d.qs[1] + hk * d.qs[2];
-        for (int idx = tid; idx < DL * V; idx += 512) {
-            const int t = idx / V, col = 8 * (idx % V);
-            const bool on = t < L && col < R;
-            const auto kp = load_parts8<IO>(kb + t * d.ks[1] + col, on);
-            const auto qp = load_parts8<IO>(qb + t * d.qs[1] + col, on);
+    const int rho = w * ITEMS / 4, tt0 = (w * ITEMS) & 3;  // this wave's r tile and first token tile
+    const bool act = rho < RT;
+    // the causal pair tiles (token tile tau, source tile sigma) of this wave: of ten, w and w + GW
+    auto tau_of = [](int idx) { return idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3; };
+    auto pairs = [&](auto f) {
 #pragma unroll
-            for (int m = 0; m < NP; ++m) {
-                *reinterpret_cast<b8v*>(sK + m * KQ + t * LD + col) = kp.p[m];
-                *reinterpret_cast<b8v*>(sQ + m * KQ + t * LD + col) = qp.p[m];
+        for (int m = 0; m < PAIRS; ++m) {
+            const int idx = w + m * GW, tau = tau_of(idx);
+            if (idx < 10) f(m, tau, idx - tau * (tau + 1) / 2);
+        }
+    };
+
+    // one block of value columns: this thread's piece of the token rows, and its wave's rows of H and dH
+    float e[CT], z[CT], y[CT];
+    v4f h0, h1, g0, g1;
+    auto fetch = [&](int hh, int p0) {
+        const int h = hk * grp + hh;
+        const int64_t ch = (static_cast<int64_t>(b) * d.H + h) * d.N + c;
+        const int p = p0 + vp;
+#pragma unroll
+        for (int x = 0; x < CT; ++x) e[x] = z[x] = y[x] = 0.0f;
+        h0 = h1 = g0 = g1 = zero4();
+        if (p < d.P) {
+            const int64_t at = (ch * DL + vt) * d.P + p, ay = ((row0 + vt) * d.H + h) * d.P + p;
+            load_row<CT>(a.E + at, e);
+            load_row<CT>(a.dZ + at, z);
+            if (vt < L) load_row<CT>(a.dy + ay, y);
+        }
+        const int ph = p0 + 8 * g;
+        if (act && ph < d.P) {
+            const int64_t at = (ch * R + 16 * rho + i) * d.P + ph;
+            h0 = *reinterpret_cast<const v4f*>(a.H + at);
+            h1 = *reinterpret_cast<const v4f*>(a.H + at + 4);
+            g0 = *reinterpret_cast<const v4f*>(a.dH + at);
+            g1 = *reinterpret_cast<const v4f*>(a.dH + at + 4);
+        }
+    };
+    {  // keys and queries in tiles of 16 tokens x 32, zeros past the length
+        typedef T raw8 __attribute__((ext_vector_type(8)));
+        constexpr int KV = (DL * V + NTHR - 1) / NTHR;
+        raw8 kr[KV], qr[KV];
+#pragma unroll
+        for (int m = 0; m < KV; ++m) {
+            const int t = (tid + m * NTHR) / V, col = 8 * (tid % V), row = t < L ? t : L - 1, from = col < R ? col : 0;
+            kr[m] = *reinterpret_cast<const raw8*>(a.k + b * d.ks[0] + (t0 + row) * d.ks[1] + hk * d.ks[2] + from);
+            qr[m] = *reinterpret_cast<const raw8*>(a.q + b * d.qs[0] + (t0 + row) * d.qs[1] + hk * d.qs[2] + from);
+        }
+        if (AHEAD) fetch(0, 0);
+#pragma unroll
+        for (int m = 0; m < KV; ++m) {
+            const int t = (tid + m * NTHR) / V, col = 8 * (tid % V);
+            if (t < DL) {
+                const auto kp = parts_of<IO>(kr[m], t < L && col < R), qp = parts_of<IO>(qr[m], t < L && col < R);
+                const int at = ((t >> 4) * KJ + (col >> 5)) * DTILE + tile_slot(t & 15, (col >> 3) & 3) * 8;
+#pragma unroll
+                for (int x = 0; x < NP; ++x) {
+                    *reinterpret_cast<b8v*>(sK + x * KQ + at) = kp.p[x];
+                    *reinterpret_cast<b8v*>(sQ + x * KQ + at) = qp.p[x];
+                }
             }
         }
     }
-    const int rho = w * ITEMS / 4, tt0 = (w * ITEMS) & 3;  // this wave's r tile and first token tile
-    const bool act = rho < RT;
-    v4f dq[ITEMS], dk[ITEMS];
+    auto kq_rows = [&](const uint16_t* m, int tile, int j) {  // operand rows: tokens 16 tile + i
+        Parts<NP> o;
 #pragma unroll
-    for (int m = 0; m < ITEMS; ++m) dq[m] = dk[m] = zero4();
-    // the causal pair tiles (token tile tau, source tile sigma) of this wave: w and w + 8 of ten
-    auto tau_of = [](int idx) { return idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3; };
-    const int ntile = w < 2 ? 2 : 1;
+        for (int x = 0; x < NP; ++x)
+            o.p[x] = *reinterpret_cast<const b8v*>(m + x * KQ + (tile * KJ + j) * DTILE + tile_slot(i, g) * 8);
+        return o;
+    };
+    auto kq_cols = [&](const uint16_t* m, int j) {  // rows: r = 16 rho + i, k over the tokens 32 j + 8 g ..
+        Parts<NP> o;
+        const int t = 32 * j + 8 * g + (i >> 2);
+        const uint16_t* at = m + ((t >> 4) * KJ + (rho >> 1)) * DTILE + 4 * (i & 1);
+        const int gg = 2 * (rho & 1) + ((i & 3) >> 1);
+#pragma unroll
+        for (int x = 0; x < NP; ++x)
+            o.p[x] = join8(lds_col4(at + x * KQ + tile_slot(t & 15, gg) * 8),
+                           lds_col4(at + x * KQ + tile_slot((t & 15) + 4, gg) * 8));
+        return o;
+    };
+    v4f dq[SHARED ? ITEMS : 1], dk[SHARED ? ITEMS : 1];
+#pragma unroll
+    for (int m = 0; m < (SHARED ? ITEMS : 1); ++m) dq[m] = dk[m] = zero4();
 
     for (int hh = 0; hh < grp; ++hh) {
         const int h = hk * grp + hh;
         const int64_t ch = (static_cast<int64_t>(b) * d.H + h) * d.N + c;
         const float* cf = a.coef + ch * DCOEF;
-        __syncthreads();
+        if (hh > 0) __syncthreads();
         if (tid <= 3 * DL) sCf[tid] = cf[tid];
         if (tid < DL) sG[tid] = reinterpret_cast<const double*>(cf + DCF)[tid];
-        v4f aq[ITEMS], akr[ITEMS], akw[ITEMS], dP[2], dA[2];
+        const float be = cf[2 * DL + vt];
+        v4f aq[ITEMS], akr[ITEMS], akw[ITEMS], dP[PAIRS], dA[PAIRS];
+#pragma unroll
+        for (int m = 0; m < PAIRS; ++m) dP[m] = dA[m] = zero4();
 #pragma unroll
         for (int m = 0; m < ITEMS; ++m) aq[m] = akr[m] = akw[m] = zero4();
-        dP[0] = dP[1] = dA[0] = dA[1] = zero4();
         float db = 0.0f, hdh = 0.0f;
-        const float* Hc = a.H + ch * (static_cast<int64_t>(R) * d.P);
-        const float* dHc = a.dH + ch * (static_cast<int64_t>(R) * d.P);
-        const float* Ec = a.E + ch * (static_cast<int64_t>(DL) * d.P);
-        const float* Zc = a.dZ + ch * (static_cast<int64_t>(DL) * d.P);
         for (int p0 = 0; p0 < d.P; p0 += PB) {
-            __syncthreads();
-            {
-                const int t = tid >> 3, pc = 4 * (tid & 7), p = p0 + pc;
-                v4f e = zero4(), z = zero4(), y = zero4();
-                if (p < d.P) {
-                    e = *reinterpret_cast<const v4f*>(Ec + t * d.P + p);
-                    z = *reinterpret_cast<const v4f*>(Zc + t * d.P + p);
-                    if (t < L) y = io<IO>::ld4(a.dy, ((row0 + t) * d.H + h) * d.P + p);
-                }
-                const float be = sCf[2 * DL + t];
-                db += e[0] * z[0] + e[1] * z[1] + e[2] * z[2] + e[3] * z[3];
-                e *= be;
-                z *= be;
-                if (p < d.P && t < all) io<IO>::st4(d_v, ((row0 + t) * d.H + h) * d.P + p, z);
-                store_parts4<3>(sm.v.U + t * LP + pc, UP, e);
-                store_parts4<3>(sm.v.Z + t * LP + pc, UP, z);
-                store_parts4<NP>(sm.v.Y + t * LP + pc, UP, y);
-            }
-            Parts<3> hp, gp;
-            if (act) {
-                const int p = p0 + 8 * g;
-                v4f h0 = zero4(), h1 = zero4(), g0 = zero4(), g1 = zero4();
-                if (p < d.P) {
-                    const int64_t at = static_cast<int64_t>(16 * rho + i) * d.P + p;
-                    h0 = *reinterpret_cast<const v4f*>(Hc + at);
-                    h1 = *reinterpret_cast<const v4f*>(Hc + at + 4);
-                    g0 = *reinterpret_cast<const v4f*>(dHc + at);
-                    g1 = *reinterpret_cast<const v4f*>(dHc + at + 4);
-                }
-                if (tt0 == 0) {
+            here();
+            if (!AHEAD) fetch(hh, p0);
+            if (p0 > 0) __syncthreads();
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) hdh += h0[v] * g0[v] + h1[v] * g1[v];
-                }
-                hp = split44<3>(h0, h1);
-                gp = split44<3>(g0, g1);
+            for (int x = 0; x < CT; ++x) {
+                db += e[x] * z[x];
+                e[x] *= be;
+                z[x] *= be;
+            }
+            if (p0 + vp < d.P && vt < all) store_row<CT>(d_v + ((row0 + vt) * d.H + h) * d.P + p0 + vp, z);
+            store_parts<3, CT>(sm.v.U + vt * LP + vp, UP, e);
+            store_parts<3, CT>(sm.v.Z + vt * LP + vp, UP, z);
+            store_parts<NP, CT>(sm.v.Y + vt * LP + vp, UP, y);
+            if (tt0 == 0) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) hdh += h0[v] * g0[v] + h1[v] * g1[v];
+            }
+            const auto hp = split44<3>(h0, h1);
+            const auto gp = split44<3>(g0, g1);
+            if (AHEAD) {  // the next block's, under way while this one is multiplied
+                if (p0 + PB < d.P)
+                    fetch(hh, p0 + PB);
+                else if (hh + 1 < grp)
+                    fetch(hh + 1, 0);
             }
             __syncthreads();
             if (act) {
@@ -199,21 +325,19 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
                     akw[m] = mma(gp, rows8<3>(sm.v.U, UP, LP, row, 8 * g), akw[m]);
                 }
             }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                if (m < ntile) {
-                    const int idx = w + 8 * m, tau = tau_of(idx), sig = idx - tau * (tau + 1) / 2;
-                    const auto u = rows8<3>(sm.v.U, UP, LP, 16 * sig + i, 8 * g);
-                    dP[m] = mma(u, rows8<NP>(sm.v.Y, UP, LP, 16 * tau + i, 8 * g), dP[m]);
-                    dA[m] = mma(u, rows8<3>(sm.v.Z, UP, LP, 16 * tau + i, 8 * g), dA[m]);
-                }
-            }
+            pairs([&](int m, int tau, int sig) {
+                const auto u = rows8<3>(sm.v.U, UP, LP, 16 * sig + i, 8 * g);
+                dP[m] = mma(u, rows8<NP>(sm.v.Y, UP, LP, 16 * tau + i, 8 * g), dP[m]);
+                dA[m] = mma(u, rows8<3>(sm.v.Z, UP, LP, 16 * tau + i, 8 * g), dA[m]);
+            });
         }
+        here();
         // results D[r][t] (lane token 16 tt + i, rows r = 16 rho + 4 g + v)
         if (act) {
 #pragma unroll
             for (int m = 0; m < ITEMS; ++m) {
-                const int t = 16 * (tt0 + m) + i, at = t * LD + 16 * rho + 4 * g;
+                const int t = 16 * (tt0 + m) + i;
+                const int at = ((tt0 + m) * KJ + (rho >> 1)) * DTILE + tile_slot(i, 2 * (rho & 1) + (g >> 1)) * 8 + 4 * (g & 1);
                 const float eg = sCf[t], tail = sCf[DL + t];
                 aq[m] *= d.scale * eg;
                 akr[m] *= -eg;
@@ -231,66 +355,54 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
                     sLoc[rho][t] = loc;
                     sWr[rho][t] = wr;
                 }
-                dq[m] += aq[m];
-                dk[m] += akr[m] + akw[m];
+                akr[m] += akw[m];  // the inter-chunk part of d_k
             }
         }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) hdh += __shfl_xor(hdh, o);
+        if (tt0 == 0) {
+            hdh = sum_over_row(hdh);
+            hdh = sum_over_g(hdh);
+        }
         if (lane == 0) sDot[w] = hdh;
-        // pair tiles D[s][t] (lane token 16 tau + i, sources 16 sig + 4 g + v)
+        here();
+        pairs([&](int m, int tau, int sig) {  // pair tile D[s][t] (lane token 16 tau + i, sources 16 sig + 4 g + v)
+            v4f kk = zero4(), qk = zero4();
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            if (m < ntile) {
-                const int idx = w + 8 * m, tau = tau_of(idx), sig = idx - tau * (tau + 1) / 2;
-                v4f kk = zero4(), qk = zero4();
-#pragma unroll
-                for (int j = 0; j < KJ; ++j) {
-                    const auto ks = rows8<NP>(sK, KQ, LD, 16 * sig + i, 32 * j + 8 * g);
-                    kk = mma(ks, rows8<NP>(sK, KQ, LD, 16 * tau + i, 32 * j + 8 * g), kk);
-                    qk = mma(ks, rows8<NP>(sQ, KQ, LD, 16 * tau + i, 32 * j + 8 * g), qk);
-                }
-                const int t = 16 * tau + i;
-                float wrow = 0.0f;
-                v4f wcol;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int s = 16 * sig + 4 * g + v;
-                    const float e = s <= t ? exp2_of(sG[t] - sG[s]) : 0.0f;
-                    const float es = s < t ? e : 0.0f;
-                    const float x = es * (d.scale * dP[m][v] * qk[v] - dA[m][v] * kk[v]);
-                    wrow += x;
-                    wcol[v] = x;
-                    dP[m][v] *= d.scale * e;
-                    dA[m][v] *= -es;
-                }
-                wrow = sum_over_g(wrow);
-                if (g == 0) sRow[sig][t] = wrow;
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) {
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) wcol[v] += __shfl_xor(wcol[v], o);
-                }
-                if (i == 0) *reinterpret_cast<v4f*>(&sCol[tau][16 * sig + 4 * g]) = wcol;
+            for (int j = 0; j < KJ; ++j) {
+                const auto ks = kq_rows(sK, sig, j);
+                kk = mma(ks, kq_rows(sK, tau, j), kk);
+                qk = mma(ks, kq_rows(sQ, tau, j), qk);
             }
-        }
+            const int t = 16 * tau + i;
+            float wrow = 0.0f;
+            v4f wcol;
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) db += __shfl_xor(db, o);
-        if ((tid & 7) == 0 && (tid >> 3) < all) d_beta[(row0 + (tid >> 3)) * d.H + h] = (tid >> 3) < L ? db : 0.0f;
+            for (int v = 0; v < 4; ++v) {
+                const int s = 16 * sig + 4 * g + v;
+                const float e2 = s <= t ? exp2_of(sG[t] - sG[s]) : 0.0f;
+                const float es = s < t ? e2 : 0.0f;
+                const float x = es * (d.scale * dP[m][v] * qk[v] - dA[m][v] * kk[v]);
+                wrow += x;
+                wcol[v] = sum_over_row(x);
+                dP[m][v] *= d.scale * e2;
+                dA[m][v] *= -es;
+            }
+            wrow = sum_over_g(wrow);
+            if (g == 0) sRow[sig][t] = wrow;
+            if (i == 0) *reinterpret_cast<v4f*>(&sCol[tau][16 * sig + 4 * g]) = wcol;
+        });
+        db = GW == 16 ? sum_over_row(db) : sum_over_half_row(db);
+        if (tid % GW == 0 && vt < all) d_beta[(row0 + vt) * d.H + h] = vt < L ? db : 0.0f;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {  // dS, then dKK
+            here();
             __syncthreads();
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                if (m < ntile) {
-                    const int idx = w + 8 * m, tau = tau_of(idx), sig = idx - tau * (tau + 1) / 2;
-                    uint16_t* at = sm.S + (16 * tau + i) * LS + 16 * sig + 4 * g;
-                    store_parts4<3>(at, SP, which ? dA[m] : dP[m]);
-                    if (sig == tau && (tau & 1) == 0) store_parts4<3>(at + 16, SP, zero4());
-                }
-            }
+            pairs([&](int m, int tau, int sig) {
+                uint16_t* at = sm.S + (16 * tau + i) * LS + 16 * sig + 4 * g;
+                store_parts4<3>(at, SP, which ? dA[m] : dP[m]);
+                if (sig == tau && (tau & 1) == 0) store_parts4<3>(at + 16, SP, zero4());
+            });
             __syncthreads();
-            if (which == 1 && w == 0) {
+            if (which == 0 && w == GW - 1) {
                 float loc = 0.0f, wr = 0.0f, hd = 0.0f;
 #pragma unroll
                 for (int m = 0; m < RT; ++m) {
@@ -303,7 +415,7 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
                     if (m >= g) loc -= sCol[m][lane];
                 }
 #pragma unroll
-                for (int m = 0; m < 8; ++m) hd += sDot[m];
+                for (int m = 0; m < RT; ++m) hd += sDot[m * 4 / ITEMS];
                 double suf = loc, pre = wr;
 #pragma unroll
                 for (int o = 1; o < 64; o <<= 1) {
@@ -319,34 +431,38 @@ __global__ __launch_bounds__(512) void k_delta_grad(DeltaShape d, DeltaScan<type
             if (act) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const auto kt = cols8<NP>(sK, KQ, LD, 32 * j, 16 * rho, i, g);
+                    const auto kt = kq_cols(sK, j);
                     Parts<NP> xt;
-                    if (which == 0) xt = cols8<NP>(sQ, KQ, LD, 32 * j, 16 * rho, i, g);
+                    if (which == 0) xt = kq_cols(sQ, j);
 #pragma unroll
                     for (int m = 0; m < ITEMS; ++m) {
                         const int tt = tt0 + m;
                         if (j <= tt / 2) {
                             const auto x = rows8<3>(sm.S, SP, LS, 16 * tt + i, 32 * j + 8 * g);
-                            if (which == 0) dq[m] = mma(kt, x, dq[m]);
-                            else dk[m] = mma(kt, x, dk[m]);
+                            if (which == 0) aq[m] = mma(kt, x, aq[m]);
+                            else akr[m] = mma(kt, x, akr[m]);
                         }
                         if (j >= tt / 2) {
                             const auto x = cols8<3>(sm.S, SP, LS, 32 * j, 16 * tt, i, g);
-                            dk[m] = mma(which == 0 ? xt : kt, x, dk[m]);
+                            akr[m] = mma(which == 0 ? xt : kt, x, akr[m]);
                         }
                     }
                 }
             }
         }
-    }
-    if (act) {
+        if (act) {
 #pragma unroll
-        for (int m = 0; m < ITEMS; ++m) {
-            const int t = 16 * (tt0 + m) + i;
-            if (t < all) {
-                const int64_t at = ((row0 + t) * d.HK + hk) * R + 16 * rho + 4 * g;
-                io<IO>::st4(d_q, at, dq[m]);
-                io<IO>::st4(d_k, at, dk[m]);
+            for (int m = 0; m < ITEMS; ++m) {
+                if constexpr (SHARED) {
+                    dq[m] += aq[m];
+                    dk[m] += akr[m];
+                }
+                const int t = 16 * (tt0 + m) + i;
+                if (hh + 1 == grp && t < all) {
+                    const int64_t at = ((row0 + t) * d.HK + hk) * R + 16 * rho + 4 * g;
+                    io<IO>::st4(d_q, at, SHARED ? dq[SHARED ? m : 0] : aq[m]);
+                    io<IO>::st4(d_k, at, SHARED ? dk[SHARED ? m : 0] : akr[m]);
+                }
             }
         }
     }
@@ -368,15 +484,23 @@ hipError_t grad_io(const DeltaShape& d, const DeltaBufs& f, hipStream_t st) {
     a.dH = f.dH;
     a.dZ = f.dZ;
     T *dq = static_cast<T*>(f.d_q), *dk = static_cast<T*>(f.d_k), *dv = static_cast<T*>(f.d_v);
-    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.HK * d.N)), block(512);
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.HK * d.N));
+    constexpr int GW = 8;
+    auto run = [&](auto r) {
+        constexpr int R = decltype(r)::value;
+        if (d.H == d.HK)
+            k_delta_grad<IO, R, false, GW><<<grid, 64 * GW, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta);
+        else
+            k_delta_grad<IO, R, true, GW><<<grid, 64 * GW, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta);
+        return hipGetLastError();
+    };
     switch (d.R) {
-        case 16: k_delta_grad<IO, 16><<<grid, block, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta); break;
-        case 32: k_delta_grad<IO, 32><<<grid, block, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta); break;
-        case 64: k_delta_grad<IO, 64><<<grid, block, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta); break;
-        case 128: k_delta_grad<IO, 128><<<grid, block, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta); break;
+        case 16: return run(std::integral_constant<int, 16>{});
+        case 32: return run(std::integral_constant<int, 32>{});
+        case 64: return run(std::integral_constant<int, 64>{});
+        case 128: return run(std::integral_constant<int, 128>{});
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
 }  // namespace

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -53,9 +54,9 @@ class ssd_dims(ctypes.Structure):
 class ssd_delta_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seq", ctypes.c_int64), ("kheads", ctypes.c_int64),
                 ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
-                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
-                ("v_stride", ctypes.c_int64 * 3), ("scale", ctypes.c_float),
-                ("io_dtype", ctypes.c_int32)]
+                *[(f"{t}_stride_{axis}", ctypes.c_int64) for t in "qkv"
+                  for axis in ("batch", "token", "head")],
+                ("scale", ctypes.c_float), ("io_dtype", ctypes.c_int32)]
 
 
 class SsdError(RuntimeError):
@@ -435,115 +436,147 @@ def ssd_step(x, dt, A, B, C, D, state, new_state, y, stream=None) -> int:
     return load_library().ssd_step(b, h, p, r, io, *args, _stream(stream))
 
 
+# The entry points below are also called a token at a time, so their marshalling is kept short:
+# addresses go to ctypes as plain integers, and a tensor is looked over once.
+_IO = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+
+
 def _io_of(t: torch.Tensor, name: str) -> int:
-    io = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}.get(t.dtype)
+    io = _IO.get(t.dtype)
     if io is None:
         raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
     return io
 
 
+def _address(t: Optional[torch.Tensor], name: str, dtype, numel: int, required: bool = True):
+    """The address of a contiguous device tensor of the right type and size (None for None)."""
+    if (t is not None and isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda
+            and t.numel() == numel and t.is_contiguous()):
+        return t.data_ptr()
+    _ptr(t, name, dtype, numel, required)  # says what is wrong
+    return None
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream \
+        if stream is None or isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _strided(t: torch.Tensor, name: str, dtype, shape):
-    """(pointer, element strides of all axes but the last) of a device tensor whose last axis is
+    """(address, element strides of all axes but the last) of a device tensor whose last axis is
     contiguous; axes of one element get stride 0."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.numel() and t.stride(-1) != 1:
+    *strides, last = t.stride()
+    if last != 1 and t.numel() and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return ctypes.c_void_p(t.data_ptr()), [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape)]
+    return t.data_ptr(), [st if n > 1 else 0 for st, n in zip(strides, shape)]
 
 
 def _delta_args(q, k, v, scale):
-    """(dims, pointers of q, k, v) for q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]``."""
-    if q.dim() != 4 or v.dim() != 4 or q.shape[:2] != v.shape[:2]:
-        raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
-    b, s, hk, r = q.shape
-    h, p = v.shape[2:]
-    d = ssd_delta_dims(b, s, hk, h, p, r)
-    d.io_dtype = _io_of(q, "q")
-    d.scale = r ** -0.5 if scale is None else float(scale)
-    ptrs = []
-    for t, name, field, shape in ((q, "q", d.q_stride, q.shape), (k, "k", d.k_stride, q.shape),
-                                  (v, "v", d.v_stride, v.shape)):
-        ptr, strides = _strided(t, name, q.dtype, shape)
-        field[:] = strides
-        ptrs.append(ptr)
-    return d, ptrs
+    """(dims, addresses of q, k, v) for q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]``, or without the
+    token axis."""
+    if q.dim() not in (3, 4) or v.dim() != q.dim() or q.shape[:-2] != v.shape[:-2]:
+        raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p] (one token: [b, hk, r], [b, h, p])")
+    io = _io_of(q, "q")
+    (pq, sq), (pk, sk), (pv, sv) = (_strided(q, "q", q.dtype, q.shape), _strided(k, "k", q.dtype, q.shape),
+                                    _strided(v, "v", q.dtype, v.shape))
+    b, *seq, hk, r = q.shape
+    h, p = v.shape[-2:]
+    if not seq:
+        seq, sq, sk, sv = (1,), (sq[0], 0, sq[1]), (sk[0], 0, sk[1]), (sv[0], 0, sv[1])
+    d = ssd_delta_dims(b, *seq, hk, h, p, r, *sq, *sk, *sv, r ** -0.5 if scale is None else scale, io)
+    return d, (pq, pk, pv)
 
 
-def ssd_delta_workspace_size(dims: ssd_delta_dims, bwd: bool) -> int:
+@functools.lru_cache(maxsize=256)
+def _delta_bytes(b, s, hk, h, p, r, io, bwd):
+    d = ssd_delta_dims(b, s, hk, h, p, r, *[0] * 9, 1.0, io)
     n = ctypes.c_size_t(0)
-    rc = load_library().ssd_delta_workspace_size(ctypes.byref(dims), int(bool(bwd)), ctypes.byref(n))
+    rc = load_library().ssd_delta_workspace_size(ctypes.byref(d), bwd, ctypes.byref(n))
     if rc:
         raise SsdError(rc, "ssd_delta_workspace_size", ssd_last_error())
     return int(n.value)
+
+
+def ssd_delta_workspace_size(dims: ssd_delta_dims, bwd: bool) -> int:
+    return _delta_bytes(dims.batch, dims.seq, dims.kheads, dims.nheads, dims.headdim, dims.dstate,
+                        dims.io_dtype, int(bool(bwd)))
+
+
+def _delta_sizes(d, q, v):
+    return v.numel() // v.shape[-1] if v.shape[-1] else 0, d.batch * d.nheads * d.headdim * d.dstate
+
+
+def _host_lengths(valid_len, batch):
+    if valid_len is None:
+        return None
+    return _ptr(valid_len, "valid_len", torch.int64, batch, False)
 
 
 def ssd_delta_fwd(q, k, v, g, beta, init, valid_len, y, final_state, ws, scale=None, stream=None) -> int:
     """q, k ``[b, s, hk, r]``, v ``[b, s, h, p]`` (last axis contiguous), g, beta ``[b, s, h]``;
     scale None is ``1 / sqrt(r)``."""
     d, qkv = _delta_args(q, k, v, scale)
-    f, tok, state = torch.float32, v.shape[0] * v.shape[1] * v.shape[2], d.batch * d.nheads * d.headdim * d.dstate
-    args = [_ptr(g, "g", f, tok, True), _ptr(beta, "beta", f, tok, True),
-            _ptr(init, "init", f, state, False),
-            _ptr(valid_len, "valid_len", torch.int64, d.batch, False),
-            _ptr(y, "y", q.dtype, v.numel(), True), _ptr(final_state, "final_state", f, state, False)]
+    f, (tok, state) = torch.float32, _delta_sizes(d, q, v)
+    args = (_address(g, "g", f, tok), _address(beta, "beta", f, tok), _address(init, "init", f, state, False),
+            _host_lengths(valid_len, d.batch), _address(y, "y", q.dtype, v.numel()),
+            _address(final_state, "final_state", f, state, False))
     wp, wb = _ws(ws)
-    return load_library().ssd_delta_fwd(ctypes.byref(d), *qkv, *args, wp, wb, _stream(stream))
+    return load_library().ssd_delta_fwd(ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream))
 
 
 def ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, valid_len, d_q, d_k, d_v, d_g, d_beta, d_init, ws,
                   scale=None, stream=None) -> int:
     d, qkv = _delta_args(q, k, v, scale)
-    f, tok, state = torch.float32, v.shape[0] * v.shape[1] * v.shape[2], d.batch * d.nheads * d.headdim * d.dstate
-    head = [_ptr(dy, "dy", q.dtype, v.numel(), True), _ptr(d_final, "d_final", f, state, False)]
-    args = [_ptr(g, "g", f, tok, True), _ptr(beta, "beta", f, tok, True),
-            _ptr(init, "init", f, state, False),
-            _ptr(valid_len, "valid_len", torch.int64, d.batch, False),
-            _ptr(d_q, "d_q", q.dtype, q.numel(), True), _ptr(d_k, "d_k", q.dtype, q.numel(), True),
-            _ptr(d_v, "d_v", q.dtype, v.numel(), True), _ptr(d_g, "d_g", f, tok, True),
-            _ptr(d_beta, "d_beta", f, tok, True), _ptr(d_init, "d_init", f, state, False)]
+    f, (tok, state), io = torch.float32, _delta_sizes(d, q, v), q.dtype
+    args = (_address(g, "g", f, tok), _address(beta, "beta", f, tok), _address(init, "init", f, state, False),
+            _host_lengths(valid_len, d.batch), _address(d_q, "d_q", io, q.numel()),
+            _address(d_k, "d_k", io, q.numel()), _address(d_v, "d_v", io, v.numel()),
+            _address(d_g, "d_g", f, tok), _address(d_beta, "d_beta", f, tok),
+            _address(d_init, "d_init", f, state, False))
     wp, wb = _ws(ws)
-    return load_library().ssd_delta_bwd(ctypes.byref(d), *head, *qkv, *args, wp, wb, _stream(stream))
+    return load_library().ssd_delta_bwd(ctypes.byref(d), _address(dy, "dy", io, v.numel()),
+                                        _address(d_final, "d_final", f, state, False), *qkv, *args, wp, wb,
+                                        _raw_stream(stream))
 
 
 def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -> int:
     """q, k ``[b, hk, r]``, v ``[b, h, p]`` (last axis contiguous), g, beta ``[b, h]``, state
     ``[nslots, h, p, r]`` updated in place, slots device int32 ``[b]`` or None, y like v."""
-    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+    if q.dim() != 3:
         raise ValueError("q and k must be [b, hk, r], v [b, h, p] and state [nslots, h, p, r]")
-    d, qkv = _delta_args(q.unsqueeze(1), k.unsqueeze(1) if k.dim() == 3 else k, v.unsqueeze(1), scale)
-    f, n = torch.float32, state.shape[0]
-    if tuple(state.shape[1:]) != (d.nheads, d.headdim, d.dstate):
+    d, qkv = _delta_args(q, k, v, scale)
+    f, io = torch.float32, q.dtype
+    if state.dim() != 4 or state.shape[1:] != (*v.shape[1:], q.shape[2]):
         raise ValueError(f"state must be [nslots, {d.nheads}, {d.headdim}, {d.dstate}] (got {list(state.shape)})")
-    if slots is not None and (slots.dtype != torch.int32 or slots.device.type != "cuda"
-                              or not slots.is_contiguous() or slots.numel() != d.batch):
+    if slots is not None and not (slots.dtype == torch.int32 and slots.is_cuda and slots.is_contiguous()
+                                  and slots.numel() == d.batch):
         raise ValueError(f"slots must be a contiguous device int32 tensor of {d.batch} elements")
-    args = [_ptr(g, "g", f, d.batch * d.nheads, True), _ptr(beta, "beta", f, d.batch * d.nheads, True),
-            _ptr(state, "state", f, state.numel(), True),
-            ctypes.c_void_p(slots.data_ptr()) if slots is not None else None,
-            _ptr(y, "y", q.dtype, v.numel(), True)]
-    return load_library().ssd_delta_step(ctypes.byref(d), n, *qkv, *args, _stream(stream))
+    bh = d.batch * d.nheads
+    return load_library().ssd_delta_step(
+        ctypes.byref(d), state.shape[0], *qkv, _address(g, "g", f, bh), _address(beta, "beta", f, bh),
+        _address(state, "state", f, state.numel()), None if slots is None else slots.data_ptr(),
+        _address(y, "y", io, v.numel()), _raw_stream(stream))
 
 
 def ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream=None) -> int:
     """x, residual, s, y ``[..., width]``, weight fp32 ``[width]``, y8 float8_e4m3fn like x, scale fp32
     ``[..., width / group]`` (group 0: one per row)."""
-    width = x.shape[-1]
-    n, io = x.numel(), _io_of(x, "x")
+    width, n, io = x.shape[-1], x.numel(), x.dtype
     rows = n // width if width else 0
-    args = [_ptr(x, "x", x.dtype, n, True), _ptr(residual, "residual", x.dtype, n, False),
-            _ptr(weight, "weight", torch.float32, width, True)]
     groups = width // group if group > 0 else 1
-    outs = [_ptr(s, "s", x.dtype, n, False), _ptr(y, "y", x.dtype, n, False),
-            _ptr(y8, "y8", torch.float8_e4m3fn, n, False),
-            _ptr(scale, "scale", torch.float32, rows * groups, False)]
-    return load_library().ssd_rms_norm(rows, width, io, float(eps), *args, int(group), *outs, _stream(stream))
+    return load_library().ssd_rms_norm(
+        rows, width, _io_of(x, "x"), eps, _address(x, "x", io, n), _address(residual, "residual", io, n, False),
+        _address(weight, "weight", torch.float32, width), int(group), _address(s, "s", io, n, False),
+        _address(y, "y", io, n, False), _address(y8, "y8", torch.float8_e4m3fn, n, False),
+        _address(scale, "scale", torch.float32, rows * groups, False), _raw_stream(stream))
 
 
 def ssd_rms_norm_workspace_size(rows, width) -> int:
@@ -555,28 +588,27 @@ def ssd_rms_norm_workspace_size(rows, width) -> int:
 
 
 def ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream=None) -> int:
-    width = s.shape[-1]
-    n, io = s.numel(), _io_of(s, "s")
-    args = [_ptr(dy, "dy", s.dtype, n, True), _ptr(s, "s", s.dtype, n, True),
-            _ptr(d_s, "d_s", s.dtype, n, False), _ptr(weight, "weight", torch.float32, width, True),
-            _ptr(d_x, "d_x", s.dtype, n, True), _ptr(d_weight, "d_weight", torch.float32, width, True)]
+    width, n, io = s.shape[-1], s.numel(), s.dtype
     wp, wb = _ws(ws)
-    return load_library().ssd_rms_norm_bwd(n // width if width else 0, width, io, float(eps), *args, wp, wb,
-                                           _stream(stream))
+    return load_library().ssd_rms_norm_bwd(
+        n // width if width else 0, width, _io_of(s, "s"), eps, _address(dy, "dy", io, n), _address(s, "s", io, n),
+        _address(d_s, "d_s", io, n, False), _address(weight, "weight", torch.float32, width),
+        _address(d_x, "d_x", io, n), _address(d_weight, "d_weight", torch.float32, width), wp, wb,
+        _raw_stream(stream))
 
 
 # ------------------------------------------------------------ allocating helpers
-@contextlib.contextmanager
+_AS_IT_IS = contextlib.nullcontext()
+
+
 def _allocating_on(stream):
     """Allocate on the stream the work runs on, so that memory freed after the call is reused in
     that stream's order."""
     if stream is None:
-        yield
-        return
+        return _AS_IT_IS
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        yield
+    return torch.cuda.stream(stream)
 
 
 def _check(rc: int, where: str):
