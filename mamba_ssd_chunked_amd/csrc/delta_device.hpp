@@ -167,27 +167,9 @@ __device__ __forceinline__ constexpr int tile_slot(int i, int g) { return 16 * g
 __device__ __forceinline__ constexpr int tri_lower(int tau, int j) { return tau < 2 ? tau : 2 * (tau - 1) + j; }
 __device__ __forceinline__ constexpr int tri_upper(int tau, int j) { return tau < 2 ? 2 * tau + j : tau + 2; }
 
-// Eight consecutive values of a token row as parts, zeros where !on.
+// Parts of a value of the io type.
 template <class IO>
 __host__ __device__ constexpr int in_parts() { return sizeof(typename IO::T) == 2 ? 1 : 3; }
-
-template <class IO>
-__device__ __forceinline__ Parts<in_parts<IO>()> load_parts8(const typename IO::T* p, bool on) {
-    Parts<in_parts<IO>()> o;
-    if constexpr (in_parts<IO>() == 1) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (on) w = *reinterpret_cast<const uint4*>(p);
-        o.p[0] = __builtin_bit_cast(b8v, w);
-    } else {
-        v4f a = zero4(), b = zero4();
-        if (on) {
-            a = *reinterpret_cast<const v4f*>(p);
-            b = *reinterpret_cast<const v4f*>(p + 4);
-        }
-        o = split44<3>(a, b);
-    }
-    return o;
-}
 
 // Eight io values as bf16 parts, zeros where !on.
 template <class IO, class V>

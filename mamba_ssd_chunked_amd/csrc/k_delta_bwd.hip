@@ -26,6 +26,7 @@ namespace ssd {
 namespace {
 
 constexpr int PB = 32;       // value columns staged at a time
+constexpr int GW = 8;        // waves of a workgroup
 constexpr int LP = PB + 8;   // their LDS row stride
 constexpr int LS = DL + 8;   // row stride of a 64 x 64 part
 
@@ -40,49 +41,6 @@ __device__ __forceinline__ void store_parts4(uint16_t* dst, int part_stride, v4f
         if (n + 1 < N)
             x -= v4f{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
-    }
-}
-template <int N, int C>
-__device__ __forceinline__ void store_parts(uint16_t* dst, int part_stride, const float (&x)[C]) {
-    if constexpr (C == 4) {
-        store_parts4<N>(dst, part_stride, v4f{x[0], x[1], x[2], x[3]});
-    } else {
-        float a = x[0], b = x[1];
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const uint32_t w = f32x2_to_bf16x2(a, b);
-            *reinterpret_cast<uint32_t*>(dst + n * part_stride) = w;
-            if (n + 1 < N) {
-                a -= __uint_as_float(w << 16);
-                b -= __uint_as_float(w & 0xffff0000u);
-            }
-        }
-    }
-}
-// C (2 or 4) consecutive values.
-template <int C, class V>
-__device__ __forceinline__ void load_row(const V* p, float (&x)[C]) {
-    typedef V vec __attribute__((ext_vector_type(C)));
-    const vec v = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-    for (int e = 0; e < C; ++e) {
-        if constexpr (sizeof(V) == 2)
-            x[e] = bf16_to_f32(v[e]);
-        else
-            x[e] = v[e];
-    }
-}
-template <int C, class V>
-__device__ __forceinline__ void store_row(V* p, const float (&x)[C]) {
-    if constexpr (sizeof(V) == 2) {
-#pragma unroll
-        for (int e = 0; e < C; e += 2) *reinterpret_cast<uint32_t*>(p + e) = f32x2_to_bf16x2(x[e], x[e + 1]);
-    } else {
-        typedef float vec __attribute__((ext_vector_type(C)));
-        vec v;
-#pragma unroll
-        for (int e = 0; e < C; ++e) v[e] = x[e];
-        *reinterpret_cast<vec*>(p) = v;
     }
 }
 // Sum over the sixteen lanes of a row, in all of them: rotations inside the row.
@@ -130,12 +88,13 @@ __device__ __forceinline__ Parts<N> cols8(const uint16_t* m, int part_stride, in
 
 }  // namespace
 
-template <class IO, int R, bool SHARED, int GW>
-__global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) void k_delta_grad(DeltaShape d, DeltaScan<typename IO::T> a,
-                                                        typename IO::T* __restrict__ d_q,
-                                                        typename IO::T* __restrict__ d_k,
-                                                        typename IO::T* __restrict__ d_v, float* __restrict__ d_g,
-                                                        float* __restrict__ d_beta) {
+// bf16 without shared heads: 76 KB of LDS and, held to 128 registers, two workgroups on a CU (655 us
+// for 160 heads of 64 chunks with p = 64, r = 128, against 999 us for one of four waves; sixteen
+// waves on one chunk: 909 us).  fp32 takes 152 KB of LDS: one workgroup a CU.
+template <class IO, int R, bool SHARED>
+__global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) void k_delta_grad(
+    DeltaShape d, DeltaScan<typename IO::T> a, typename IO::T* __restrict__ d_q, typename IO::T* __restrict__ d_k,
+    typename IO::T* __restrict__ d_v, float* __restrict__ d_g, float* __restrict__ d_beta) {
     using T = typename IO::T;
     constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, KJ = RP / 32;
     constexpr int RT = R / 16, ITEMS = RT * 4 < GW ? 1 : RT * 4 / GW, V = RP / 8, NTHR = GW * 64;
@@ -143,8 +102,8 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
     // loads better (160 heads of 64 chunks, bf16, p = 64, r = 128: 655 against 857 us), except where
     // a workgroup goes through several value heads (16 heads in 8, 777 tokens: 45 against 38 us).
     constexpr bool AHEAD = SHARED;
-    constexpr int CT = PB / GW;             // value columns of one thread's piece of a token row
-    constexpr int PAIRS = GW < 10 ? 2 : 1;  // pair tiles of one wave
+    constexpr int CT = PB / GW;  // value columns of one thread's piece of a token row
+    constexpr int PAIRS = 2;     // pair tiles of one wave
     constexpr int KQ = 4 * KJ * DTILE, UP = DL * LP, SP = DL * LS;
     __shared__ __align__(16) uint16_t sK[NP * KQ], sQ[NP * KQ];
     __shared__ __align__(16) union {
@@ -204,20 +163,17 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
     };
 
     // one block of value columns: this thread's piece of the token rows, and its wave's rows of H and dH
-    float e[CT], z[CT], y[CT];
-    v4f h0, h1, g0, g1;
+    v4f e, z, y, h0, h1, g0, g1;
     auto fetch = [&](int hh, int p0) {
         const int h = hk * grp + hh;
         const int64_t ch = (static_cast<int64_t>(b) * d.H + h) * d.N + c;
         const int p = p0 + vp;
-#pragma unroll
-        for (int x = 0; x < CT; ++x) e[x] = z[x] = y[x] = 0.0f;
-        h0 = h1 = g0 = g1 = zero4();
+        e = z = y = h0 = h1 = g0 = g1 = zero4();
         if (p < d.P) {
             const int64_t at = (ch * DL + vt) * d.P + p, ay = ((row0 + vt) * d.H + h) * d.P + p;
-            load_row<CT>(a.E + at, e);
-            load_row<CT>(a.dZ + at, z);
-            if (vt < L) load_row<CT>(a.dy + ay, y);
+            e = *reinterpret_cast<const v4f*>(a.E + at);
+            z = *reinterpret_cast<const v4f*>(a.dZ + at);
+            if (vt < L) y = io<IO>::ld4(a.dy, ay);
         }
         const int ph = p0 + 8 * g;
         if (act && ph < d.P) {
@@ -293,16 +249,13 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
             here();
             if (!AHEAD) fetch(hh, p0);
             if (p0 > 0) __syncthreads();
-#pragma unroll
-            for (int x = 0; x < CT; ++x) {
-                db += e[x] * z[x];
-                e[x] *= be;
-                z[x] *= be;
-            }
-            if (p0 + vp < d.P && vt < all) store_row<CT>(d_v + ((row0 + vt) * d.H + h) * d.P + p0 + vp, z);
-            store_parts<3, CT>(sm.v.U + vt * LP + vp, UP, e);
-            store_parts<3, CT>(sm.v.Z + vt * LP + vp, UP, z);
-            store_parts<NP, CT>(sm.v.Y + vt * LP + vp, UP, y);
+            db += e[0] * z[0] + e[1] * z[1] + e[2] * z[2] + e[3] * z[3];
+            e *= be;
+            z *= be;
+            if (p0 + vp < d.P && vt < all) io<IO>::st4(d_v, ((row0 + vt) * d.H + h) * d.P + p0 + vp, z);
+            store_parts4<3>(sm.v.U + vt * LP + vp, UP, e);
+            store_parts4<3>(sm.v.Z + vt * LP + vp, UP, z);
+            store_parts4<NP>(sm.v.Y + vt * LP + vp, UP, y);
             if (tt0 == 0) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) hdh += h0[v] * g0[v] + h1[v] * g1[v];
@@ -390,7 +343,7 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
             if (g == 0) sRow[sig][t] = wrow;
             if (i == 0) *reinterpret_cast<v4f*>(&sCol[tau][16 * sig + 4 * g]) = wcol;
         });
-        db = GW == 16 ? sum_over_row(db) : sum_over_half_row(db);
+        db = sum_over_half_row(db);  // the GW threads of a token row
         if (tid % GW == 0 && vt < all) d_beta[(row0 + vt) * d.H + h] = vt < L ? db : 0.0f;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {  // dS, then dKK
@@ -425,7 +378,9 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
                 }
                 pre = __shfl_up(pre, 1);
                 if (lane == 0) pre = 0.0;
-                const double out = suf + pre + static_cast<double>(sCf[3 * DL]) * hd;
+                double out = suf + pre + static_cast<double>(sCf[3 * DL]) * hd;
+                // a state forgotten at once: exactly zero, where the sums leave their rounding
+                if (sG[lane] - (lane > 0 ? sG[lane - 1] : 0.0) < -1000.0) out = 0.0;
                 if (lane < all) d_g[(row0 + lane) * d.H + h] = lane < L ? static_cast<float>(out) : 0.0f;
             }
             if (act) {
@@ -485,13 +440,12 @@ hipError_t grad_io(const DeltaShape& d, const DeltaBufs& f, hipStream_t st) {
     a.dZ = f.dZ;
     T *dq = static_cast<T*>(f.d_q), *dk = static_cast<T*>(f.d_k), *dv = static_cast<T*>(f.d_v);
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.HK * d.N));
-    constexpr int GW = 8;
     auto run = [&](auto r) {
         constexpr int R = decltype(r)::value;
         if (d.H == d.HK)
-            k_delta_grad<IO, R, false, GW><<<grid, 64 * GW, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta);
+            k_delta_grad<IO, R, false><<<grid, 64 * GW, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta);
         else
-            k_delta_grad<IO, R, true, GW><<<grid, 64 * GW, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta);
+            k_delta_grad<IO, R, true><<<grid, 64 * GW, 0, st>>>(d, a, dq, dk, dv, f.d_g, f.d_beta);
         return hipGetLastError();
     };
     switch (d.R) {

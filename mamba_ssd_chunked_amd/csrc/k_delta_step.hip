@@ -7,6 +7,8 @@
 // consecutive lanes, which reduce S k and S q by butterflies; a thread's state loads are all issued
 // before their first use, and each thread loads its slice of k and q once.  The state is updated
 // in place: each element is read and written by the same thread.
+#include <type_traits>
+
 #include "ssd_device.hpp"
 #include "ssd_launch.hpp"
 
@@ -18,7 +20,7 @@ __device__ __forceinline__ float dot4(v4f a, v4f b) { return a[0] * b[0] + a[1] 
 
 }  // namespace
 
-// R4 = dstate / 4 lanes per state row; K passes of NT / R4 rows per workgroup (blockIdx.y picks them).
+// R4 = dstate / 4 lanes per state row; K passes of NT / R4 rows, a workgroup per (b, h).
 template <class IO, int R4, int K>
 __global__ __launch_bounds__(NT) void k_delta_step(DeltaShape d, int nslots, const typename IO::T* __restrict__ q,
                                                    const typename IO::T* __restrict__ k,
@@ -30,7 +32,7 @@ __global__ __launch_bounds__(NT) void k_delta_step(DeltaShape d, int nslots, con
     const int64_t bh = blockIdx.x;
     const int h = static_cast<int>(bh % d.H), b = static_cast<int>(bh / d.H);
     const int c4 = threadIdx.x % R4;
-    const int row0 = static_cast<int>(blockIdx.y) * (ROWS * K) + threadIdx.x / R4;
+    const int row0 = threadIdx.x / R4;
     const int slot = slots ? slots[b] : b;
     if (slot < 0 || slot >= nslots) {  // an idle row
 #pragma unroll
@@ -79,22 +81,21 @@ template <class IO, int R4>
 hipError_t step_r(const DeltaShape& d, int nslots, const void* q, const void* k, const void* v, const float* g,
                   const float* beta, float* state, const int32_t* slots, void* y, hipStream_t st) {
     using T = typename IO::T;
-    constexpr int ROWS = NT / R4;
-    const int64_t bh = static_cast<int64_t>(d.B) * d.H;
-    int K = d.P > ROWS ? d.P / ROWS : 1;
-    const int per = K;
-    const dim3 grid(static_cast<unsigned>(bh), static_cast<unsigned>(per / K));
-    const T *qq = static_cast<const T*>(q), *kk = static_cast<const T*>(k), *vv = static_cast<const T*>(v);
-    T* yy = static_cast<T*>(y);
-    switch (K) {
-        case 1: k_delta_step<IO, R4, 1><<<grid, NT, 0, st>>>(d, nslots, qq, kk, vv, g, beta, state, slots, yy); break;
-        case 2: k_delta_step<IO, R4, 2><<<grid, NT, 0, st>>>(d, nslots, qq, kk, vv, g, beta, state, slots, yy); break;
-        case 4: k_delta_step<IO, R4, 4><<<grid, NT, 0, st>>>(d, nslots, qq, kk, vv, g, beta, state, slots, yy); break;
-        case 8: k_delta_step<IO, R4, 8><<<grid, NT, 0, st>>>(d, nslots, qq, kk, vv, g, beta, state, slots, yy); break;
-        case 16: k_delta_step<IO, R4, 16><<<grid, NT, 0, st>>>(d, nslots, qq, kk, vv, g, beta, state, slots, yy); break;
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H));
+    auto run = [&](auto p) {
+        constexpr int ROWS = NT / R4, P = decltype(p)::value;
+        k_delta_step<IO, R4, (P > ROWS ? P / ROWS : 1)>
+            <<<grid, NT, 0, st>>>(d, nslots, static_cast<const T*>(q), static_cast<const T*>(k),
+                                  static_cast<const T*>(v), g, beta, state, slots, static_cast<T*>(y));
+        return hipGetLastError();
+    };
+    switch (d.P) {
+        case 16: return run(std::integral_constant<int, 16>{});
+        case 32: return run(std::integral_constant<int, 32>{});
+        case 64: return run(std::integral_constant<int, 64>{});
+        case 128: return run(std::integral_constant<int, 128>{});
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
 template <class IO>

@@ -463,16 +463,13 @@ def _raw_stream(stream) -> int:
 
 
 def _strided(t: torch.Tensor, name: str, dtype, shape):
-    """(address, element strides of all axes but the last) of a device tensor whose last axis is
-    contiguous; axes of one element get stride 0."""
+    """(address, element strides of all axes but the last) of a tensor whose last axis is contiguous; axes of one element get stride 0."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
     *strides, last = t.stride()
     if last != 1 and t.numel() and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
@@ -487,6 +484,8 @@ def _delta_args(q, k, v, scale):
     io = _io_of(q, "q")
     (pq, sq), (pk, sk), (pv, sv) = (_strided(q, "q", q.dtype, q.shape), _strided(k, "k", q.dtype, q.shape),
                                     _strided(v, "v", q.dtype, v.shape))
+    if not (q.is_cuda and k.is_cuda and v.is_cuda):
+        raise ValueError("q, k and v must be device tensors")
     b, *seq, hk, r = q.shape
     h, p = v.shape[-2:]
     if not seq:
