@@ -38,7 +38,8 @@ struct DeltaScan {
     float *final_state, *d_init;
     float* coef;
     uint16_t *M, *P, *NT, *Kp, *Qp;
-    float *H, *E, *dH, *dZ;
+    float *H, *E, *dH, *dZ, *carry;
+    int segs, seg_chunks;  // segments of the chunk axis, and their chunks
 };
 
 template <int N>

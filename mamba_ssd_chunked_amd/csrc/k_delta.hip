@@ -329,7 +329,9 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
 
 namespace {
 
-enum ScanMode { kOutputs, kRecord, kReverse };
+// kOutputs: y and the final state; kCarry: what a segment does to the state; kRecord and kReverse: the
+// backward's two recurrences.
+enum ScanMode { kOutputs, kCarry, kRecord, kReverse };
 
 // Loading waves of a scan workgroup: a wave has at most 63 loads under way, and a chunk of fp32
 // operands is twice that.
@@ -348,6 +350,13 @@ __host__ __device__ constexpr int scan_loaders() { return in_parts<IO>() == 1 ? 
 // into the buffer that its predecessor has just left: the phases of a chunk are ordered so that
 // between the last read of a buffer and the first read of its next contents lies another phase's
 // matrix work.  They count their own loads; the computing waves meet them at barriers only.
+//
+// Where few heads leave most of the chip idle, the forward's chunks are cut into segments that run
+// side by side.  A segment maps its entry state by rows: h -> h T + b, the same T [r, r] for every
+// row.  kCarry runs the recurrence through each segment but the last, on p more rows than r: the
+// value columns from zero, which gives b, and r columns with v = 0 from the rows of the identity,
+// which gives T (of the first segment only the value columns, from init).  k_delta_join then
+// goes from segment to segment, and the outputs start from what it leaves.
 template <class IO, int R, int W, int TM, ScanMode MODE>
 struct Scan {
     using T = typename IO::T;
@@ -360,9 +369,10 @@ struct Scan {
     static constexpr int NL = scan_loaders<IO>(), CW = W * TM;
     static constexpr int TT = 4 / TM;  // token tiles that a wave finishes for its team
     // LDS, bytes
-    static constexpr int KBYTES = NP * QT * 1024, KBUFS = MODE == kRecord ? 2 : 1;
-    static constexpr int QBYTES = MODE == kRecord ? 0 : KBYTES;
-    static constexpr int MBYTES = 3 * DTRI * 1024, PBYTES = MODE == kRecord ? 0 : NQ * DTRI * 1024;
+    static constexpr bool LEAN = MODE == kRecord || MODE == kCarry;  // neither q nor P
+    static constexpr int KBYTES = NP * QT * 1024, KBUFS = LEAN ? 2 : 1;
+    static constexpr int QBYTES = LEAN ? 0 : KBYTES;
+    static constexpr int MBYTES = 3 * DTRI * 1024, PBYTES = LEAN ? 0 : NQ * DTRI * 1024;
     static constexpr int VBYTES = DL * 16 * W * sizeof(T);
     static constexpr int oK = 0, oQ = oK + KBUFS * KBYTES, oM = oQ + QBYTES, oP = oM + MBYTES, oV = oP + PBYTES,
                          oC = oV + VBYTES, oX = oC + 2 * 4 * DCF, LDS = oX + (TM > 1 ? CW * 4096 : 0);
@@ -375,6 +385,7 @@ struct Scan {
     const DeltaShape& d;
     const DeltaScan<T>& a;
     int lane, w, tm, i, g, pt, p0, pw, h, b, hk, chunks, len;
+    int seg, c0, c1;  // the segment and its chunks
     int64_t bh;
 
     __device__ Scan(char* smem, const DeltaShape& dd, const DeltaScan<T>& aa, int64_t blk) : sm(smem), d(dd), a(aa) {
@@ -385,14 +396,37 @@ struct Scan {
         pt = w / TM;  // tile of the workgroup
         tm = w % TM;  // place in its team
         const int pbs = d.P / (16 * W);
-        pw = static_cast<int>(blk % pbs) * 16 * W;  // the workgroup's first column
-        p0 = pw + 16 * pt;                          // the team's
-        bh = blk / pbs;
+        seg = 0;
+        if constexpr (MODE == kCarry) {
+            const int all = pbs + d.R / (16 * W), per = pbs + (a.segs - 2) * all;
+            int at = static_cast<int>(blk % per);
+            bh = blk / per;
+            if (at >= pbs) {
+                seg = 1 + (at - pbs) / all;
+                at = (at - pbs) % all;
+            }
+            pw = at * 16 * W;
+        } else {
+            pw = static_cast<int>(blk % pbs) * 16 * W;  // the workgroup's first column
+            bh = blk / pbs;
+            if constexpr (MODE == kOutputs) {
+                seg = static_cast<int>(bh % a.segs);
+                bh /= a.segs;
+            }
+        }
+        p0 = pw + 16 * pt;  // the team's
         h = static_cast<int>(bh % d.H);
         b = static_cast<int>(bh / d.H);
         hk = h / (d.H / d.HK);
         len = a.len ? static_cast<int>(a.len[b]) : d.S;
         chunks = (len + DL - 1) / DL;
+        c0 = 0;
+        c1 = chunks;
+        if constexpr (MODE == kOutputs || MODE == kCarry) {
+            c0 = seg * a.seg_chunks;
+            if (c0 > chunks) c0 = chunks;
+            if (c1 > c0 + a.seg_chunks) c1 = c0 + a.seg_chunks;
+        }
     }
 
     // -------------------------------------------------------------- loads into LDS
@@ -430,7 +464,7 @@ struct Scan {
     __device__ void load_v(const T* x, int64_t sb, int64_t st, int64_t sh, int c) const {
         constexpr int U = 16 * W * sizeof(T) / 16;  // 16-byte units of a row
         const int last = (len - c * DL < DL ? len - c * DL : DL) - 1;
-        const T* base = x + b * sb + static_cast<int64_t>(c) * DL * st + h * sh + pw;
+        const T* base = x + b * sb + static_cast<int64_t>(c) * DL * st + h * sh + (MODE == kCarry && pw >= d.P ? 0 : pw);
 #pragma unroll
         for (int m = 0; m < nV; ++m) {
             const int n = unit(m, VBYTES / 1024), u = n * 64 + lane, row = u / U;
@@ -491,18 +525,31 @@ struct Scan {
 
     // -------------------------------------------------------------- states
     __device__ int row_of(int rho) const { return 32 * (tm * JW + (rho >> 1)) + 8 * g + 4 * (rho & 1); }
-    __device__ void load_state(v4f (&s)[RT], const float* src) const {
+    // This lane's row (value column p0 + i) of a state [rows, r], or null.
+    __device__ const float* state_row(const float* src, int64_t at, int rows) const {
+        return src ? src + (at * rows + p0 + i) * R : nullptr;
+    }
+    __device__ float* carry_row(int of) const {  // what segment `of` leaves
+        return const_cast<float*>(state_row(a.carry, bh * (a.segs - 1) + of, d.P + R));
+    }
+    __device__ void load_state(v4f (&s)[RT], const float* row) const {
 #pragma unroll
         for (int rho = 0; rho < RT; ++rho) {
             const int r = row_of(rho);
-            s[rho] = src && r < R ? at4(src + (bh * d.P + p0 + i) * R + r) : zero4();
+            s[rho] = row && r < R ? at4(row + r) : zero4();
         }
     }
-    __device__ void store_state(const v4f (&s)[RT], float* dst) const {
+    __device__ void unit_state(v4f (&s)[RT]) const {
+#pragma unroll
+        for (int rho = 0; rho < RT; ++rho)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) s[rho][v] = row_of(rho) + v == p0 - d.P + i ? 1.0f : 0.0f;
+    }
+    __device__ void store_state(const v4f (&s)[RT], float* row) const {
 #pragma unroll
         for (int rho = 0; rho < RT; ++rho) {
             const int r = row_of(rho);
-            if (dst && r < R) *reinterpret_cast<v4f*>(dst + (bh * d.P + p0 + i) * R + r) = s[rho];
+            if (row && r < R) *reinterpret_cast<v4f*>(row + r) = s[rho];
         }
     }
     // A chunk's state for the gradient kernel, [r, P] rows.
@@ -680,12 +727,12 @@ struct Scan {
             load_v(a.v, d.vs[0], d.vs[1], d.vs[2], c);
         };
         if constexpr (MODE == kOutputs) {
-            load_qk(oQ, a.q, a.Qp, d.qs, 0);
-            load_coef(0, 0);
-            m(0);
-            load_qk(oK, a.k, a.Kp, d.ks, 0);
-            for (int c = 0; c < chunks; ++c) {
-                const bool more = c + 1 < chunks;
+            load_qk(oQ, a.q, a.Qp, d.qs, c0);
+            load_coef(c0, c0);
+            m(c0);
+            load_qk(oK, a.k, a.Kp, d.ks, c0);
+            for (int c = c0; c < c1; ++c) {
+                const bool more = c + 1 < c1;
                 wait_barrier<nM + nV + nK>();  // q and the coefficients
                 copy_tiles<NQ * DTRI>(oP, a.P + (bh * d.N + c) * (NQ * DTRI * DTILE));
                 wait_barrier<nP>();  // M, v and k
@@ -704,11 +751,11 @@ struct Scan {
                 }
             }
         } else {
-            load_qk(oK, a.k, a.Kp, d.ks, 0);
-            load_coef(0, 0);
-            m(0);
-            for (int c = 0; c < chunks; ++c) {
-                const bool more = c + 1 < chunks;
+            load_qk(oK + (c0 & 1) * KBYTES, a.k, a.Kp, d.ks, c0);
+            load_coef(c0, c0);
+            m(c0);
+            for (int c = c0; c < c1; ++c) {
+                const bool more = c + 1 < c1;
                 wait_barrier<0>();
                 if (more) load_qk(oK + ((c + 1) & 1) * KBYTES, a.k, a.Kp, d.ks, c + 1);
                 if constexpr (TM > 1) wait_barrier<63>();
@@ -722,15 +769,23 @@ struct Scan {
     }
 
     __device__ void forward() const {
+        // a segment after which the row ends (or that starts past its end) need not be carried
+        if (MODE == kCarry && c0 + a.seg_chunks >= chunks) return;
         if (w >= CW) {
-            if (chunks > 0) load_forward();
+            if (c0 < c1) load_forward();
             return;
         }
+        const bool values = MODE != kCarry || p0 < d.P;
         v4f s[RT];
-        load_state(s, a.init);
-        int c = 0;
-        for (; c < chunks; ++c) {
-            const int kb = oK + (MODE == kRecord ? (c & 1) * KBYTES : 0);
+        if (!values)
+            unit_state(s);
+        else if (seg == 0)
+            load_state(s, state_row(a.init, bh, d.P));
+        else
+            load_state(s, MODE == kOutputs && c0 < c1 ? carry_row(seg - 1) : nullptr);
+        int c = c0;
+        for (; c < c1; ++c) {
+            const int kb = oK + (LEAN ? (c & 1) * KBYTES : 0);
             v4f x[4], y[4], u[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) x[t] = y[t] = u[t] = zero4();
@@ -747,7 +802,7 @@ struct Scan {
             team_sum(x);
             // R = v - e^G x, E = M R (value column p0 + i, tokens 16 t + 4 g + v)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) x[t] = value(t) - at4(cf + 16 * t + 4 * g) * x[t];
+            for (int t = 0; t < 4; ++t) x[t] = (values ? value(t) : zero4()) - at4(cf + 16 * t + 4 * g) * x[t];
             tri_product<true>(u, oM, x);
             v4f z[4];
             meet();  // M and v are free
@@ -787,12 +842,16 @@ struct Scan {
             }
             mfma_settle();
         }
+        if constexpr (MODE == kCarry) store_state(s, carry_row(seg));
         if constexpr (MODE == kOutputs) {
-            store_state(s, a.final_state);
+            // the segment that holds the row's last chunk, or the first one of an empty row
+            if (c1 == chunks && (c0 < c1 || seg == 0)) store_state(s, const_cast<float*>(state_row(a.final_state, bh, d.P)));
             v4f zero[TT];
 #pragma unroll
             for (int t = 0; t < TT; ++t) zero[t] = zero4();
-            for (; c < d.N; ++c) store_y(zero, c);  // chunks past the row's length
+            const int end = (seg + 1) * a.seg_chunks < d.N ? (seg + 1) * a.seg_chunks : d.N;
+            if (c < seg * a.seg_chunks) c = seg * a.seg_chunks;
+            for (; c < end; ++c) store_y(zero, c);  // chunks past the row's length
         }
     }
 
@@ -841,7 +900,7 @@ struct Scan {
             return;
         }
         v4f s[RT];
-        load_state(s, a.d_final);
+        load_state(s, state_row(a.d_final, bh, d.P));
         for (int c = chunks - 1; c >= 0; --c) {
             v4f u[4], dy[4], x[4], gq[RT];
             meet();  // P^T, q, dy and the coefficients are here
@@ -890,7 +949,7 @@ struct Scan {
             meet();  // k is free
             mfma_settle();
         }
-        store_state(s, a.d_init);
+        store_state(s, const_cast<float*>(state_row(a.d_init, bh, d.P)));
     }
 
     // A computing wave's side of a barrier: its LDS reads have returned.
@@ -905,6 +964,58 @@ __global__ __launch_bounds__(64 * (W * TM + scan_loaders<IO>()), 2) void k_delta
     using S = Scan<IO, R, W, TM, kOutputs>;
     __shared__ __align__(16) char sm[S::LDS];
     S(sm, d, a, xcd_order(blockIdx.x, gridDim.x)).forward();
+}
+
+template <class IO, int R, int W, int TM>
+__global__ __launch_bounds__(64 * (W * TM + scan_loaders<IO>()), 2) void k_delta_carry(DeltaShape d,
+                                                                                    DeltaScan<typename IO::T> a) {
+    using S = Scan<IO, R, W, TM, kCarry>;
+    __shared__ __align__(16) char sm[S::LDS];
+    S(sm, d, a, xcd_order(blockIdx.x, gridDim.x)).forward();
+}
+
+// From segment to segment, per (b, h) and 16 value columns: the state at the end of segment s,
+// H_s = H_{s-1} T_s + b_s, in the place of b_s.  Four waves share out the columns of r; the
+// products are fp32 MFMAs.
+template <int R>
+__global__ __launch_bounds__(256) void k_delta_join(DeltaShape d, const int64_t* __restrict__ len, float* carry,
+                                                    int segs, int seg_chunks) {
+    constexpr int LH = R + 4, RT = (R / 16 + 3) / 4;
+    __shared__ __align__(16) float sH[2][16 * LH];
+    const int tiles = d.P / 16;
+    const int64_t bh = blockIdx.x / tiles;
+    const int p0 = 16 * static_cast<int>(blockIdx.x % tiles);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+    const int n = len ? static_cast<int>(len[bh / d.H]) : d.S, chunks = (n + DL - 1) / DL;
+    float* of = carry + bh * (segs - 1) * static_cast<int64_t>(d.P + R) * R;
+    if (2 * seg_chunks >= chunks) return;  // nothing is carried past the first segment
+    for (int x = threadIdx.x; x < 16 * R; x += 256) sH[0][x / R * LH + x % R] = of[p0 * R + x];
+    for (int s = 1; (s + 1) * seg_chunks < chunks; ++s) {
+        of += static_cast<int64_t>(d.P + R) * R;
+        const float *H = sH[(s + 1) & 1], *T = of + d.P * R;
+        float *to = sH[s & 1], *b = of + p0 * R;
+        v4f acc[RT];
+#pragma unroll
+        for (int m = 0; m < RT; ++m) {
+            const int col = 16 * (w * RT + m) + i;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[m][v] = col < R ? b[(4 * g + v) * R + col] : 0.0f;
+        }
+        __syncthreads();
+        if (w * RT * 16 < R) {
+#pragma unroll
+            for (int k = 0; k < R; k += 4)
+#pragma unroll
+                for (int m = 0; m < RT; ++m)
+                    acc[m] = mfma16(H[i * LH + k + g], T[(k + g) * R + 16 * (w * RT + m) + i], acc[m]);
+#pragma unroll
+            for (int m = 0; m < RT; ++m) {
+                const int col = 16 * (w * RT + m) + i;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) b[(4 * g + v) * R + col] = to[(4 * g + v) * LH + col] = acc[m][v];
+            }
+        }
+    }
 }
 
 // Both recurrences of the backward: the first half of the workgroups run the reverse, which takes
@@ -949,6 +1060,9 @@ DeltaScan<typename IO::T> typed(const DeltaBufs& f) {
     a.E = f.E;
     a.dH = f.dH;
     a.dZ = f.dZ;
+    a.carry = f.carry;
+    a.segs = 1;
+    a.seg_chunks = 0;
     return a;
 }
 
@@ -965,51 +1079,87 @@ hipError_t prep_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t
     return hipGetLastError();
 }
 
+// Workgroups of one segment and one kind of work.
 template <class IO, int R, int W, int TM>
-hipError_t scan_w(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
+hipError_t scan_w(const DeltaShape& d, const DeltaBufs& f, ScanMode mode, int segs, hipStream_t st) {
     constexpr int NTHR = 64 * (W * TM + scan_loaders<IO>());
-    const auto a = typed<IO>(f);
-    const int64_t wgs = static_cast<int64_t>(d.B) * d.H * (d.P / (16 * W));
-    if (bwd)
-        k_delta_states<IO, R, W, TM><<<dim3(static_cast<unsigned>(2 * wgs)), NTHR, 0, st>>>(d, a);
-    else
-        k_delta_scan<IO, R, W, TM><<<dim3(static_cast<unsigned>(wgs)), NTHR, 0, st>>>(d, a);
+    auto a = typed<IO>(f);
+    a.segs = segs;
+    a.seg_chunks = (d.N + segs - 1) / segs;
+    const int64_t heads = static_cast<int64_t>(d.B) * d.H;
+    const int pbs = d.P / (16 * W), rbs = d.R / (16 * W);
+    if (mode == kReverse) {
+        k_delta_states<IO, R, W, TM><<<dim3(static_cast<unsigned>(2 * heads * pbs)), NTHR, 0, st>>>(d, a);
+    } else if (mode == kOutputs) {
+        k_delta_scan<IO, R, W, TM><<<dim3(static_cast<unsigned>(heads * segs * pbs)), NTHR, 0, st>>>(d, a);
+    } else if constexpr (R >= 16 * W) {
+        const int per = pbs + (segs - 2) * (pbs + rbs);
+        k_delta_carry<IO, R, W, TM><<<dim3(static_cast<unsigned>(heads * per)), NTHR, 0, st>>>(d, a);
+    } else {
+        return hipErrorInvalidValue;
+    }
     return hipGetLastError();
 }
 
+// The fewest columns per workgroup with which the workgroups still find a CU each; in fp32,
+// where a chunk is mostly matrix work, two rounds of teams of two also beat one of single waves.
 template <class IO, int R>
-hipError_t scan_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
+hipError_t scan_r(const DeltaShape& d, const DeltaBufs& f, ScanMode mode, int segs, hipStream_t st) {
     constexpr int KJ = R < 32 ? 1 : R / 32;
-    // the fewest columns per workgroup with which the workgroups still find a CU each; in fp32,
-    // where a chunk is mostly matrix work, two rounds of teams of two also beat one of single waves
-    const int64_t tiles = static_cast<int64_t>(d.B) * d.H * (d.P / 16), all = bwd ? 2 * tiles : tiles;
-    const int W = all <= 256 || d.P < 32 ? 1 : (in_parts<IO>() == 3 ? tiles : all) <= 512 || d.P < 64 ? 2 : 4;
+    const int64_t heads = static_cast<int64_t>(d.B) * d.H;
+    const int rows = mode == kCarry && d.R < d.P ? d.R : d.P;  // whole workgroups of either kind of column
+    const int64_t tiles = mode == kCarry ? heads * (d.P / 16 + (segs - 2) * ((d.P + d.R) / 16))
+                                         : heads * segs * (d.P / 16);
+    const int64_t all = mode == kReverse ? 2 * tiles : tiles;
+    const int W = all <= 256 || rows < 32 ? 1 : (in_parts<IO>() == 3 ? tiles : all) <= 512 || rows < 64 ? 2 : 4;
     const int TM = W <= 2 && KJ >= 2 ? 2 : 1;
     // scan config
     if constexpr (KJ >= 2) switch (10 * W + TM) {
-        case 12: return scan_w<IO, R, 1, 2>(d, f, bwd, st);
-        case 22: return scan_w<IO, R, 2, 2>(d, f, bwd, st);
-        case 41: return scan_w<IO, R, 4, 1>(d, f, bwd, st);
+        case 12: return scan_w<IO, R, 1, 2>(d, f, mode, segs, st);
+        case 22: return scan_w<IO, R, 2, 2>(d, f, mode, segs, st);
+        case 41: return scan_w<IO, R, 4, 1>(d, f, mode, segs, st);
     } else switch (W) {
-        case 1: return scan_w<IO, R, 1, 1>(d, f, bwd, st);
-        case 2: return scan_w<IO, R, 2, 1>(d, f, bwd, st);
-        case 4: return scan_w<IO, R, 4, 1>(d, f, bwd, st);
+        case 1: return scan_w<IO, R, 1, 1>(d, f, mode, segs, st);
+        case 2: return scan_w<IO, R, 2, 1>(d, f, mode, segs, st);
+        case 4: return scan_w<IO, R, 4, 1>(d, f, mode, segs, st);
     }
     return hipErrorInvalidValue;
+}
+
+template <class IO, int R>
+hipError_t scans(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
+    const int segs = bwd ? 1 : delta_segments(d);
+    if (segs > 1) {
+        if (hipError_t e = scan_r<IO, R>(d, f, kCarry, segs, st); e != hipSuccess) return e;
+        const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * (d.P / 16)));
+        k_delta_join<R><<<grid, 256, 0, st>>>(d, f.len, f.carry, segs, (d.N + segs - 1) / segs);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return scan_r<IO, R>(d, f, bwd ? kReverse : kOutputs, segs, st);
 }
 
 template <class IO>
 hipError_t by_r(const DeltaShape& d, const DeltaBufs& f, bool prep, bool bwd, hipStream_t st) {
     switch (d.R) {
-        case 16: return prep ? prep_r<IO, 16>(d, f, bwd, st) : scan_r<IO, 16>(d, f, bwd, st);
-        case 32: return prep ? prep_r<IO, 32>(d, f, bwd, st) : scan_r<IO, 32>(d, f, bwd, st);
-        case 64: return prep ? prep_r<IO, 64>(d, f, bwd, st) : scan_r<IO, 64>(d, f, bwd, st);
-        case 128: return prep ? prep_r<IO, 128>(d, f, bwd, st) : scan_r<IO, 128>(d, f, bwd, st);
+        case 16: return prep ? prep_r<IO, 16>(d, f, bwd, st) : scans<IO, 16>(d, f, bwd, st);
+        case 32: return prep ? prep_r<IO, 32>(d, f, bwd, st) : scans<IO, 32>(d, f, bwd, st);
+        case 64: return prep ? prep_r<IO, 64>(d, f, bwd, st) : scans<IO, 64>(d, f, bwd, st);
+        case 128: return prep ? prep_r<IO, 128>(d, f, bwd, st) : scans<IO, 128>(d, f, bwd, st);
         default: return hipErrorInvalidValue;
     }
 }
 
 }  // namespace
+
+// Enough segments for a workgroup of four tiles on every CU.  The carries cost (p + r) / p of a scan
+// without outputs, so the chain has to become a good deal shorter: at least four segments, of at
+// least eight chunks.
+int delta_segments(const DeltaShape& d) {
+    const int64_t wgs = static_cast<int64_t>(d.B) * d.H * (d.P < 64 ? 1 : d.P / 64);
+    int64_t n = wgs > 0 ? 256 / wgs : 1;
+    if (n > d.N / 8) n = d.N / 8;
+    return n < 4 ? 1 : static_cast<int>(n);
+}
 
 hipError_t launch_delta_prep(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
     return d.io == 1 ? by_r<BF16>(d, f, true, bwd, st) : by_r<F32>(d, f, true, bwd, st);

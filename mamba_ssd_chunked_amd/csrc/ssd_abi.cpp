@@ -500,7 +500,8 @@ int check_delta_lens(const char* who, const ssd::DeltaShape& d, const int64_t* v
 
 // Workspace of the delta rule: the lengths, then per chunk and head the coefficients and the
 // triangular operands (6 tiles of 512 bf16 values a part); the backward adds the other triangular
-// operands, the entry states and the gradients of the leaving states, E and dZ.
+// operands, the entry states and the gradients of the leaving states, E and dZ; a forward in
+// segments the states and transitions between them.
 size_t delta_plan(const ssd::DeltaShape& d, bool bwd, void* ws, ssd::DeltaBufs* f) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -522,6 +523,9 @@ size_t delta_plan(const ssd::DeltaShape& d, bool bwd, void* ws, ssd::DeltaBufs* 
         f->dH = reinterpret_cast<float*>(take(state * n));
         f->E = reinterpret_cast<float*>(take(rows * n));
         f->dZ = reinterpret_cast<float*>(take(rows * n));
+    } else {
+        const size_t between = static_cast<size_t>(ssd::delta_segments(d) - 1);
+        f->carry = reinterpret_cast<float*>(take(4 * between * d.B * d.H * (d.P + d.R) * d.R));
     }
     return off;
 }

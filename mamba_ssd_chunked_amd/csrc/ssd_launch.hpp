@@ -308,6 +308,7 @@ struct DeltaBufs {
     float* coef;
     uint16_t *M, *P, *NT, *Kp, *Qp;
     float *H, *E, *dH, *dZ;
+    float* carry;  // forward in segments: [b, h, segments - 1, p + r, r]
 };
 
 // Bytes of Kp and Qp each (the bf16 parts of k and q per (b, key head, chunk)); 0 where the scans
@@ -316,6 +317,9 @@ inline size_t delta_parts_bytes(const DeltaShape& d) {
     if (d.io == 1 && d.R >= 32) return 0;
     return static_cast<size_t>(d.B) * d.HK * d.N * (d.io == 1 ? 1 : 3) * 64 * (d.R < 32 ? 32 : d.R) * 2;
 }
+
+// Segments of the chunk axis that the forward runs side by side (1: it runs through).
+int delta_segments(const DeltaShape& d);
 
 // Decay factors and triangular operands of every chunk.
 hipError_t launch_delta_prep(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st);

@@ -99,6 +99,29 @@ def test_many_heads(heads, p, r, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("b,s,h,p,r,lens", [
+    (1, 2100, 1, 16, 16, None), (2, 2048, 1, 32, 32, (2048, 2047)), (1, 4160, 2, 128, 64, None),
+    (1, 4096, 4, 64, 128, None), (1, 4096, 8, 64, 128, None), (1, 2560, 6, 64, 16, None), (1, 5800, 1, 16, 128, None),
+    (5, 2600, 1, 64, 64, (2600, 0, 1, 640, 1300)), (4, 2600, 1, 16, 32, (577, 1152, 1153, 576))])
+def test_long_sequences_of_few_heads(b, s, h, p, r, lens, dtype):
+    """The chunks in segments side by side: every split, rows that end in, at and before any segment."""
+    w = ref.delta_inputs(b, s, h, h, p, r, seed=35 + s, dtype=dtype)
+    w["g"] *= 0.05  # the first segments are not forgotten by the last one
+    pick = [0, h - 1] if h > 1 else [0]
+    cut = {n: t[:, pick] if n in ("init", "d_final") else t[:, :, pick] for n, t in w.items()}
+    y, final = ref.delta_rule(*(cut[n] for n in ("q", "k", "v", "g", "beta", "init")), lens)
+    if lens:
+        for i, n in enumerate(lens):
+            for t in ("q", "k", "v", "beta"):
+                w[t][i, n:] = float("nan")
+    say("case long", b, s, h, p, r, dtype)
+    got = run(dev(w), None if lens is None else list(lens), back=False)
+    check({"y": got["y"][:, :, pick], "final": got["final"][:, pick]}, {"y": y, "final": final}, f"long {s} {h}")
+    for i, n in enumerate(lens or []):
+        assert not got["y"][i, n:].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("grp", [1, 3])
 def test_ragged_rows(grp, dtype):
     """Rows of any length, an empty one and whole empty chunks: padding is never read (NaN there, and
