@@ -37,7 +37,7 @@ struct DeltaScan {
     const float *init, *d_final;
     float *final_state, *d_init;
     float* coef;
-    uint16_t *M, *P, *NT, *Kp, *Qp;
+    uint16_t *M, *P, *NT;
     float *H, *E, *dH, *dZ, *carry;
     int segs, seg_chunks;  // segments of the chunk axis, and their chunks
 };

@@ -28,10 +28,10 @@ namespace {
 
 constexpr int CS = DL + 4;  // LDS row stride of a 64 x 64 fp32 matrix
 
-// Whether the scans read q and k as bf16 parts that the preparation wrote (fp32 io, or rows
-// shorter than an operand) rather than from the caller's tensors.
+// Whether the scans' loading waves take q and k through registers, to cut them into bf16 parts (fp32
+// io) or to fill up rows shorter than an operand, rather than straight into LDS.
 template <class IO, int R>
-__host__ __device__ constexpr bool stage_parts() { return in_parts<IO>() == 3 || R < 32; }
+__host__ __device__ constexpr bool through_registers() { return in_parts<IO>() == 3 || R < 32; }
 
 // Below this a log decay counts as this: exp() of either is zero in fp32, and differences of
 // cumulative sums stay finite where g is -inf (a state that is forgotten at once).
@@ -141,8 +141,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
                                                     const float* __restrict__ beta,
                                                     const int64_t* __restrict__ len,
                                                     float* __restrict__ coef, uint16_t* __restrict__ Mo,
-                                                    uint16_t* __restrict__ Po, uint16_t* __restrict__ No,
-                                                    uint16_t* __restrict__ Kp, uint16_t* __restrict__ Qp) {
+                                                    uint16_t* __restrict__ Po, uint16_t* __restrict__ No) {
     using T = typename IO::T;
     constexpr int NP = in_parts<IO>(), KJ = R < 32 ? 1 : R / 32;
     constexpr int NY = BWD ? 3 : (NP == 1 ? 2 : 3);
@@ -205,17 +204,6 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
 #pragma unroll
         for (int n = 0; n < NP; ++n)
             *reinterpret_cast<b8v*>(sm + ((n * 4 + w) * KJ + j) * 1024 + lane * 16) = kw[j].p[n];
-        if constexpr (stage_parts<IO, R>()) {
-            if (h == hk * (d.H / d.HK)) {  // one value head writes the parts of its key head
-                const int64_t at = ((static_cast<int64_t>(b) * d.HK + hk) * d.N + c) * (NP * 4 * KJ * DTILE) +
-                                   (w * KJ + j) * DTILE + tile_slot(i, g) * 8;
-#pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    *reinterpret_cast<b8v*>(Kp + at + n * (4 * KJ * DTILE)) = kw[j].p[n];
-                    *reinterpret_cast<b8v*>(Qp + at + n * (4 * KJ * DTILE)) = qw[j].p[n];
-                }
-            }
-        }
     }
     __syncthreads();
     // K K^T as D[s][t] (lane token 16 w + i, sources 16 sg + 4 g + v), Q K^T the same way or, for
@@ -362,7 +350,7 @@ struct Scan {
     using T = typename IO::T;
     static constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, KJ = RP / 32;
     static constexpr int JW = KJ / TM, RT = RP / 16 / TM;  // steps of r and state tiles of one wave
-    static constexpr bool PARTS = stage_parts<IO, R>();
+    static constexpr bool CUT = through_registers<IO, R>();
     // parts of y's operands: an output rounded to bf16 needs no third part (2^-17 of it)
     static constexpr int NQ = MODE == kOutputs && NP == 1 ? 2 : 3;
     static constexpr int QT = 4 * KJ;  // tiles per part
@@ -378,7 +366,7 @@ struct Scan {
                          oC = oV + VBYTES, oX = oC + 2 * 4 * DCF, LDS = oX + (TM > 1 ? CW * 4096 : 0);
     // loads of one loading wave
     static constexpr int per(int n) { return (n + NL - 1) / NL; }
-    static constexpr int nK = per(NP * QT), nQ = nK, nM = per(3 * DTRI), nP = per(NQ * DTRI), nV = per(VBYTES / 1024),
+    static constexpr int nK = CUT ? 0 : per(QT), nQ = nK, nM = per(3 * DTRI), nP = per(NQ * DTRI), nV = per(VBYTES / 1024),
                          nC = 1;
 
     char* sm;
@@ -441,23 +429,35 @@ struct Scan {
         for (int m = 0; m < per(N); ++m) load_to_lds(src + unit(m, N) * DTILE + lane * 8, dst + unit(m, N) * 1024);
     }
     // Tokens of chunk c of q or k.  Rows past the length repeat its last row: what they feed is
-    // multiplied by the zeros of beta and e^G there.
-    __device__ void load_qk(int at, const T* x, const uint16_t* parts, const int64_t (&stride)[3], int c) const {
-        if constexpr (PARTS) {
-            copy_tiles<NP * QT>(at, parts + ((static_cast<int64_t>(b) * d.HK + hk) * d.N + c) * (NP * QT * DTILE));
-        } else {
-            const int gs = lane >> 4, is = (lane & 15) ^ (4 * gs);
-            const int last = (len - c * DL < DL ? len - c * DL : DL) - 1;
-            const T* base = x + b * stride[0] + static_cast<int64_t>(c) * DL * stride[1] + hk * stride[2] + 8 * gs;
-            const uint32_t dst = lds_addr(sm) + at;
+    // multiplied by the zeros of beta and e^G there.  f(this wave's m-th tile, the tile, the address).
+    template <class F>
+    __device__ void each_qk(const T* x, const int64_t (&stride)[3], int c, F&& f) const {
+        const int gs = lane >> 4, is = (lane & 15) ^ (4 * gs);
+        const int last = (len - c * DL < DL ? len - c * DL : DL) - 1;
+        const T* base = x + b * stride[0] + static_cast<int64_t>(c) * DL * stride[1] + hk * stride[2] + (8 * gs < R ? 8 * gs : 0);
 #pragma unroll
-            for (int tau = 0; tau < 4; ++tau) {
-                const int row = 16 * tau + is;
-                const T* src = base + (row < last ? row : last) * stride[1];
+        for (int m = 0; m < QT / NL; ++m) {
+            const int tile = w - CW + m * NL, tau = tile / KJ, j = tile % KJ, row = 16 * tau + is;
+            f(m, tile, base + (row < last ? row : last) * stride[1] + 32 * j);
+        }
+    }
+    __device__ void load_qk(int at, const T* x, const int64_t (&stride)[3], int c) const {
+        const uint32_t dst = lds_addr(sm) + at;
+        each_qk(x, stride, c, [&](int, int tile, const T* src) { load_to_lds(src, dst + tile * 1024); });
+    }
+    // The same through registers: fetched a chunk ahead, cut and written when the buffer is free.
+    typedef T raw8 __attribute__((ext_vector_type(8)));
+    typedef raw8 Ahead[QT / NL];
+    __device__ void fetch_qk(Ahead& r, const T* x, const int64_t (&stride)[3], int c) const {
+        each_qk(x, stride, c, [&](int m, int, const T* src) { r[m] = *reinterpret_cast<const raw8*>(src); });
+    }
+    __device__ void put_qk(int at, const Ahead& r) const {
 #pragma unroll
-                for (int j = 0; j < KJ; ++j)
-                    if (NL == 1 || (tau * KJ + j) % NL == w - CW) load_to_lds(src + 32 * j, dst + (tau * KJ + j) * 1024);
-            }
+        for (int m = 0; m < QT / NL; ++m) {
+            const auto x = parts_of<IO>(r[m], R >= 32 || lane < 2 * R);  // 16 lanes for 8 columns
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+                *reinterpret_cast<b8v*>(sm + at + (n * QT + w - CW + m * NL) * 1024 + lane * 16) = x.p[n];
         }
     }
     // Tokens of chunk c of v or dy, the workgroup's columns, row-major.
@@ -721,43 +721,75 @@ struct Scan {
         }
     }
 
+    // Waits count the loads into LDS that were issued after the ones waited for; those into registers
+    // are the compiler's to wait for, and only make these waits end later.
     __device__ void load_forward() const {
         auto m = [&](int c) {
             copy_tiles<3 * DTRI>(oM, a.M + (bh * d.N + c) * (3 * DTRI * DTILE));
             load_v(a.v, d.vs[0], d.vs[1], d.vs[2], c);
         };
+        Ahead kr, qr;
         if constexpr (MODE == kOutputs) {
-            load_qk(oQ, a.q, a.Qp, d.qs, c0);
+            if constexpr (CUT) {
+                fetch_qk(qr, a.q, d.qs, c0);
+                fetch_qk(kr, a.k, d.ks, c0);
+                put_qk(oQ, qr);
+                if (c0 + 1 < c1) fetch_qk(qr, a.q, d.qs, c0 + 1);
+            } else {
+                load_qk(oQ, a.q, d.qs, c0);
+            }
             load_coef(c0, c0);
             m(c0);
-            load_qk(oK, a.k, a.Kp, d.ks, c0);
+            if constexpr (!CUT) load_qk(oK, a.k, d.ks, c0);
             for (int c = c0; c < c1; ++c) {
                 const bool more = c + 1 < c1;
                 wait_barrier<nM + nV + nK>();  // q and the coefficients
+                if constexpr (CUT) put_qk(oK, kr);
                 copy_tiles<NQ * DTRI>(oP, a.P + (bh * d.N + c) * (NQ * DTRI * DTILE));
                 wait_barrier<nP>();  // M, v and k
                 if (more) {
-                    load_qk(oQ, a.q, a.Qp, d.qs, c + 1);
+                    if constexpr (CUT)
+                        put_qk(oQ, qr);
+                    else
+                        load_qk(oQ, a.q, d.qs, c + 1);
                     load_coef(c + 1, c + 1);
+                    if constexpr (CUT) fetch_qk(kr, a.k, d.ks, c + 1);
                 }
                 if constexpr (TM > 1) wait_barrier<63>();
                 wait_barrier<63>();
                 if (more) {
                     m(c + 1);
                     wait_barrier<nQ + nC + nM + nV>();  // P
-                    load_qk(oK, a.k, a.Kp, d.ks, c + 1);
+                    if constexpr (!CUT)
+                        load_qk(oK, a.k, d.ks, c + 1);
+                    else if (c + 2 < c1)
+                        fetch_qk(qr, a.q, d.qs, c + 2);
                 } else {
                     wait_barrier<0>();
                 }
             }
         } else {
-            load_qk(oK + (c0 & 1) * KBYTES, a.k, a.Kp, d.ks, c0);
+            auto buf = [](int c) { return oK + (c & 1) * KBYTES; };
+            if constexpr (CUT) {
+                fetch_qk(kr, a.k, d.ks, c0);
+                put_qk(buf(c0), kr);
+                if (c0 + 1 < c1) fetch_qk(kr, a.k, d.ks, c0 + 1);
+            } else {
+                load_qk(buf(c0), a.k, d.ks, c0);
+            }
             load_coef(c0, c0);
             m(c0);
             for (int c = c0; c < c1; ++c) {
                 const bool more = c + 1 < c1;
                 wait_barrier<0>();
-                if (more) load_qk(oK + ((c + 1) & 1) * KBYTES, a.k, a.Kp, d.ks, c + 1);
+                if (more) {
+                    if constexpr (CUT) {
+                        put_qk(buf(c + 1), kr);
+                        if (c + 2 < c1) fetch_qk(kr, a.k, d.ks, c + 2);
+                    } else {
+                        load_qk(buf(c + 1), a.k, d.ks, c + 1);
+                    }
+                }
                 if constexpr (TM > 1) wait_barrier<63>();
                 wait_barrier<63>();
                 if (more) {
@@ -875,22 +907,39 @@ struct Scan {
         const int64_t tok = static_cast<int64_t>(d.H) * d.P;
         auto front = [&](int c) {  // what the first two phases read
             copy_tiles<3 * DTRI>(oP, a.P + (bh * d.N + c) * (3 * DTRI * DTILE));
-            load_qk(oQ, a.q, a.Qp, d.qs, c);
+            if constexpr (!CUT) load_qk(oQ, a.q, d.qs, c);
             load_v(a.dy, d.S * tok, tok, d.P, c);
             load_coef(c, c);
         };
-        front(chunks - 1);
-        copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + chunks - 1) * (3 * DTRI * DTILE));
-        load_qk(oK, a.k, a.Kp, d.ks, chunks - 1);
-        for (int c = chunks - 1; c >= 0; --c) {
+        const int last = chunks - 1;
+        Ahead kr, qr;
+        if constexpr (CUT) {
+            fetch_qk(qr, a.q, d.qs, last);
+            fetch_qk(kr, a.k, d.ks, last);
+            put_qk(oQ, qr);
+            if (last > 0) fetch_qk(qr, a.q, d.qs, last - 1);
+        }
+        front(last);
+        copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + last) * (3 * DTRI * DTILE));
+        if constexpr (!CUT) load_qk(oK, a.k, d.ks, last);
+        for (int c = last; c >= 0; --c) {
             wait_barrier<nM + nK>();  // P^T, q, dy and the coefficients
-            wait_barrier<0>();        // N^T and k
-            if (c > 0) front(c - 1);
+            if constexpr (CUT) put_qk(oK, kr);
+            wait_barrier<0>();  // N^T and k
+            if (c > 0) {
+                if constexpr (CUT) put_qk(oQ, qr);
+                front(c - 1);
+                if constexpr (CUT) fetch_qk(kr, a.k, d.ks, c - 1);
+            }
             if constexpr (TM > 1) wait_barrier<63>();
             wait_barrier<63>();
             if (c > 0) copy_tiles<3 * DTRI>(oM, a.NT + (bh * d.N + c - 1) * (3 * DTRI * DTILE));
             wait_barrier<63>();
-            if (c > 0) load_qk(oK, a.k, a.Kp, d.ks, c - 1);
+            if constexpr (!CUT) {
+                if (c > 0) load_qk(oK, a.k, d.ks, c - 1);
+            } else if (c > 1) {
+                fetch_qk(qr, a.q, d.qs, c - 2);
+            }
         }
     }
 
@@ -1054,8 +1103,6 @@ DeltaScan<typename IO::T> typed(const DeltaBufs& f) {
     a.M = f.M;
     a.P = f.P;
     a.NT = f.NT;
-    a.Kp = f.Kp;
-    a.Qp = f.Qp;
     a.H = f.H;
     a.E = f.E;
     a.dH = f.dH;
@@ -1071,11 +1118,11 @@ hipError_t prep_r(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t
     const auto a = typed<IO>(f);
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * d.N));
     if (bwd)
-        k_delta_prep<IO, R, true><<<grid, 256, 0, st>>>(d, a.q, a.k, f.g, f.beta, a.len, a.coef, a.M, a.P, a.NT,
-                                                    a.Kp, a.Qp);
+        k_delta_prep<IO, R, true><<<grid, 256, 0, st>>>(d, a.q, a.k, f.g, f.beta, a.len, a.coef, a.M, a.P,
+                                                    a.NT);
     else
         k_delta_prep<IO, R, false><<<grid, 256, 0, st>>>(d, a.q, a.k, f.g, f.beta, a.len, a.coef, a.M, a.P,
-                                                     nullptr, a.Kp, a.Qp);
+                                                     nullptr);
     return hipGetLastError();
 }
 

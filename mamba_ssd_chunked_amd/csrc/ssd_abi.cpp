@@ -515,8 +515,6 @@ size_t delta_plan(const ssd::DeltaShape& d, bool bwd, void* ws, ssd::DeltaBufs* 
     f->coef = reinterpret_cast<float*>(take(6 * 64 * 4 * n));
     f->M = reinterpret_cast<uint16_t*>(take(3 * tri * n));
     f->P = reinterpret_cast<uint16_t*>(take((bwd || d.io == SSD_F32 ? 3 : 2) * tri * n));
-    f->Kp = reinterpret_cast<uint16_t*>(take(ssd::delta_parts_bytes(d)));
-    f->Qp = reinterpret_cast<uint16_t*>(take(ssd::delta_parts_bytes(d)));
     if (bwd) {
         f->NT = reinterpret_cast<uint16_t*>(take(3 * tri * n));
         f->H = reinterpret_cast<float*>(take(state * n));

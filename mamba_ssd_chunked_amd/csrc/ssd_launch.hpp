@@ -298,7 +298,7 @@ struct DeltaShape {
 
 // Everything the delta kernels read and write.  len: device copy of valid_len, or null.
 // Workspace, per (b, h, chunk): coef; M, P (forward and backward), NT (backward) in bf16
-// parts; Kp, Qp; the backward's entry states H and leaving gradients dH [r, p], E and dZ [64, p].
+// parts; the backward's entry states H and leaving gradients dH [r, p], E and dZ [64, p].
 struct DeltaBufs {
     const void *q, *k, *v, *dy;
     const float *g, *beta, *init, *d_final;
@@ -306,17 +306,10 @@ struct DeltaBufs {
     void *y, *d_q, *d_k, *d_v;
     float *final_state, *d_g, *d_beta, *d_init;
     float* coef;
-    uint16_t *M, *P, *NT, *Kp, *Qp;
+    uint16_t *M, *P, *NT;
     float *H, *E, *dH, *dZ;
     float* carry;  // forward in segments: [b, h, segments - 1, p + r, r]
 };
-
-// Bytes of Kp and Qp each (the bf16 parts of k and q per (b, key head, chunk)); 0 where the scans
-// read the tensors themselves.
-inline size_t delta_parts_bytes(const DeltaShape& d) {
-    if (d.io == 1 && d.R >= 32) return 0;
-    return static_cast<size_t>(d.B) * d.HK * d.N * (d.io == 1 ? 1 : 3) * 64 * (d.R < 32 ? 32 : d.R) * 2;
-}
 
 // Segments of the chunk axis that the forward runs side by side (1: it runs through).
 int delta_segments(const DeltaShape& d);

@@ -170,18 +170,20 @@ def test_delta_pointers_lengths_and_workspace_are_refused(lib):
 
 def test_delta_workspace_plan(lib):
     """Lengths; per chunk and head 6 x 64 floats and triangular operands of 6 tiles of 512 bf16 values
-    a part (three parts; P of a bf16 forward two); fp32 or narrow keys and queries as three or one
-    parts of at least 32 columns; backward: one more triangular operand, H, dH, E and dZ."""
+    a part (three parts; P of a bf16 forward two); backward: one more triangular operand, H, dH, E and dZ."""
     up = lambda v: (v + 255) // 256 * 256  # noqa: E731
     b, s, hk, h, p, r = 2, 100, 2, 4, 32, 64
     n, tri = b * h * 2, 6 * 512 * 2
     base = up(8 * b) + up(6 * 64 * 4 * n) + up(3 * tri * n)
     more = up(3 * tri * n) + 2 * up(4 * p * r * n) + 2 * up(4 * 64 * p * n)
-    parts = 2 * up(3 * 2 * 64 * r * b * hk * 2)
     assert ssd.ssd_delta_workspace_size(dims(), False) == base + up(2 * tri * n)
     assert ssd.ssd_delta_workspace_size(dims(), True) == base + up(3 * tri * n) + more
-    assert ssd.ssd_delta_workspace_size(dims(io=0), False) == base + up(3 * tri * n) + parts
+    assert ssd.ssd_delta_workspace_size(dims(io=0), False) == base + up(3 * tri * n)
     assert ssd.ssd_delta_workspace_size(dims(s=0), True) == up(8 * b)
+    # a long sequence of few heads: 8 segments of 8 chunks, and between them p + r rows of r
+    n, one = 64, dims(b=1, s=4096, hk=1, h=1)
+    assert ssd.ssd_delta_workspace_size(one, False) == up(8) + up(6 * 64 * 4 * n) + up(3 * tri * n) + up(2 * tri * n) \
+        + up(4 * 7 * (p + r) * r)
 
 
 def test_delta_step_refusals(lib):
