@@ -1198,14 +1198,34 @@ hipError_t by_r(const DeltaShape& d, const DeltaBufs& f, bool prep, bool bwd, hi
 
 }  // namespace
 
-// Enough segments for a workgroup of four tiles on every CU.  The carries cost (p + r) / p of a scan
-// without outputs, so the chain has to become a good deal shorter: at least four segments, of at
-// least eight chunks.
+// Microseconds that `tiles` tiles of 16 state rows take for a chunk each (p = 64, r = 128), with
+// outputs or only carried: in one round of teams on their own, in one of teams on a CU by twos, or in
+// rounds of four tiles a CU (which scan_r goes by).
+static int64_t chunk_time(const DeltaShape& d, int64_t tiles, bool outputs) {
+    static const int us[2][2][3] = {{{4, 4, 5}, {4, 7, 10}}, {{2, 3, 3}, {3, 3, 4}}};
+    const int* t = us[d.io][outputs];
+    return tiles <= 256 ? t[0] : tiles <= 512 ? t[1] : t[2] * ((tiles + 1023) / 1024);
+}
+
+// The number of segments with the shortest way: of a segment the chunks, carried and then with
+// outputs, and the joins (6 us each).  A sequence is left whole unless that saves a fifth.  Whole and
+// in segments, the whole forward (p = 64, r = 128): fp32, 2048 tokens, 1 head, 156 and 75 us; 8192
+// tokens, 24 heads, 685 and 366; 65,536 tokens, 32 heads, 4.2 and 3.5 ms; bf16, 4096 tokens, 8 heads,
+// 165 and 86 us; 16,384 tokens, 32 heads, 750 and 500.
 int delta_segments(const DeltaShape& d) {
-    const int64_t wgs = static_cast<int64_t>(d.B) * d.H * (d.P < 64 ? 1 : d.P / 64);
-    int64_t n = wgs > 0 ? 256 / wgs : 1;
-    if (n > d.N / 8) n = d.N / 8;
-    return n < 4 ? 1 : static_cast<int>(n);
+    const int64_t heads = static_cast<int64_t>(d.B) * d.H, p = d.P / 16, r = d.R / 16;
+    if (d.N < 16 || heads * p > 256) return 1;  // (few chunks; heads that fill the chip)
+    int64_t best = d.N * chunk_time(d, heads * p, true) * 4 / 5;
+    int segs = 1;
+    for (int n = 3; n <= d.N / 4 && n * heads * p <= 1024; ++n) {
+        const int64_t chunks = (d.N + n - 1) / n, carried = heads * (p + (n - 2) * (p + r));
+        const int64_t way = chunks * (chunk_time(d, carried, false) + chunk_time(d, n * heads * p, true)) + 6 * n;
+        if (way < best) {
+            best = way;
+            segs = n;
+        }
+    }
+    return segs;
 }
 
 hipError_t launch_delta_prep(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
