@@ -457,9 +457,12 @@ def _address(t: Optional[torch.Tensor], name: str, dtype, numel: int, required: 
     return None
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream \
-        if stream is None or isinstance(stream, torch.cuda.Stream) else int(stream)
+def _raw_stream(stream, on: torch.Tensor) -> int:
+    """The address of a stream, for None of the current one of the device `on` lies on (asked for
+    directly: making a Stream object of it takes 2.5 us)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(on.device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _strided(t: torch.Tensor, name: str, dtype, shape):
@@ -528,7 +531,7 @@ def ssd_delta_fwd(q, k, v, g, beta, init, valid_len, y, final_state, ws, scale=N
             _host_lengths(valid_len, d.batch), _address(y, "y", q.dtype, v.numel()),
             _address(final_state, "final_state", f, state, False))
     wp, wb = _ws(ws)
-    return load_library().ssd_delta_fwd(ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream))
+    return load_library().ssd_delta_fwd(ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream, q))
 
 
 def ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, valid_len, d_q, d_k, d_v, d_g, d_beta, d_init, ws,
@@ -543,7 +546,7 @@ def ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, valid_len, d_q, d_k, d_v,
     wp, wb = _ws(ws)
     return load_library().ssd_delta_bwd(ctypes.byref(d), _address(dy, "dy", io, v.numel()),
                                         _address(d_final, "d_final", f, state, False), *qkv, *args, wp, wb,
-                                        _raw_stream(stream))
+                                        _raw_stream(stream, q))
 
 
 def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -> int:
@@ -562,7 +565,7 @@ def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -
     return load_library().ssd_delta_step(
         ctypes.byref(d), state.shape[0], *qkv, _address(g, "g", f, bh), _address(beta, "beta", f, bh),
         _address(state, "state", f, state.numel()), None if slots is None else slots.data_ptr(),
-        _address(y, "y", io, v.numel()), _raw_stream(stream))
+        _address(y, "y", io, v.numel()), _raw_stream(stream, q))
 
 
 def ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream=None) -> int:
@@ -575,7 +578,7 @@ def ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream=None) 
         rows, width, _io_of(x, "x"), eps, _address(x, "x", io, n), _address(residual, "residual", io, n, False),
         _address(weight, "weight", torch.float32, width), int(group), _address(s, "s", io, n, False),
         _address(y, "y", io, n, False), _address(y8, "y8", torch.float8_e4m3fn, n, False),
-        _address(scale, "scale", torch.float32, rows * groups, False), _raw_stream(stream))
+        _address(scale, "scale", torch.float32, rows * groups, False), _raw_stream(stream, x))
 
 
 def ssd_rms_norm_workspace_size(rows, width) -> int:
@@ -593,7 +596,7 @@ def ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream=None) ->
         n // width if width else 0, width, _io_of(s, "s"), eps, _address(dy, "dy", io, n), _address(s, "s", io, n),
         _address(d_s, "d_s", io, n, False), _address(weight, "weight", torch.float32, width),
         _address(d_x, "d_x", io, n), _address(d_weight, "d_weight", torch.float32, width), wp, wb,
-        _raw_stream(stream))
+        _raw_stream(stream, s))
 
 
 # ------------------------------------------------------------ allocating helpers
@@ -786,7 +789,7 @@ def delta_rule(q, k, v, g, beta, init=None, valid_len=None, scale=None, want_fin
     are read in place), log decay g and write strength beta ``[b, s, h]`` fp32, init ``[b, h, p, r]``
     fp32 or None, valid_len host int64 ``[b]`` (or a list) or None, scale None for ``1 / sqrt(r)``."""
     with _allocating_on(stream):
-        y = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        y = v.new_empty(v.shape)
         final = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), dtype=torch.float32,
                             device=q.device) if want_final else None
         ws = delta_workspace(q, k, v, False) if ws is None else ws
@@ -800,7 +803,7 @@ def delta_rule_bwd(dy, q, k, v, g, beta, init=None, d_final=None, valid_len=None
     """Gradients of ``<dy, y> + <d_final, final_state>`` of delta_rule, from its inputs: returns
     dict(d_q, d_k, d_v, d_g, d_beta, d_init)."""
     with _allocating_on(stream):
-        new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+        new = lambda t: t.new_empty(t.shape)  # noqa: E731
         out = dict(d_q=new(q), d_k=new(k), d_v=new(v), d_g=new(g), d_beta=new(beta),
                    d_init=torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]),
                                       dtype=torch.float32, device=q.device) if want_d_init else None)
@@ -816,7 +819,7 @@ def delta_step(q, k, v, g, beta, state, slots=None, scale=None, stream=None):
     v ``[b, h, p]``, g, beta ``[b, h]``; state ``[nslots, h, p, r]`` is updated in place; slots (device
     int32 ``[b]``) names each row's slot, negative for an idle row.  Returns y ``[b, h, p]``."""
     with _allocating_on(stream):
-        y = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        y = v.new_empty(v.shape)
         _check(ssd_delta_step(q, k, v, g, beta, state, slots, y, scale, stream), "ssd_delta_step")
     return y
 
