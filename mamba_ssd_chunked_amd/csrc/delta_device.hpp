@@ -157,6 +157,29 @@ __device__ __forceinline__ void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N < 63 ? N : 63) : "memory");
 }
 
+// Sum over N = 4, 8, 16 or 32 consecutive lanes, in all of them: inside a row of sixteen by the
+// vector unit's own lane moves (mirrored halves, then swaps in pairs; rotations of a whole row).
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+template <int N>
+__device__ __forceinline__ float sum_over_lanes(float x) {
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32);
+    if constexpr (N >= 16) {
+        x += moved<0x128>(x);
+        x += moved<0x124>(x);
+        x += moved<0x122>(x);
+        x += moved<0x121>(x);
+        if constexpr (N == 32) x += __shfl_xor(x, 16);
+    } else {
+        if constexpr (N == 8) x += moved<0x141>(x);  // lane 7 - i
+        x += moved<0x4e>(x);                         // lane i ^ 2
+        x += moved<0xb1>(x);                         // lane i ^ 1
+    }
+    return x;
+}
+
 // LDS order of a 64-token matrix [64, r] of bf16: 16 x 32 tiles (token tile tau, step j), each
 // a kilobyte: the eight values r = 32 j + 8 g .. of token 16 tau + i at 16-byte slot
 // 16 g + (i ^ 4 g).  A tile is then one lane-linear operand read (rows), and the four rows x four

@@ -43,23 +43,6 @@ __device__ __forceinline__ void store_parts4(uint16_t* dst, int part_stride, v4f
                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
     }
 }
-// Sum over the sixteen lanes of a row, in all of them: rotations inside the row.
-template <int CTRL>
-__device__ __forceinline__ float row_rotated(float x) {
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float sum_over_row(float x) {
-    x += row_rotated<0x128>(x);
-    x += row_rotated<0x124>(x);
-    x += row_rotated<0x122>(x);
-    return x + row_rotated<0x121>(x);
-}
-// The same over each half of a row (mirrored within it, then swapped in fours, pairs, ones).
-__device__ __forceinline__ float sum_over_half_row(float x) {
-    x += row_rotated<0x141>(x);  // lane 7 - i of the half
-    x += row_rotated<0x4e>(x);   // lane i ^ 2
-    return x + row_rotated<0xb1>(x);  // lane i ^ 1
-}
 template <int N>
 __device__ __forceinline__ v4f sum_parts4(const uint16_t* src, int part_stride) {
     v4f x = zero4();
@@ -312,7 +295,7 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
             }
         }
         if (tt0 == 0) {
-            hdh = sum_over_row(hdh);
+            hdh = sum_over_lanes<16>(hdh);
             hdh = sum_over_g(hdh);
         }
         if (lane == 0) sDot[w] = hdh;
@@ -335,7 +318,7 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
                 const float es = s < t ? e2 : 0.0f;
                 const float x = es * (d.scale * dP[m][v] * qk[v] - dA[m][v] * kk[v]);
                 wrow += x;
-                wcol[v] = sum_over_row(x);
+                wcol[v] = sum_over_lanes<16>(x);
                 dP[m][v] *= d.scale * e2;
                 dA[m][v] *= -es;
             }
@@ -343,7 +326,7 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
             if (g == 0) sRow[sig][t] = wrow;
             if (i == 0) *reinterpret_cast<v4f*>(&sCol[tau][16 * sig + 4 * g]) = wcol;
         });
-        db = sum_over_half_row(db);  // the GW threads of a token row
+        db = sum_over_lanes<8>(db);  // the GW threads of a token row
         if (tid % GW == 0 && vt < all) d_beta[(row0 + vt) * d.H + h] = vt < L ? db : 0.0f;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {  // dS, then dKK

@@ -9,7 +9,7 @@
 // in place: each element is read and written by the same thread.
 #include <type_traits>
 
-#include "ssd_device.hpp"
+#include "delta_device.hpp"
 #include "ssd_launch.hpp"
 
 namespace ssd {
@@ -20,15 +20,15 @@ __device__ __forceinline__ float dot4(v4f a, v4f b) { return a[0] * b[0] + a[1] 
 
 }  // namespace
 
-// R4 = dstate / 4 lanes per state row; K passes of NT / R4 rows, a workgroup per (b, h).
-template <class IO, int R4, int K>
+// R4 = dstate / 4 lanes per state row, P = headdim; a workgroup per (b, h).
+template <class IO, int R4, int P>
 __global__ __launch_bounds__(NT) void k_delta_step(DeltaShape d, int nslots, const typename IO::T* __restrict__ q,
                                                    const typename IO::T* __restrict__ k,
                                                    const typename IO::T* __restrict__ v,
                                                    const float* __restrict__ g, const float* __restrict__ beta,
                                                    float* __restrict__ state, const int32_t* __restrict__ slots,
                                                    typename IO::T* __restrict__ y) {
-    constexpr int ROWS = NT / R4;
+    constexpr int ROWS = NT / R4, K = P > ROWS ? P / ROWS : 1;  // rows of a pass, passes
     const int64_t bh = blockIdx.x;
     const int h = static_cast<int>(bh % d.H), b = static_cast<int>(bh / d.H);
     const int c4 = threadIdx.x % R4;
@@ -37,17 +37,17 @@ __global__ __launch_bounds__(NT) void k_delta_step(DeltaShape d, int nslots, con
     if (slot < 0 || slot >= nslots) {  // an idle row
 #pragma unroll
         for (int m = 0; m < K; ++m)
-            if (c4 == 0 && row0 + m * ROWS < d.P) io<IO>::st(y, bh * d.P + row0 + m * ROWS, 0.0f);
+            if (c4 == 0 && row0 + m * ROWS < P) io<IO>::st(y, bh * P + row0 + m * ROWS, 0.0f);
         return;
     }
     const int hk = h / (d.H / d.HK);
-    v4f* S = reinterpret_cast<v4f*>(state) + (static_cast<int64_t>(slot) * d.H + h) * d.P * R4;
+    v4f* S = reinterpret_cast<v4f*>(state) + (static_cast<int64_t>(slot) * d.H + h) * P * R4;
     v4f s[K];
     float vv[K];
 #pragma unroll
     for (int m = 0; m < K; ++m) {
         const int p = row0 + m * ROWS;
-        if (p < d.P) {
+        if (p < P) {
             s[m] = __builtin_nontemporal_load(S + p * R4 + c4);
             vv[m] = io<IO>::ld(v, b * d.vs[0] + h * d.vs[2] + p);
         }
@@ -56,21 +56,15 @@ __global__ __launch_bounds__(NT) void k_delta_step(DeltaShape d, int nslots, con
     const v4f q4 = io<IO>::ld4(q, b * d.qs[0] + hk * d.qs[2] + 4 * c4);
     const float a = exp2_of(static_cast<double>(g[bh]) * kLog2e), be = beta[bh];
     float kq = dot4(k4, q4);
-#pragma unroll
-    for (int o = R4 / 2; o >= 1; o >>= 1) kq += __shfl_xor(kq, o);
+    kq = sum_over_lanes<R4>(kq);
 #pragma unroll
     for (int m = 0; m < K; ++m) {
         const int p = row0 + m * ROWS;
-        if (p < d.P) {  // whole rows are in or out together
-            float sk = dot4(s[m], k4), sq = dot4(s[m], q4);
-#pragma unroll
-            for (int o = R4 / 2; o >= 1; o >>= 1) {
-                sk += __shfl_xor(sk, o);
-                sq += __shfl_xor(sq, o);
-            }
+        if (p < P) {  // whole rows are in or out together
+            const float sk = sum_over_lanes<R4>(dot4(s[m], k4)), sq = sum_over_lanes<R4>(dot4(s[m], q4));
             const float u = be * (vv[m] - a * sk);
             __builtin_nontemporal_store(a * s[m] + u * k4, S + p * R4 + c4);
-            if (c4 == 0) io<IO>::st(y, bh * d.P + p, d.scale * (a * sq + u * kq));
+            if (c4 == 0) io<IO>::st(y, bh * P + p, d.scale * (a * sq + u * kq));
         }
     }
 }
@@ -83,8 +77,7 @@ hipError_t step_r(const DeltaShape& d, int nslots, const void* q, const void* k,
     using T = typename IO::T;
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H));
     auto run = [&](auto p) {
-        constexpr int ROWS = NT / R4, P = decltype(p)::value;
-        k_delta_step<IO, R4, (P > ROWS ? P / ROWS : 1)>
+        k_delta_step<IO, R4, decltype(p)::value>
             <<<grid, NT, 0, st>>>(d, nslots, static_cast<const T*>(q), static_cast<const T*>(k),
                                   static_cast<const T*>(v), g, beta, state, slots, static_cast<T*>(y));
         return hipGetLastError();

@@ -277,8 +277,10 @@ __global__ __launch_bounds__(1024) void k_rms_norm_weight(const float* __restric
     const int c = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int col = static_cast<int>(blockIdx.x) * 32 + c;
     float acc = 0.0f;
-    if (col < width)
+    if (col < width) {
+#pragma unroll 8  // as many loads under way
         for (int64_t t = run; t < teams; t += 32) acc += part[t * width + col];
+    }
     sh[run][c] = acc;
     __syncthreads();
     if (run == 0 && col < width) {
