@@ -340,8 +340,10 @@ int ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int
  *   it are not read, leave the state alone, and give y and gradients of exactly zero.
  * bf16 io: the products take the bf16 inputs as they are and everything else (states, decays, the
  * triangular inverse, sums) in fp32; y, d_q, d_k, d_v are rounded to nearest even.  Results are
- * bitwise reproducible.  No launch exceeds 2^32 work-items: batch * nheads * max(8 * (seq + 63),
- * 8 * headdim) < 2^32 (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
+ * bitwise reproducible.  A NaN or an infinity among a row's tokens spreads over its chunk of 64
+ * tokens and on from there, in that head (and d_q, d_k of its key head) only.  No launch exceeds
+ * 2^32 work-items: batch * nheads * max(8 * (seq + 63), 16 * max(headdim, 64)) < 2^32
+ * (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,
  * SSD_ERR_HIP.
  */

@@ -134,6 +134,12 @@ __device__ __forceinline__ void invert_lower(const float* C, float* X) {
 //
 // Wave w has the tokens 16 w .. + 15: their rows of K and Q stay in its registers as operands, and
 // the key rows of the others come through LDS, which the fp32 matrices take over afterwards.
+//
+// Bound by HBM: it reads q and k and writes two triangular matrices.  160 heads of 64 chunks, bf16,
+// r = 128: 0.79 GB in 139-146 us, 5.4 TB/s (with K and Q as fp32 in LDS and substitution there: 217
+// us); 32 heads of 1024 chunks, fp32: 3.9 GB in 644-664 us.  A preparation of its own doubles the
+// reads of q and k, but has the inverses, long chains of dependent steps, in 10,240 workgroups at once
+// instead of in the 160 of the scan, each before the next chunk.
 template <class IO, int R, bool BWD>
 __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename IO::T* __restrict__ q,
                                                     const typename IO::T* __restrict__ k,
@@ -338,6 +344,19 @@ __host__ __device__ constexpr int scan_loaders() { return in_parts<IO>() == 1 ? 
 // into the buffer that its predecessor has just left: the phases of a chunk are ordered so that
 // between the last read of a buffer and the first read of its next contents lies another phase's
 // matrix work.  They count their own loads; the computing waves meet them at barriers only.
+// (Computing waves that issued the loads themselves: bf16, 160 heads, 291 against 232 us; loads
+// into registers there: 1084 us.)
+//
+// Measured with outputs, p = 64, r = 128, a chunk in each launch shape: bf16 3.6 us (four single
+// waves, 160 workgroups on as many CUs, so that 96 of the 256 stand idle: 64 chunks 232 us); fp32
+// 3.4 us (one team), 6.1 us (two teams), 9.7 us (four waves).  Single waves in fp32 at 256 tiles: 4.9 ms for 1024 chunks
+// against 3.5 ms by teams.  A team's sums cost more than its shorter chain wins where the chip is
+// full of single waves.
+//
+// fp32 keys and queries are cut into parts by the loading waves: written as parts by the
+// preparation they are half as large again in every read (32 heads of 1024 chunks: preparation 1314,
+// scan 1175 us, against 683 and 1238); four loading waves beside the computing ones cost a scan that is
+// bound by the vector unit something (96 heads of 32 chunks: 165 -> 197 us, preparation 121 -> 82).
 //
 // Where few heads leave most of the chip idle, the forward's chunks are cut into segments that run
 // side by side.  A segment maps its entry state by rows: h -> h T + b, the same T [r, r] for every
@@ -1069,7 +1088,8 @@ __global__ __launch_bounds__(256) void k_delta_join(DeltaShape d, const int64_t*
 
 // Both recurrences of the backward: the first half of the workgroups run the reverse, which takes
 // about twice as long, the second half recompute the entry states and E.  Started last, the short
-// ones fill in where the chip does not hold all of them at once.
+// ones fill in where the chip does not hold all of them at once (bf16, 160 heads of 64 chunks: 630
+// us, the other way round 923).  Writes H, dH, E and dZ, 1.17 GB there, at 4.0 TB/s of all traffic.
 template <class IO, int R, int W, int TM>
 __global__ __launch_bounds__(64 * (W * TM + scan_loaders<IO>()), 2) void k_delta_states(DeltaShape d,
                                                                                      DeltaScan<typename IO::T> a) {

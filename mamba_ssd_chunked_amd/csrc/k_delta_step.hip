@@ -3,10 +3,12 @@
 // Per (batch row, value head) with the state S [p, r] of the row's slot:
 //   u = beta (v - e^g S k),   S' = e^g S + u k^T,   y = scale S' q = scale (e^g (S q) + u (k.q)).
 // Both dot products are taken of the old state in one pass, so a state element is read once and
-// written once: 8 bytes for 6 flops, bound by HBM.  A state row (r / 4 float4s) is held by r / 4
-// consecutive lanes, which reduce S k and S q by butterflies; a thread's state loads are all issued
-// before their first use, and each thread loads its slice of k and q once.  The state is updated
-// in place: each element is read and written by the same thread.
+// written once: 8 bytes for 6 flops, bound by HBM: 62 rows of 80 heads, p = 64, r = 128, take 61 us,
+// 5.3 TB/s.  (With the row count known only at run time the loads of a thread stood behind branches,
+// one at a time: 95 us; with sums through the LDS crossbar instead of lane moves as well: 101 us.)
+// A state row (r / 4 float4s) is held by r / 4 consecutive lanes, which add up S k and S q; a
+// thread's state loads are all issued before their first use, and each thread loads its slice of k
+// and q once.  The state is updated in place: each element is read and written by the same thread.
 #include <type_traits>
 
 #include "delta_device.hpp"

@@ -460,9 +460,10 @@ int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape*
     if (!pow2_in(dims->headdim, 16, 128) || !pow2_in(dims->dstate, 16, 128))
         return fail(SSD_ERR_UNSUPPORTED, "%s: headdim and dstate must be 16, 32, 64 or 128 (got %lld, %lld)", who,
                     (long long)dims->headdim, (long long)dims->dstate);
-    // a workgroup of at most 512 work-items per chunk of 64 tokens and head, and two of 4 per
-    // value column and head
-    const double per_bh = std::max(8.0 * ((double)dims->seq + 63.0), 8.0 * (double)dims->headdim);
+    // a workgroup of at most 512 work-items per chunk of 64 tokens and head; the two recurrences of
+    // the backward, 512 each for 64 value columns (or fewer) of a head
+    const double per_bh =
+        std::max(8.0 * ((double)dims->seq + 63.0), 16.0 * std::max((double)dims->headdim, 64.0));
     if (dims->batch > (1 << 30) || dims->seq > (1 << 30) || dims->nheads > (1 << 30) ||
         (double)dims->batch * dims->nheads * per_bh > ssd::kMaxGridItems)
         return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch would exceed 2^32 work-items "

@@ -7,9 +7,10 @@
 namespace ssd {
 
 // Work-items one launch may have along x: the AQL dispatch packet stores the grid
-// size in 32 bits.  No workgroup of the library has more than 256 work-items, so
-// an entry point that bounds its largest grid by this (less one workgroup for the
-// rounding up of block counts) never asks for a grid the packet cannot hold.
+// size in 32 bits.  No workgroup of the scan, moments and step kernels has more than
+// 256 work-items, so an entry point that bounds its largest grid by this (less one
+// workgroup for the rounding up of block counts) never asks for a grid the packet
+// cannot hold.  The delta rule's grids are exact numbers of workgroups.
 constexpr double kMaxGridItems = 4294967295.0 - 256.0;
 
 struct Shape {

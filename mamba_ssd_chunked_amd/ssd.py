@@ -8,7 +8,8 @@ element count for ``dims`` -- so that a wrong buffer is refused on the host
 instead of faulting on the GPU -- pass the raw pointers and return the C status
 code.  ``forward``, ``backward``, ``state_moments`` and ``state_moments_bwd``
 allocate outputs and workspace with torch and raise :class:`SsdError` on a
-nonzero status.  Every step of the computation runs in the HIP library; there
+nonzero status.  So do ``delta_rule``, ``delta_rule_bwd`` and ``delta_step`` (the gated delta
+rule) and ``rms_norm`` and ``rms_norm_bwd``; q, k and v of the delta rule may be strided.  Every step of the computation runs in the HIP library; there
 is no Python or CPU fallback, and importing a function whose library is missing
 raises immediately.
 """

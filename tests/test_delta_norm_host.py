@@ -121,7 +121,7 @@ BAD_DIMS = [(dict(io_dtype=2), DTYPE), (dict(batch=-1), SHAPE), (dict(seq=-1), S
             (dict(headdim=24), UNSUPPORTED), (dict(headdim=256), UNSUPPORTED), (dict(dstate=8), UNSUPPORTED),
             (dict(dstate=96), UNSUPPORTED), (dict(q_stride_token=-8), SHAPE), (dict(k_stride_head=4), UNSUPPORTED),
             (dict(v_stride_batch=12), UNSUPPORTED), (dict(batch=1 << 40), UNSUPPORTED), (dict(seq=1 << 40), UNSUPPORTED),
-            (dict(batch=1 << 20, seq=1 << 20), UNSUPPORTED)]
+            (dict(batch=1 << 20, seq=1 << 20), UNSUPPORTED), (dict(batch=700000, seq=1, headdim=128), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("over,code", BAD_DIMS)
