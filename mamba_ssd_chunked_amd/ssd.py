@@ -467,7 +467,8 @@ def _raw_stream(stream, on: torch.Tensor) -> int:
 
 
 def _strided(t: torch.Tensor, name: str, dtype, shape):
-    """(address, element strides of all axes but the last) of a tensor whose last axis is contiguous; axes of one element get stride 0."""
+    """(address, element strides of all axes but the last) of a tensor whose last axis is contiguous;
+    axes of one element get stride 0."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
