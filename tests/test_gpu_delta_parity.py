@@ -399,3 +399,20 @@ def test_binding_refusals_on_the_device():
         ssd.delta_step(*tok, state=w["init"][..., :32].contiguous())
     with pytest.raises(ssd.SsdError, match="slot"):
         ssd.delta_step(*tok, state=w["init"][:1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("b,s,h,p,r", [(1, 2100, 1, 16, 16), (2, 2600, 2, 64, 64), (1, 4096, 8, 64, 128), (3, 1100, 1, 128, 128)])
+def test_long_sequences_are_bitwise_reproducible(b, s, h, p, r, dtype):
+    """Segments joined in a fixed order, whatever the workspace held before."""
+    w = dev(ref.delta_inputs(b, s, h, h, p, r, seed=161, dtype=dtype))
+    a = [w[n] for n in ("q", "k", "v", "g", "beta")]
+    say("case long again", b, s, h, p, r, dtype)
+    ws = ssd.delta_workspace(*a[:3], False)
+    first = None
+    for fill in (0xff, 0, 0x3f, 0xff, 0x7b):
+        y, final = ssd.delta_rule(*a, init=w["init"], ws=ws.fill_(fill))
+        torch.cuda.synchronize()
+        first = first or (y, final)
+        assert torch.isfinite(final).all()
+        assert torch.equal(y, first[0]) and torch.equal(final, first[1])
