@@ -453,7 +453,8 @@ struct Scan {
     __device__ void each_qk(const T* x, const int64_t (&stride)[3], int c, F&& f) const {
         const int gs = lane >> 4, is = (lane & 15) ^ (4 * gs);
         const int last = (len - c * DL < DL ? len - c * DL : DL) - 1;
-        const T* base = x + b * stride[0] + static_cast<int64_t>(c) * DL * stride[1] + hk * stride[2] + (8 * gs < R ? 8 * gs : 0);
+        const T* base = x + b * stride[0] + static_cast<int64_t>(c) * DL * stride[1] + hk * stride[2] +
+                        (8 * gs < R ? 8 * gs : 0);
 #pragma unroll
         for (int m = 0; m < QT / NL; ++m) {
             const int tile = w - CW + m * NL, tau = tile / KJ, j = tile % KJ, row = 16 * tau + is;
@@ -510,7 +511,8 @@ struct Scan {
     // r = 32 (rho / 2) + 8 g + 4 (rho % 2) + v: two state tiles hold eight consecutive r per lane.
     __device__ Parts<NP> col_op(int base, int rho, int j) const {
         Parts<NP> o;
-        const int at = base + (2 * j * KJ + tm * JW + (rho >> 1)) * 1024 + tile_slot(4 * g + (i >> 2), i & 3) * 16 + (rho & 1) * 8;
+        const int at = base + (2 * j * KJ + tm * JW + (rho >> 1)) * 1024 + tile_slot(4 * g + (i >> 2), i & 3) * 16 +
+                       (rho & 1) * 8;
 #pragma unroll
         for (int n = 0; n < NP; ++n)
             o.p[n] = join8(lds_col4(reinterpret_cast<const uint16_t*>(sm + at + n * QT * 1024)),
@@ -724,7 +726,8 @@ struct Scan {
             if constexpr (TM == 1) {
                 mix<4 * terms(NQ, NQ), 3>();
                 fence();
-                mma_b(*reinterpret_cast<v4f(*)[2]>(&y[TT / 2]), u1, *reinterpret_cast<const Parts<NQ>(*)[2]>(&op[1][TT / 2]));
+                mma_b(*reinterpret_cast<v4f(*)[2]>(&y[TT / 2]), u1,
+                      *reinterpret_cast<const Parts<NQ>(*)[2]>(&op[1][TT / 2]));
             } else {
                 mma_b(y, u1, op[1]);
             }

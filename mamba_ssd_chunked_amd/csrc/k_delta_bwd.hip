@@ -275,7 +275,8 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
 #pragma unroll
             for (int m = 0; m < ITEMS; ++m) {
                 const int t = 16 * (tt0 + m) + i;
-                const int at = ((tt0 + m) * KJ + (rho >> 1)) * DTILE + tile_slot(i, 2 * (rho & 1) + (g >> 1)) * 8 + 4 * (g & 1);
+                const int at = ((tt0 + m) * KJ + (rho >> 1)) * DTILE + tile_slot(i, 2 * (rho & 1) + (g >> 1)) * 8 +
+                               4 * (g & 1);
                 const float eg = sCf[t], tail = sCf[DL + t];
                 aq[m] *= d.scale * eg;
                 akr[m] *= -eg;
