@@ -33,6 +33,12 @@ constexpr int CS = DL + 4;  // LDS row stride of a 64 x 64 fp32 matrix
 template <class IO, int R>
 __host__ __device__ constexpr bool through_registers() { return in_parts<IO>() == 3 || R < 32; }
 
+// Kilobytes of an operand tile of P: three bf16 parts, or for bf16 io's outputs its 512 fp32 values (a
+// lane's first four, then all lanes' second), which the scan cuts into parts itself: 12 KB a chunk
+// instead of 18, and the sums that make y keep all 24 bits of P.
+template <class IO>
+__host__ __device__ constexpr int p_kilobytes(bool bwd) { return bwd || in_parts<IO>() == 3 ? 3 : 2; }
+
 // Below this a log decay counts as this: exp() of either is zero in fp32, and differences of
 // cumulative sums stay finite where g is -inf (a state that is forgotten at once).
 constexpr float kMinLogDecay = -1.0e4f;
@@ -150,7 +156,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
                                                     uint16_t* __restrict__ Po, uint16_t* __restrict__ No) {
     using T = typename IO::T;
     constexpr int NP = in_parts<IO>(), KJ = R < 32 ? 1 : R / 32;
-    constexpr int NY = BWD ? 3 : (NP == 1 ? 2 : 3);
+    constexpr int PK = p_kilobytes<IO>(BWD);
     constexpr int MAT = DL * CS;
     constexpr int KB = NP * 4 * KJ * 1024, MB = (BWD ? 3 : 2) * MAT * 4;
     __shared__ __align__(16) char sm[KB > MB ? KB : MB];
@@ -233,7 +239,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
     }
     __syncthreads();
     const int t = 16 * w + i;
-    uint16_t* po = Po + ch * (NY * DTRI * DTILE);
+    uint16_t* po = Po + ch * (PK * DTRI * DTILE);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         if (s <= w) {
@@ -254,20 +260,25 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
                     const int tt = 16 * w + 4 * g + v, src = 16 * s + i;
                     qk[s][v] = src <= tt ? d.scale * qk[s][v] * exp2_of(sG[tt] - sG[src]) : 0.0f;
                 }
-                put_half<NY>(po, tri_upper(s, w / 2), lane, w & 1, qk[s]);
+                put_half<3>(po, tri_upper(s, w / 2), lane, w & 1, qk[s]);
             }
         }
     }
     if constexpr (BWD) {
-        if ((w & 1) == 0) put_half<NY>(po, tri_upper(w + 1, w / 2), lane, 0, zero4());  // above the diagonal
+        if ((w & 1) == 0) put_half<3>(po, tri_upper(w + 1, w / 2), lane, 0, zero4());  // above the diagonal
     } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (j <= w / 2) {
-                const auto pp = split44<NY>(qk[2 * j], qk[2 * j + 1]);
+                uint16_t* at = po + tri_lower(w, j) * DTILE + lane * 8;
+                if constexpr (PK == 2) {
 #pragma unroll
-                for (int n = 0; n < NY; ++n)
-                    *reinterpret_cast<b8v*>(po + (n * DTRI + tri_lower(w, j)) * DTILE + lane * 8) = pp.p[n];
+                    for (int hf = 0; hf < 2; ++hf) *reinterpret_cast<v4f*>(at + hf * DTRI * DTILE) = qk[2 * j + hf];
+                } else {
+                    const auto pp = split44<3>(qk[2 * j], qk[2 * j + 1]);
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) *reinterpret_cast<b8v*>(at + n * DTRI * DTILE) = pp.p[n];
+                }
             }
         }
     }
@@ -370,8 +381,7 @@ struct Scan {
     static constexpr int NP = in_parts<IO>(), RP = R < 32 ? 32 : R, KJ = RP / 32;
     static constexpr int JW = KJ / TM, RT = RP / 16 / TM;  // steps of r and state tiles of one wave
     static constexpr bool CUT = through_registers<IO, R>();
-    // parts of y's operands: an output rounded to bf16 needs no third part (2^-17 of it)
-    static constexpr int NQ = MODE == kOutputs && NP == 1 ? 2 : 3;
+    static constexpr int PK = p_kilobytes<IO>(MODE == kReverse);
     static constexpr int QT = 4 * KJ;  // tiles per part
     static constexpr int NL = scan_loaders<IO>(), CW = W * TM;
     static constexpr int TT = 4 / TM;  // token tiles that a wave finishes for its team
@@ -379,13 +389,13 @@ struct Scan {
     static constexpr bool LEAN = MODE == kRecord || MODE == kCarry;  // neither q nor P
     static constexpr int KBYTES = NP * QT * 1024, KBUFS = LEAN ? 2 : 1;
     static constexpr int QBYTES = LEAN ? 0 : KBYTES;
-    static constexpr int MBYTES = 3 * DTRI * 1024, PBYTES = LEAN ? 0 : NQ * DTRI * 1024;
+    static constexpr int MBYTES = 3 * DTRI * 1024, PBYTES = LEAN ? 0 : PK * DTRI * 1024;
     static constexpr int VBYTES = DL * 16 * W * sizeof(T);
     static constexpr int oK = 0, oQ = oK + KBUFS * KBYTES, oM = oQ + QBYTES, oP = oM + MBYTES, oV = oP + PBYTES,
                          oC = oV + VBYTES, oX = oC + 2 * 4 * DCF, LDS = oX + (TM > 1 ? CW * 4096 : 0);
     // loads of one loading wave
     static constexpr int per(int n) { return (n + NL - 1) / NL; }
-    static constexpr int nK = CUT ? 0 : per(QT), nQ = nK, nM = per(3 * DTRI), nP = per(NQ * DTRI), nV = per(VBYTES / 1024),
+    static constexpr int nK = CUT ? 0 : per(QT), nQ = nK, nM = per(3 * DTRI), nP = per(PK * DTRI), nV = per(VBYTES / 1024),
                          nC = 1;
 
     char* sm;
@@ -605,7 +615,7 @@ struct Scan {
     // c <- c + X s^T (SWAP: its transpose) over this wave's share of r, X = k or q in LDS, from the
     // state's parts, or parts made on the way (MAKE): a step's operands are read, and the next
     // step's parts made, while the matrix cores are at the step before.
-    template <bool SWAP, int N, bool MAKE>
+    template <bool SWAP, bool MAKE>
     __device__ void rows_product(v4f (&c)[4], int base, Parts<3> (&sp)[JW], const v4f (&s)[RT]) const {
         Parts<NP> op[2][4];
 #pragma unroll
@@ -618,16 +628,13 @@ struct Scan {
                 for (int t = 0; t < 4; ++t) op[(j + 1) & 1][t] = row_op(base, t, j + 1);
             }
             fence();
-            Parts<N> sn;
-#pragma unroll
-            for (int n = 0; n < N; ++n) sn.p[n] = sp[j].p[n];
             if constexpr (SWAP)
-                mma_b(c, sn, op[j & 1]);
+                mma_b(c, sp[j], op[j & 1]);
             else
-                mma_a(c, op[j & 1], sn);
+                mma_a(c, op[j & 1], sp[j]);
             if (MAKE && j + 1 < JW) {
                 sp[j + 1] = split44<3>(s[2 * j + 2], s[2 * j + 3]);
-                mix<4 * terms(NP, N), 176 / (4 * terms(NP, N)) / 4 + 1>();
+                mix<4 * terms(NP, 3), 176 / (4 * terms(NP, 3)) / 4 + 1>();
             }
             fence();
         }
@@ -708,29 +715,49 @@ struct Scan {
         }
     }
 
-    // y <- y + P u for this wave's token tiles
+    // An operand tile of P as it lies in LDS, and its parts.
+    struct PTile {
+        v4f x[PK];
+    };
+    __device__ PTile p_tile(int tile) const {
+        PTile o;
+#pragma unroll
+        for (int n = 0; n < PK; ++n) o.x[n] = at4(reinterpret_cast<const float*>(sm + oP + (n * DTRI + tile) * 1024 + lane * 16));
+        return o;
+    }
+    __device__ static Parts<3> p_parts(const PTile& p) {
+        if constexpr (PK == 2)
+            return split44<3>(p.x[0], p.x[1]);
+        else
+            return __builtin_bit_cast(Parts<3>, p);
+    }
+    // y <- y + P u for this wave's token tiles; what is left to cut for the second step is cut while
+    // the matrix cores are at the first
     __device__ void intra(v4f (&y)[TT], const v4f (&u)[4]) const {
-        Parts<NQ> op[2][TT];
-        const bool two = TM == 1 || tm >= TM / 2;  // tiles whose rows reach the second step
+        constexpr int T2 = TM == 1 ? 2 : 0;  // the first tile that reaches the second step
+        PTile raw[2][TT];
+        const bool two = TM == 1 || tm >= TM / 2;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) op[0][t] = tri_op<NQ>(oP, tri_lower(tm * TT + t, 0));
+        for (int t = 0; t < TT; ++t) raw[0][t] = p_tile(tri_lower(tm * TT + t, 0));
         if (two) {
 #pragma unroll
-            for (int t = TM == 1 ? 2 : 0; t < TT; ++t) op[1][t] = tri_op<NQ>(oP, tri_lower(tm * TT + t, 1));
+            for (int t = T2; t < TT; ++t) raw[1][t] = p_tile(tri_lower(tm * TT + t, 1));
         }
-        const auto u0 = split44<NQ>(u[0], u[1]);
+        Parts<3> op[TT], op1[TT - T2];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) op[t] = p_parts(raw[0][t]);
+        const auto u0 = split44<3>(u[0], u[1]);
         fence();
-        mma_b(y, u0, op[0]);
+        mma_b(y, u0, op);
         if (two) {
-            const auto u1 = split44<NQ>(u[2], u[3]);
+            const auto u1 = split44<3>(u[2], u[3]);
+#pragma unroll
+            for (int t = T2; t < TT; ++t) op1[t - T2] = p_parts(raw[1][t]);
             if constexpr (TM == 1) {
-                mix<4 * terms(NQ, NQ), 3>();
+                mix<4 * terms(3, 3), PK == 2 ? 7 : 3>();
                 fence();
-                mma_b(*reinterpret_cast<v4f(*)[2]>(&y[TT / 2]), u1,
-                      *reinterpret_cast<const Parts<NQ>(*)[2]>(&op[1][TT / 2]));
-            } else {
-                mma_b(y, u1, op[1]);
             }
+            mma_b(*reinterpret_cast<v4f(*)[TT - T2]>(&y[T2]), u1, op1);
         }
     }
 
@@ -767,7 +794,7 @@ struct Scan {
                 const bool more = c + 1 < c1;
                 wait_barrier<nM + nV + nK>();  // q and the coefficients
                 if constexpr (CUT) put_qk(oK, kr);
-                copy_tiles<NQ * DTRI>(oP, a.P + (bh * d.N + c) * (NQ * DTRI * DTILE));
+                copy_tiles<PK * DTRI>(oP, a.P + (bh * d.N + c) * (PK * DTRI * DTILE));
                 wait_barrier<nP>();  // M, v and k
                 if (more) {
                     if constexpr (CUT)
@@ -847,11 +874,11 @@ struct Scan {
             meet();  // outputs: q and the coefficients are here, P is free; else everything is here
             const float* cf = coef(c);
             if constexpr (MODE == kOutputs) {
-                rows_product<true, NQ, true>(y, oQ, sp, s);
+                rows_product<true, true>(y, oQ, sp, s);
                 meet();  // M, v and k are here, q is free
-                rows_product<false, 3, false>(x, kb, sp, s);
+                rows_product<false, false>(x, kb, sp, s);
             } else {
-                rows_product<false, 3, true>(x, kb, sp, s);
+                rows_product<false, true>(x, kb, sp, s);
             }
             team_sum(x);
             // R = v - e^G x, E = M R (value column p0 + i, tokens 16 t + 4 g + v)
@@ -995,7 +1022,7 @@ struct Scan {
             add_outer(gq, oQ, dy);
             meet();  // N^T and k are here, P^T, q and dy are free
             Parts<3> sp[JW];
-            rows_product<false, 3, true>(x, oK, sp, s);
+            rows_product<false, true>(x, oK, sp, s);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 u[t] = at4(cf + DL + 16 * t + 4 * g) * x[t];
