@@ -177,12 +177,12 @@ __global__ __launch_bounds__(team_block(TS)) void k_rms_norm(NormShape n, const 
             for (int o = 1; o < n.group / EV; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
         }
         const float sc = top > 0.0f ? top / kF8Max : 1.0f;
-        const float up = top < 0x1p-100f ? 0x1p100f : 1.0f;  // 448 / top is infinite below 2^-119
-        const float inv = top > 0.0f ? kF8Max / (top * up) : 1.0f;
+        const float up = top < 0x1p-100f ? 0x1p100f : 1.0f;  // below 2^-117 the scale is denormal: fewer bits
+        const float by = top > 0.0f ? top * up / kF8Max : 1.0f;
         if (col < n.width) {
             float o[EV];
 #pragma unroll
-            for (int e = 0; e < EV; ++e) o[e] = v[m][e] * up * inv;
+            for (int e = 0; e < EV; ++e) o[e] = v[m][e] * up / by;
             stv8<EV>(y8 + at + col, o);
             if (col % n.group == 0) scale[row * groups + col / n.group] = sc;
         }
