@@ -365,8 +365,8 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
                 pre = __shfl_up(pre, 1);
                 if (lane == 0) pre = 0.0;
                 double out = suf + pre + static_cast<double>(sCf[3 * DL]) * hd;
-                // a state forgotten at once: exactly zero, where the sums leave their rounding
-                if (sG[lane] - (lane > 0 ? sG[lane - 1] : 0.0) < -1000.0) out = 0.0;
+                // a decay of 0, which forgets the state: exactly zero, where the sums leave their rounding
+                if (exp2_of(sG[lane] - (lane > 0 ? sG[lane - 1] : 0.0)) == 0.0f) out = 0.0;
                 if (lane < all) d_g[(row0 + lane) * d.H + h] = lane < L ? static_cast<float>(out) : 0.0f;
             }
             if (act) {

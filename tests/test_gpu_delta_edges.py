@@ -1,0 +1,41 @@
+"""The gated delta rule at the edges of its definition."""
+import pytest
+import torch
+
+import delta_ref as ref
+from gpu_common import say
+from mamba_ssd_chunked_amd import ssd
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+NAMES = ("q", "k", "v", "g", "beta")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ssd.load_library()
+
+
+def dev(w):
+    return {n: t.cuda() if isinstance(t, torch.Tensor) else t for n, t in w.items()}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [-120.0, -300.0, -690.0])
+def test_decays_of_zero_have_no_gradient(gate, dtype):
+    """A decay that is 0 in fp32 forgets the state whatever its logarithm: among ordinary tokens the
+    gradient of that logarithm (below 1e-50 in 64 bits) is exactly zero."""
+    w = ref.delta_inputs(2, 140, 1, 2, 32, 64, seed=321, dtype=dtype)
+    at = [0, 5, 22, 63, 64, 90, 139]
+    w["g"][:, at] = gate
+    say("case zero decay", gate, dtype)
+    d = dev(w)
+    got = ssd.delta_rule_bwd(d["dy"], *(d[n] for n in NAMES), init=d["init"], d_final=d["d_final"])
+    torch.cuda.synchronize()
+    assert not got["d_g"][:, at].any()
+    rest = [t for t in range(140) if t not in at]
+    want = ref.delta_rule_bwd(w["dy"], *(w[n] for n in NAMES), w["init"], w["d_final"])
+    assert ref.rel(got["d_g"][:, rest], want["d_g"][:, rest]) < (2e-5 if dtype == F32 else 2.5e-3)
