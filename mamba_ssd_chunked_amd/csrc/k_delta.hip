@@ -766,7 +766,10 @@ struct Scan {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             const int64_t tok = static_cast<int64_t>(c) * DL + 16 * (tm * TT + t) + i;
-            if (tok < d.S) io<IO>::st4(a.y, ((b * static_cast<int64_t>(d.S) + tok) * d.H + h) * d.P + p0 + 4 * g, y[t]);
+            // past the length zeros as they are: as products they would be NaN beside a NaN or an infinity
+            if (tok < d.S)
+                io<IO>::st4(a.y, ((b * static_cast<int64_t>(d.S) + tok) * d.H + h) * d.P + p0 + 4 * g,
+                            tok < len ? y[t] : zero4());
         }
     }
 

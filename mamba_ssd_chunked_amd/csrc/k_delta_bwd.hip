@@ -237,7 +237,8 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
             db += e[0] * z[0] + e[1] * z[1] + e[2] * z[2] + e[3] * z[3];
             e *= be;
             z *= be;
-            if (p0 + vp < d.P && vt < all) io<IO>::st4(d_v, ((row0 + vt) * d.H + h) * d.P + p0 + vp, z);
+            if (p0 + vp < d.P && vt < all)  // past the length zeros as they are, beside NaN too
+                io<IO>::st4(d_v, ((row0 + vt) * d.H + h) * d.P + p0 + vp, vt < L ? z : zero4());
             store_parts4<3>(sm.v.U + vt * LP + vp, UP, e);
             store_parts4<3>(sm.v.Z + vt * LP + vp, UP, z);
             store_parts4<NP>(sm.v.Y + vt * LP + vp, UP, y);
@@ -401,8 +402,8 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
                 const int t = 16 * (tt0 + m) + i;
                 if (hh + 1 == grp && t < all) {
                     const int64_t at = ((row0 + t) * d.HK + hk) * R + 16 * rho + 4 * g;
-                    io<IO>::st4(d_q, at, SHARED ? dq[SHARED ? m : 0] : aq[m]);
-                    io<IO>::st4(d_k, at, SHARED ? dk[SHARED ? m : 0] : akr[m]);
+                    io<IO>::st4(d_q, at, t >= L ? zero4() : SHARED ? dq[SHARED ? m : 0] : aq[m]);
+                    io<IO>::st4(d_k, at, t >= L ? zero4() : SHARED ? dk[SHARED ? m : 0] : akr[m]);
                 }
             }
         }

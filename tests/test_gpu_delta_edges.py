@@ -39,3 +39,26 @@ def test_decays_of_zero_have_no_gradient(gate, dtype):
     rest = [t for t in range(140) if t not in at]
     want = ref.delta_rule_bwd(w["dy"], *(w[n] for n in NAMES), w["init"], w["d_final"])
     assert ref.rel(got["d_g"][:, rest], want["d_g"][:, rest]) < (2e-5 if dtype == F32 else 2.5e-3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heads", [2, 100, 160])
+def test_past_the_length_is_zero_beside_bad_values(heads, bad, dtype):
+    """Tokens past a row's length give zeros also where the row's own tokens hold a NaN or an infinity,
+    in the last chunk or before it, or its initial state does."""
+    b, s, p, r, lens = 4, 150, 64, 64, (100, 150, 1, 131)
+    w = ref.delta_inputs(b, s, heads, heads, p, r, seed=331, dtype=dtype)
+    w["v"][0, 70, :, 3], w["k"][0, 80, 0, 5] = bad, bad
+    w["v"][2, 0], w["init"][3, :, 2] = bad, bad
+    w["dy"][0, 99], w["d_final"][3, :, 1] = bad, bad
+    say("case past the length", heads, bad, dtype)
+    d = dev(w)
+    a = [d[n] for n in NAMES]
+    y, _ = ssd.delta_rule(*a, init=d["init"], valid_len=lens)
+    got = ssd.delta_rule_bwd(d["dy"], *a, init=d["init"], d_final=d["d_final"], valid_len=lens)
+    torch.cuda.synchronize()
+    assert torch.isfinite(y[1]).all() and not torch.isfinite(y[0, :100]).all()
+    for n, t in {"y": y, **{n: got[n] for n in ("d_q", "d_k", "d_v", "d_g", "d_beta")}}.items():
+        for i, m in enumerate(lens):
+            assert not t[i, m:].any(), (n, i)
