@@ -364,7 +364,9 @@ int ssd_delta_workspace_size(const ssd_delta_dims* dims, int bwd, size_t* bytes)
 
 /*
  * Outputs of a whole sequence, chunk by chunk.  final_state and init are nullable (not written;
- * zero initial state).  Nothing is saved for the backward.
+ * zero initial state).  final_state may equal init (updated in place, at the price of running long
+ * sequences of few heads chunk after chunk), otherwise the two must not overlap
+ * (SSD_ERR_UNSUPPORTED).  Nothing is saved for the backward.
  */
 int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, const void* v,
                   const float* g, const float* beta, const float* init, const int64_t* valid_len,
@@ -372,8 +374,8 @@ int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, cons
 
 /*
  * Gradients of <dy, y> + <d_final, final_state> from the leaves (the states are recomputed).
- * d_final and init nullable (= zero), d_init nullable (not written); the other gradients are
- * required.  d_q and d_k are summed over the value heads that share a key head.
+ * d_final and init nullable (= zero), d_init nullable (not written; it may equal d_final, but not
+ * overlap it otherwise: SSD_ERR_UNSUPPORTED); the other gradients are required.  d_q and d_k are summed over the value heads that share a key head.
  */
 int ssd_delta_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_final, const void* q,
                   const void* k, const void* v, const float* g, const float* beta,

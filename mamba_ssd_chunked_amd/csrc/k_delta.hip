@@ -1228,7 +1228,9 @@ hipError_t scan_r(const DeltaShape& d, const DeltaBufs& f, ScanMode mode, int se
 
 template <class IO, int R>
 hipError_t scans(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
-    const int segs = bwd ? 1 : delta_segments(d);
+    // in place (final_state is init) the chunks run through: side by side, the last segment would write
+    // what the first may still have to read
+    const int segs = bwd || (f.init && f.init == f.final_state) ? 1 : delta_segments(d);
     if (segs > 1) {
         if (hipError_t e = scan_r<IO, R>(d, f, kCarry, segs, st); e != hipSuccess) return e;
         const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * (d.P / 16)));

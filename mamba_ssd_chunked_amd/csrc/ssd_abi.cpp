@@ -446,6 +446,12 @@ int fwd_impl(const char* who, const ssd_dims* dims, const void* x, const float* 
     return ok();
 }
 
+// Whether two arrays of n floats share memory without being the same array.
+bool overlap_unequal(const float* x, const float* y, size_t n) {
+    const char *a = reinterpret_cast<const char*>(x), *b = reinterpret_cast<const char*>(y);
+    return x && y && a != b && a < b + 4 * n && b < a + 4 * n;
+}
+
 // ------------------------------------------------------------ gated delta rule, norm
 int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape* d) {
     if (!dims) return fail(SSD_ERR_NULL, "%s: dims is NULL", who);
@@ -1048,10 +1054,7 @@ int ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int
     if (int rc = check_align(C, "C", ia)) return rc;
     if (int rc = check_align(state, "state", 16)) return rc;
     if (int rc = check_align(new_state, "new_state", 16)) return rc;
-    const size_t sbytes = (size_t)batch * nheads * headdim * dstate * sizeof(float);
-    const char* a = reinterpret_cast<const char*>(state);
-    const char* b = reinterpret_cast<const char*>(new_state);
-    if (a != b && a < b + sbytes && b < a + sbytes)
+    if (overlap_unequal(state, new_state, (size_t)batch * nheads * headdim * dstate))
         return fail(SSD_ERR_UNSUPPORTED, "ssd_step: state and new_state overlap without being equal");
     ssd::StepShape s{(int)batch, (int)nheads, (int)headdim, (int)dstate, io_dtype};
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -1078,6 +1081,8 @@ int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, cons
     if (tok && (!q || !k || !v || !g || !beta || !y))
         return fail(SSD_ERR_NULL, "%s: q, k, v, g, beta and y are required", who);
     if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {y, "y"}, {init, "init"}, {final_state, "final_state"}})) return rc;
+    if (overlap_unequal(init, final_state, (size_t)d.B * d.H * d.P * d.R))
+        return fail(SSD_ERR_UNSUPPORTED, "%s: init and final_state overlap without being equal", who);
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
     ssd::DeltaBufs f{};
     const size_t need = delta_plan(d, false, ws, &f);
@@ -1119,6 +1124,8 @@ int ssd_delta_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fin
     if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {dy, "dy"}, {d_q, "d_q"}, {d_k, "d_k"}, {d_v, "d_v"}, {init, "init"},
                                   {d_final, "d_final"}, {d_init, "d_init"}}))
         return rc;
+    if (overlap_unequal(d_final, d_init, (size_t)d.B * d.H * d.P * d.R))
+        return fail(SSD_ERR_UNSUPPORTED, "%s: d_final and d_init overlap without being equal", who);
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
     ssd::DeltaBufs f{};
     const size_t need = delta_plan(d, true, ws, &f);

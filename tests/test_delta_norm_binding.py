@@ -1,0 +1,37 @@
+"""What the entry points of the gated delta rule and the norm refuse, and what the binding hands over,
+without a GPU (the addresses here are fake and never dereferenced)."""
+import ctypes
+
+import pytest
+
+from mamba_ssd_chunked_amd import ssd
+
+FAKE = 1 << 20
+UNSUPPORTED = 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ssd.load_library()
+
+
+def address(off=0):
+    return ctypes.c_void_p(FAKE + off)
+
+
+def dims(b=2, s=100, hk=2, h=4, p=32, r=64, io=1):
+    return ssd.ssd_delta_dims(b, s, hk, h, p, r, s * hk * r, hk * r, r, s * hk * r, hk * r, r, s * h * p, h * p, p,
+                              r ** -0.5, io)
+
+
+@pytest.mark.parametrize("seq", [0, 100])
+def test_states_that_overlap_without_being_equal_are_refused(lib, seq):
+    d, F = dims(s=seq), address()
+    size = 4 * d.batch * d.nheads * d.headdim * d.dstate
+    for off in (16, size - 16):
+        for first, second in ((0, off), (off, 0)):
+            rc = lib.ssd_delta_fwd(ctypes.byref(d), *[F] * 5, address(first), None, F, address(second), F, 1 << 40, None)
+            assert rc == UNSUPPORTED and "overlap" in ssd.ssd_last_error()
+            rc = lib.ssd_delta_bwd(ctypes.byref(d), F, address(first), *[F] * 6, None, *[F] * 5, address(second), F,
+                                   1 << 40, None)
+            assert rc == UNSUPPORTED and "overlap" in ssd.ssd_last_error()

@@ -62,3 +62,32 @@ def test_past_the_length_is_zero_beside_bad_values(heads, bad, dtype):
     for n, t in {"y": y, **{n: got[n] for n in ("d_q", "d_k", "d_v", "d_g", "d_beta")}}.items():
         for i, m in enumerate(lens):
             assert not t[i, m:].any(), (n, i)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("b,s,h,p,r", [(1, 4096, 8, 64, 128), (2, 2100, 1, 16, 16), (2, 130, 3, 64, 64)])
+def test_states_in_place(b, s, h, p, r, dtype):
+    """final_state may be init, and d_init d_final, also where segments of the sequence would run side by
+    side: the results of separate arrays, up to the order of the segments' sums."""
+    w = dev(ref.delta_inputs(b, s, h, h, p, r, seed=341, dtype=dtype))
+    w["g"] *= 0.05
+    a = [w[n] for n in NAMES]
+    say("case in place", b, s, h, p, r, dtype)
+    y, final = ssd.delta_rule(*a, init=w["init"])
+    want = ssd.delta_rule_bwd(w["dy"], *a, init=w["init"], d_final=w["d_final"])
+    ws = ssd.delta_workspace(*a[:3], False)
+    outs = []
+    for _ in range(3):
+        state, y2 = w["init"].clone(), torch.empty_like(y)
+        assert ssd.ssd_delta_fwd(*a, state, None, y2, state, ws) == 0
+        outs.append((y2, state))
+    ws = ssd.delta_workspace(*a[:3], True)
+    g, ds = [torch.empty_like(t) for t in a], w["d_final"].clone()
+    assert ssd.ssd_delta_bwd(w["dy"], ds, *a, w["init"], None, *g, ds, ws) == 0
+    torch.cuda.synchronize()
+    for y2, state in outs:
+        assert torch.equal(y2, outs[0][0]) and torch.equal(state, outs[0][1])
+    assert ref.rel(outs[0][1], final) < 2e-5 and ref.rel(outs[0][0], y) < (2e-5 if dtype == F32 else 2.5e-3)
+    assert torch.equal(ds, want["d_init"])
+    for n, t in zip(NAMES, g):
+        assert torch.equal(t, want["d_" + n]), n
