@@ -394,8 +394,8 @@ hipError_t launch_reduce_heads(const Shape& s, const double* dA_part0, const dou
 
 __global__ __launch_bounds__(NT) void copy_or_zero(float* __restrict__ dst,
                                                   const float* __restrict__ src, int64_t n) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
-    if (i < n) dst[i] = src ? src[i] : 0.0f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * NT;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x; i < n; i += step) dst[i] = src ? src[i] : 0.0f;
 }
 
 struct I64Pack {
@@ -420,9 +420,11 @@ hipError_t launch_set_i64(int64_t* dst, const int64_t* vals, int64_t fill, int64
 }
 
 hipError_t launch_copy_or_zero(float* dst, const float* src, int64_t n, hipStream_t st) {
-    if (n <= 0 || !dst) return hipSuccess;
-    hipLaunchKernelGGL(copy_or_zero, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0,
-                       st, dst, src, n);
+    if (n <= 0 || !dst || dst == src) return hipSuccess;
+    // states of every size an entry point accepts, in at most 2^20 workgroups (2^28 work-items)
+    const int64_t blocks = (n + NT - 1) / NT, cap = 1 << 20;
+    hipLaunchKernelGGL(copy_or_zero, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(NT), 0, st, dst, src,
+                       n);
     return hipGetLastError();
 }
 

@@ -91,3 +91,26 @@ def test_states_in_place(b, s, h, p, r, dtype):
     assert torch.equal(ds, want["d_init"])
     for n, t in zip(NAMES, g):
         assert torch.equal(t, want["d_" + n]), n
+
+
+def test_empty_sequences_of_more_than_2_to_the_32_state_values():
+    """The states of an empty sequence are copied whole, past the work-items of one launch."""
+    b, p, r = 262144 + 5, 128, 128
+    e = [torch.empty(b, 0, 1, n, device="cuda") for n in (r, r, p)] + [torch.empty(b, 0, 1, device="cuda")] * 2
+    init = torch.empty(b, 1, p, r, device="cuda")
+    probe = torch.tensor([0, 1, 65535, 65536, 131072, 262143, 262144, b - 1], device="cuda")
+    mark = torch.randn(len(probe), 1, p, r, device="cuda")
+    init.fill_(2.0)
+    init[probe] = mark
+    say("case empty large")
+    _, final = ssd.delta_rule(*e, init=init)
+    torch.cuda.synchronize()
+    assert torch.equal(final[probe], mark)
+    for lo in range(0, b, 32768):
+        assert torch.equal(final[lo:lo + 32768], init[lo:lo + 32768]), lo
+    del final
+    g = ssd.delta_rule_bwd(e[2], *e, d_final=init)
+    torch.cuda.synchronize()
+    assert torch.equal(g["d_init"][probe], mark)
+    for lo in range(0, b, 32768):
+        assert torch.equal(g["d_init"][lo:lo + 32768], init[lo:lo + 32768]), lo
