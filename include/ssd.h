@@ -406,8 +406,9 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
  *   y8 [rows, width] bytes;   scale [rows, width / group] fp32
  * residual is nullable; s is required with a residual (it may be the residual itself) and must be
  * NULL without one; y is nullable if y8 is given; y8 and scale come together or not at all.
- * rows >= 0, 0 < width <= 32768, group 0 or 32, 64, 128 or 256 and dividing width.  Tensors are
- * contiguous and 16-byte aligned.  s is rounded to the io dtype where it is stored; the norm is
+ * 0 <= rows < 2^22 (a launch has up to 1024 work-items per row; rows do not depend on each other, so
+ * more are split over calls; SSD_ERR_UNSUPPORTED), 0 < width <= 32768, group 0 or 32, 64, 128 or 256
+ * and dividing width.  Tensors are contiguous and 16-byte aligned.  s is rounded to the io dtype where it is stored; the norm is
  * taken of the fp32 sum, and y and y8 are each rounded once from fp32.
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_HIP.
  */
@@ -420,7 +421,8 @@ int ssd_rms_norm(int64_t rows, int64_t width, int io_dtype, float eps, const voi
  * the same gradient to x and to the residual:
  *   d_x = d_s + (weight dy - n mean(n weight dy)) / sqrt(mean(s^2) + eps)   [rows, width] io dtype
  *   d_weight = sum over rows of dy n                                        [width] fp32
- * d_s is nullable (= zero); d_x may be d_s.  The workspace (ssd_rms_norm_workspace_size, 256-byte
+ * d_s is nullable (= zero); d_x may be d_s; any number of rows (rows * width up to 2^60).  The
+ * workspace (ssd_rms_norm_workspace_size, 256-byte
  * aligned) holds partial sums of d_weight, which are added in a fixed order.
  */
 int ssd_rms_norm_bwd(int64_t rows, int64_t width, int io_dtype, float eps, const void* dy,

@@ -552,10 +552,9 @@ int validate_norm(const char* who, int64_t rows, int64_t width, int io_dtype, fl
                     (long long)rows, (long long)width, (double)eps);
     if (width > 32768)
         return fail(SSD_ERR_UNSUPPORTED, "%s: width must be at most 32768 (got %lld)", who, (long long)width);
-    // a team of at most 1024 work-items per row
-    if (rows > (1 << 22) - 1)
-        return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch could exceed 2^32 work-items "
-                    "(split the rows)", who);
+    if (rows > ((int64_t)1 << 60) / width)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: rows * width must be at most 2^60 (got %lld, %lld)", who, (long long)rows,
+                    (long long)width);
     *n = ssd::NormShape{rows, (int)width, (int)width, io_dtype, eps};
     return SSD_OK;
 }
@@ -1188,6 +1187,10 @@ int ssd_rms_norm(int64_t rows, int64_t width, int io_dtype, float eps, const voi
     const char* who = "ssd_rms_norm";
     ssd::NormShape n;
     if (int rc = validate_norm(who, rows, width, io_dtype, eps, &n)) return rc;
+    // a team of up to 1024 work-items has a row (the gradient's teams, 1024 at most, take any number of them)
+    if (rows > (1 << 22) - 1)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: at most 2^22 - 1 rows in one call (got %lld: split the rows)", who,
+                    (long long)rows);
     if (group != 0 && (!pow2_in(group, 32, 256) || width % group != 0))
         return fail(SSD_ERR_UNSUPPORTED, "%s: group must be 0, or 32, 64, 128 or 256 and divide width (got %lld for "
                     "width %lld)", who, (long long)group, (long long)width);

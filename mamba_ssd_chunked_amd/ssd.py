@@ -826,11 +826,14 @@ def delta_step(q, k, v, g, beta, state, slots=None, scale=None, stream=None):
     return y
 
 
+_NORM_ROWS = 1 << 21  # rows of one call among several (one takes fewer than 2^22)
+
+
 def rms_norm(x, weight, eps=1e-6, residual=None, out8=False, group=0, want_y=None, stream=None):
     """Root-mean-square norm of x ``[..., width]`` (see ssd_rms_norm).  Returns a dict of: ``s`` = x +
     residual (with a residual), ``y`` (by default where out8 is false), and with out8 ``y8``
     (float8_e4m3fn) and ``scale`` (fp32 ``[..., width / group]``, group 0: one per row) with
-    y = y8 * scale."""
+    y = y8 * scale.  Any number of rows, from 2^22 on in several calls."""
     want_y = not out8 if want_y is None else want_y
     width = x.shape[-1]
     with _allocating_on(stream):
@@ -839,7 +842,14 @@ def rms_norm(x, weight, eps=1e-6, residual=None, out8=False, group=0, want_y=Non
         y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if out8 else None
         groups = width // group if group > 0 else 1
         scale = torch.empty((*x.shape[:-1], groups), device=x.device) if out8 else None
-        _check(ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream), "ssd_rms_norm")
+        rows = x.numel() // width if width else 0
+        if rows < 2 * _NORM_ROWS or not x.is_contiguous():
+            _check(ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream), "ssd_rms_norm")
+        else:
+            for lo in range(0, rows, _NORM_ROWS):
+                a, r, *out = (None if t is None else t.view(rows, -1)[lo: lo + _NORM_ROWS]
+                              for t in (x, residual, s, y, y8, scale))
+                _check(ssd_rms_norm(a, r, weight, eps, group, *out, stream), "ssd_rms_norm")
     return {k: t for k, t in (("s", s), ("y", y), ("y8", y8), ("scale", scale)) if t is not None}
 
 

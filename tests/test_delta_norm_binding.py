@@ -35,3 +35,14 @@ def test_states_that_overlap_without_being_equal_are_refused(lib, seq):
             rc = lib.ssd_delta_bwd(ctypes.byref(d), F, address(first), *[F] * 6, None, *[F] * 5, address(second), F,
                                    1 << 40, None)
             assert rc == UNSUPPORTED and "overlap" in ssd.ssd_last_error()
+
+
+def test_norm_gradient_takes_any_number_of_rows(lib):
+    """A team has as many rows as it takes, so the number of rows bounds no launch: the gradient's checks
+    pass a per-head norm of many tokens on (to the check of its workspace), and its workspace stops growing."""
+    for rows in ((1 << 22) - 1, 1 << 22, 5 << 30):
+        assert ssd.ssd_rms_norm_workspace_size(rows, 64) == 4 * 1024 * 64
+        rc = lib.ssd_rms_norm_bwd(rows, 64, 1, 1e-6, *[address()] * 6, address(), 4 * 1024 * 64 - 1, None)
+        assert rc == 5 and "workspace" in ssd.ssd_last_error()
+    rc = lib.ssd_rms_norm_bwd(1 << 55, 64, 1, 1e-6, *[address()] * 6, address(), 1 << 40, None)
+    assert rc == UNSUPPORTED
