@@ -841,7 +841,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None, out8=False, group=0, want_y=Non
         y = torch.empty_like(x) if want_y else None
         y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if out8 else None
         groups = width // group if group > 0 else 1
-        scale = torch.empty((*x.shape[:-1], groups), device=x.device) if out8 else None
+        scale = torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=x.device) if out8 else None
         rows = x.numel() // width if width else 0
         if rows < 2 * _NORM_ROWS or not x.is_contiguous():
             _check(ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream), "ssd_rms_norm")

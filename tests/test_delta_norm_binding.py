@@ -3,6 +3,7 @@ without a GPU (the addresses here are fake and never dereferenced)."""
 import ctypes
 
 import pytest
+import torch
 
 from mamba_ssd_chunked_amd import ssd
 
@@ -46,3 +47,18 @@ def test_norm_gradient_takes_any_number_of_rows(lib):
         assert rc == 5 and "workspace" in ssd.ssd_last_error()
     rc = lib.ssd_rms_norm_bwd(1 << 55, 64, 1, 1e-6, *[address()] * 6, address(), 1 << 40, None)
     assert rc == UNSUPPORTED
+
+
+@pytest.mark.parametrize("default", [torch.float32, torch.bfloat16, torch.float64])
+def test_scales_are_fp32_whatever_torchs_default_type(monkeypatch, default):
+    seen = {}
+    monkeypatch.setattr(ssd, "ssd_rms_norm",
+                        lambda x, res, w, eps, group, s, y, y8, scale, stream: seen.update(scale=scale) or 0)
+    was = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        out = ssd.rms_norm(torch.zeros(3, 64, dtype=torch.bfloat16), torch.ones(64, dtype=torch.float32), out8=True,
+                           group=32)
+    finally:
+        torch.set_default_dtype(was)
+    assert out["scale"] is seen["scale"] and out["scale"].dtype == torch.float32 and out["scale"].shape == (3, 2)
