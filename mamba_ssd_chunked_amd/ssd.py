@@ -449,12 +449,21 @@ def _io_of(t: torch.Tensor, name: str) -> int:
     return io
 
 
-def _address(t: Optional[torch.Tensor], name: str, dtype, numel: int, required: bool = True):
-    """The address of a contiguous device tensor of the right type and size (None for None)."""
+def _merged(got, want) -> bool:
+    """Whether a shape is another with its leading axes merged into one, as of a view."""
+    n = len(want) - len(got)
+    return n > 0 and len(got) > 0 and got[1:] == want[n + 1:] and got[0] == math.prod(want[: n + 1])
+
+
+def _address(t: Optional[torch.Tensor], name: str, dtype, shape, required: bool = True):
+    """The address of a contiguous device tensor of the right type and shape, in which leading axes may
+    be merged (None for None)."""
     if (t is not None and isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda
-            and t.numel() == numel and t.is_contiguous()):
+            and (t.shape == shape or _merged(t.shape, shape)) and t.is_contiguous()):
         return t.data_ptr()
-    _ptr(t, name, dtype, numel, required)  # says what is wrong
+    _ptr(t, name, dtype, math.prod(shape), required)  # says what is wrong, but for the order of the axes
+    if t is not None:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     return None
 
 
@@ -514,8 +523,9 @@ def ssd_delta_workspace_size(dims: ssd_delta_dims, bwd: bool) -> int:
                         dims.io_dtype, int(bool(bwd)))
 
 
-def _delta_sizes(d, q, v):
-    return v.numel() // v.shape[-1] if v.shape[-1] else 0, d.batch * d.nheads * d.headdim * d.dstate
+def _delta_shapes(q, v):
+    """Shapes of the gates, [b, s, h], and of the states, [b, h, p, r]."""
+    return v.shape[:-1], (v.shape[0], *v.shape[-2:], q.shape[-1])
 
 
 def _host_lengths(valid_len, batch):
@@ -528,9 +538,9 @@ def ssd_delta_fwd(q, k, v, g, beta, init, valid_len, y, final_state, ws, scale=N
     """q, k ``[b, s, hk, r]``, v ``[b, s, h, p]`` (last axis contiguous), g, beta ``[b, s, h]``;
     scale None is ``1 / sqrt(r)``."""
     d, qkv = _delta_args(q, k, v, scale)
-    f, (tok, state) = torch.float32, _delta_sizes(d, q, v)
+    f, (tok, state) = torch.float32, _delta_shapes(q, v)
     args = (_address(g, "g", f, tok), _address(beta, "beta", f, tok), _address(init, "init", f, state, False),
-            _host_lengths(valid_len, d.batch), _address(y, "y", q.dtype, v.numel()),
+            _host_lengths(valid_len, d.batch), _address(y, "y", q.dtype, v.shape),
             _address(final_state, "final_state", f, state, False))
     wp, wb = _ws(ws)
     return load_library().ssd_delta_fwd(ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream, q))
@@ -539,14 +549,14 @@ def ssd_delta_fwd(q, k, v, g, beta, init, valid_len, y, final_state, ws, scale=N
 def ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, valid_len, d_q, d_k, d_v, d_g, d_beta, d_init, ws,
                   scale=None, stream=None) -> int:
     d, qkv = _delta_args(q, k, v, scale)
-    f, (tok, state), io = torch.float32, _delta_sizes(d, q, v), q.dtype
+    f, (tok, state), io = torch.float32, _delta_shapes(q, v), q.dtype
     args = (_address(g, "g", f, tok), _address(beta, "beta", f, tok), _address(init, "init", f, state, False),
-            _host_lengths(valid_len, d.batch), _address(d_q, "d_q", io, q.numel()),
-            _address(d_k, "d_k", io, q.numel()), _address(d_v, "d_v", io, v.numel()),
+            _host_lengths(valid_len, d.batch), _address(d_q, "d_q", io, q.shape),
+            _address(d_k, "d_k", io, q.shape), _address(d_v, "d_v", io, v.shape),
             _address(d_g, "d_g", f, tok), _address(d_beta, "d_beta", f, tok),
             _address(d_init, "d_init", f, state, False))
     wp, wb = _ws(ws)
-    return load_library().ssd_delta_bwd(ctypes.byref(d), _address(dy, "dy", io, v.numel()),
+    return load_library().ssd_delta_bwd(ctypes.byref(d), _address(dy, "dy", io, v.shape),
                                         _address(d_final, "d_final", f, state, False), *qkv, *args, wp, wb,
                                         _raw_stream(stream, q))
 
@@ -563,24 +573,24 @@ def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -
     if slots is not None and not (slots.dtype == torch.int32 and slots.is_cuda and slots.is_contiguous()
                                   and slots.numel() == d.batch):
         raise ValueError(f"slots must be a contiguous device int32 tensor of {d.batch} elements")
-    bh = d.batch * d.nheads
+    bh = v.shape[:2]
     return load_library().ssd_delta_step(
         ctypes.byref(d), state.shape[0], *qkv, _address(g, "g", f, bh), _address(beta, "beta", f, bh),
-        _address(state, "state", f, state.numel()), None if slots is None else slots.data_ptr(),
-        _address(y, "y", io, v.numel()), _raw_stream(stream, q))
+        _address(state, "state", f, state.shape), None if slots is None else slots.data_ptr(),
+        _address(y, "y", io, v.shape), _raw_stream(stream, q))
 
 
 def ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream=None) -> int:
     """x, residual, s, y ``[..., width]``, weight fp32 ``[width]``, y8 float8_e4m3fn like x, scale fp32
     ``[..., width / group]`` (group 0: one per row)."""
-    width, n, io = x.shape[-1], x.numel(), x.dtype
-    rows = n // width if width else 0
+    n, io = x.shape, x.dtype
+    width = n[-1]
     groups = width // group if group > 0 else 1
     return load_library().ssd_rms_norm(
-        rows, width, _io_of(x, "x"), eps, _address(x, "x", io, n), _address(residual, "residual", io, n, False),
-        _address(weight, "weight", torch.float32, width), int(group), _address(s, "s", io, n, False),
+        x.numel() // width if width else 0, width, _io_of(x, "x"), eps, _address(x, "x", io, n), _address(residual, "residual", io, n, False),
+        _address(weight, "weight", torch.float32, n[-1:]), int(group), _address(s, "s", io, n, False),
         _address(y, "y", io, n, False), _address(y8, "y8", torch.float8_e4m3fn, n, False),
-        _address(scale, "scale", torch.float32, rows * groups, False), _raw_stream(stream, x))
+        _address(scale, "scale", torch.float32, (*n[:-1], groups), False), _raw_stream(stream, x))
 
 
 def ssd_rms_norm_workspace_size(rows, width) -> int:
@@ -592,12 +602,13 @@ def ssd_rms_norm_workspace_size(rows, width) -> int:
 
 
 def ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream=None) -> int:
-    width, n, io = s.shape[-1], s.numel(), s.dtype
+    n, io = s.shape, s.dtype
+    width = n[-1]
     wp, wb = _ws(ws)
     return load_library().ssd_rms_norm_bwd(
-        n // width if width else 0, width, _io_of(s, "s"), eps, _address(dy, "dy", io, n), _address(s, "s", io, n),
-        _address(d_s, "d_s", io, n, False), _address(weight, "weight", torch.float32, width),
-        _address(d_x, "d_x", io, n), _address(d_weight, "d_weight", torch.float32, width), wp, wb,
+        s.numel() // width if width else 0, width, _io_of(s, "s"), eps, _address(dy, "dy", io, n), _address(s, "s", io, n),
+        _address(d_s, "d_s", io, n, False), _address(weight, "weight", torch.float32, n[-1:]),
+        _address(d_x, "d_x", io, n), _address(d_weight, "d_weight", torch.float32, n[-1:]), wp, wb,
         _raw_stream(stream, s))
 
 
@@ -790,6 +801,8 @@ def delta_rule(q, k, v, g, beta, init=None, valid_len=None, scale=None, want_fin
     q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]`` (fp32 or bf16; slices of one projection's output
     are read in place), log decay g and write strength beta ``[b, s, h]`` fp32, init ``[b, h, p, r]``
     fp32 or None, valid_len host int64 ``[b]`` (or a list) or None, scale None for ``1 / sqrt(r)``."""
+    if q.dim() != 4:
+        raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
     with _allocating_on(stream):
         y = v.new_empty(v.shape)
         final = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), dtype=torch.float32,
@@ -804,6 +817,8 @@ def delta_rule_bwd(dy, q, k, v, g, beta, init=None, d_final=None, valid_len=None
                    want_d_init=True, ws=None, stream=None):
     """Gradients of ``<dy, y> + <d_final, final_state>`` of delta_rule, from its inputs: returns
     dict(d_q, d_k, d_v, d_g, d_beta, d_init)."""
+    if q.dim() != 4:
+        raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
     with _allocating_on(stream):
         new = lambda t: t.new_empty(t.shape)  # noqa: E731
         out = dict(d_q=new(q), d_k=new(k), d_v=new(v), d_g=new(g), d_beta=new(beta),

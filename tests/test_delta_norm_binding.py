@@ -5,6 +5,7 @@ import ctypes
 import pytest
 import torch
 
+import delta_ref as ref
 from mamba_ssd_chunked_amd import ssd
 
 FAKE = 1 << 20
@@ -62,3 +63,96 @@ def test_scales_are_fp32_whatever_torchs_default_type(monkeypatch, default):
     finally:
         torch.set_default_dtype(was)
     assert out["scale"] is seen["scale"] and out["scale"].dtype == torch.float32 and out["scale"].shape == (3, 2)
+
+
+# ---------------------------------------------------------------------------- the binding's own checks
+class OnDevice(torch.Tensor):
+    """A host tensor that says it lies on a GPU."""
+    at = 0
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", self.at))
+
+    def get_device(self):
+        return self.at
+
+
+class Library:
+    """Takes every call and remembers it."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, args))
+            return 0
+        return entry
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(ssd, "load_library", lambda: lib)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda at: 100 + at, raising=False)
+    return lib.calls
+
+
+def on(t, at=0):
+    t = t.detach().as_subclass(OnDevice)
+    t.at = at
+    return t
+
+
+B, S, HK, H, P, R = 2, 12, 2, 4, 16, 32
+
+
+def problem():
+    """Arguments of every entry point by name, on a device."""
+    w = {n: on(t) for n, t in ref.delta_inputs(B, S, HK, H, P, R, seed=6).items()}
+    new = lambda *sh, **kw: on(torch.zeros(*sh, **kw))  # noqa: E731
+    a = {n: w[n] for n in ("q", "k", "v", "g", "beta")}
+    state = lambda: new(B, H, P, R)  # noqa: E731
+    ws = new(1 << 16, dtype=torch.uint8)
+    fwd = dict(a, init=w["init"], valid_len=torch.tensor([S, 3]), y=new(B, S, H, P), final_state=state(), ws=ws)
+    bwd = dict(dy=w["dy"], d_final=w["d_final"], **a, init=w["init"], valid_len=None, d_q=new(B, S, HK, R),
+               d_k=new(B, S, HK, R), d_v=new(B, S, H, P), d_g=new(B, S, H), d_beta=new(B, S, H), d_init=state(), ws=ws)
+    step = dict({n: on(t[:, 0].contiguous()) for n, t in a.items()}, state=new(5, H, P, R),
+                slots=new(B, dtype=torch.int32), y=new(B, H, P))
+    x = lambda: new(B, S, 64)  # noqa: E731
+    norm = dict(x=x(), residual=x(), weight=new(64), eps=1e-6, group=32, s=x(), y=x(),
+                y8=new(B, S, 64, dtype=torch.float8_e4m3fn), scale=new(B, S, 2))
+    norm_bwd = dict(dy=x(), s=x(), d_s=x(), weight=new(64), eps=1e-6, d_x=x(), d_weight=new(64), ws=ws)
+    return {"ssd_delta_fwd": fwd, "ssd_delta_bwd": bwd, "ssd_delta_step": step, "ssd_rms_norm": norm,
+            "ssd_rms_norm_bwd": norm_bwd}
+
+
+ARGS = [(f, n) for f, a in problem().items() for n in a if isinstance(a[n], OnDevice) and n not in ("ws", "slots")]
+
+
+@pytest.mark.parametrize("f,name", ARGS)
+def test_axes_in_another_order_are_refused(calls, f, name):
+    """As many values in another order, such as gates [b, h, s], would be taken for what they are not."""
+    a = problem()[f]
+    assert getattr(ssd, f)(**a) == 0 and len(calls) == 1
+    t = a[name]
+    a[name] = on(t.reshape(2, -1) if t.dim() == 1 else t.transpose(-1, -2).contiguous())
+    with pytest.raises(ValueError, match="must be"):
+        getattr(ssd, f)(**a)
+    assert len(calls) == 1
+
+
+def test_leading_axes_may_be_merged(calls):
+    for f, a in problem().items():
+        for n in ("g", "beta", "init", "y", "final_state", "d_g", "d_init", "residual", "s", "y8", "scale", "dy", "d_x"):
+            if n in a and not (n == "s" and f == "ssd_rms_norm_bwd"):
+                a[n] = on(a[n].flatten(0, 1))
+        assert getattr(ssd, f)(**a) == 0, f
+    assert len(calls) == 5
+
+
+def test_a_sequence_entry_point_refuses_a_single_token():
+    a = [t[:, 0] for t in ref.delta_inputs(B, 1, HK, H, P, R, seed=6, init=False).values() if t is not None]
+    with pytest.raises(ValueError, match=r"\[b, s, hk, r\]"):
+        ssd.delta_rule(*a[:5])
+    with pytest.raises(ValueError, match=r"\[b, s, hk, r\]"):
+        ssd.delta_rule_bwd(a[5], *a[:5])
