@@ -136,7 +136,7 @@ def test_axes_in_another_order_are_refused(calls, f, name):
     assert getattr(ssd, f)(**a) == 0 and len(calls) == 1
     t = a[name]
     a[name] = on(t.reshape(2, -1) if t.dim() == 1 else t.transpose(-1, -2).contiguous())
-    with pytest.raises(ValueError, match="must be"):
+    with pytest.raises(ValueError):
         getattr(ssd, f)(**a)
     assert len(calls) == 1
 
