@@ -9,9 +9,9 @@ instead of faulting on the GPU -- pass the raw pointers and return the C status
 code.  ``forward``, ``backward``, ``state_moments`` and ``state_moments_bwd``
 allocate outputs and workspace with torch and raise :class:`SsdError` on a
 nonzero status.  So do ``delta_rule``, ``delta_rule_bwd`` and ``delta_step`` (the gated delta
-rule) and ``rms_norm`` and ``rms_norm_bwd``; q, k and v of the delta rule may be strided.  Every step of the computation runs in the HIP library; there
-is no Python or CPU fallback, and importing a function whose library is missing
-raises immediately.
+rule) and ``rms_norm`` and ``rms_norm_bwd``; q, k and v of the delta rule may be strided.  Every step
+of the computation runs in the HIP library; there is no Python or CPU fallback, and importing a
+function whose library is missing raises immediately.
 """
 from __future__ import annotations
 
@@ -455,23 +455,47 @@ def _merged(got, want) -> bool:
     return n > 0 and len(got) > 0 and got[1:] == want[n + 1:] and got[0] == math.prod(want[: n + 1])
 
 
-def _address(t: Optional[torch.Tensor], name: str, dtype, shape, required: bool = True):
-    """The address of a contiguous device tensor of the right type and shape, in which leading axes may
-    be merged (None for None)."""
-    if (t is not None and isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda
+def _device_of(t: torch.Tensor, name: str) -> int:
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return at
+
+
+def _address(t: Optional[torch.Tensor], name: str, dtype, shape, at: int, required: bool = True):
+    """The address of a contiguous tensor of the right type and shape, in which leading axes may be
+    merged, on device `at` (None for None)."""
+    if (t is not None and isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == at
             and (t.shape == shape or _merged(t.shape, shape)) and t.is_contiguous()):
         return t.data_ptr()
-    _ptr(t, name, dtype, math.prod(shape), required)  # says what is wrong, but for the order of the axes
+    _ptr(t, name, dtype, math.prod(shape), required)  # says what is wrong, but for the device and the axes
     if t is not None:
+        if t.get_device() != at:
+            raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on device {at}")
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     return None
 
 
-def _raw_stream(stream, on: torch.Tensor) -> int:
-    """The address of a stream, for None of the current one of the device `on` lies on (asked for
-    directly: making a Stream object of it takes 2.5 us)."""
+def _workspace(ws: Optional[torch.Tensor], at: int):
+    """(address, bytes) of a workspace, which has to lie on device `at`."""
+    if ws is not None and ws.is_cuda and ws.get_device() != at:
+        raise ValueError(f"ws is on device {ws.get_device()}, the first tensor on device {at}")
+    return _ws(ws)
+
+
+def _launch(entry, at: int, *args) -> int:
+    """entry(*args) with device `at` current: the library launches on the current device."""
+    if torch._C._cuda_getDevice() == at:
+        return entry(*args)
+    with torch.cuda.device(at):
+        return entry(*args)
+
+
+def _raw_stream(stream, at: int) -> int:
+    """The address of a stream, for None of the current one of device `at` (asked for directly: making
+    a Stream object of it takes 2.5 us)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(on.device.index)
+        return torch._C._cuda_getCurrentRawStream(at)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -491,21 +515,22 @@ def _strided(t: torch.Tensor, name: str, dtype, shape):
 
 
 def _delta_args(q, k, v, scale):
-    """(dims, addresses of q, k, v) for q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]``, or without the
-    token axis."""
+    """(dims, addresses of q, k, v, their device) for q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]``, or
+    without the token axis."""
     if q.dim() not in (3, 4) or v.dim() != q.dim() or q.shape[:-2] != v.shape[:-2]:
         raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p] (one token: [b, hk, r], [b, h, p])")
     io = _io_of(q, "q")
     (pq, sq), (pk, sk), (pv, sv) = (_strided(q, "q", q.dtype, q.shape), _strided(k, "k", q.dtype, q.shape),
                                     _strided(v, "v", q.dtype, v.shape))
-    if not (q.is_cuda and k.is_cuda and v.is_cuda):
-        raise ValueError("q, k and v must be device tensors")
+    at = q.get_device()
+    if at < 0 or k.get_device() != at or v.get_device() != at:
+        raise ValueError("q, k and v must be device tensors of one device")
     b, *seq, hk, r = q.shape
     h, p = v.shape[-2:]
     if not seq:
         seq, sq, sk, sv = (1,), (sq[0], 0, sq[1]), (sk[0], 0, sk[1]), (sv[0], 0, sv[1])
     d = ssd_delta_dims(b, *seq, hk, h, p, r, *sq, *sk, *sv, r ** -0.5 if scale is None else scale, io)
-    return d, (pq, pk, pv)
+    return d, (pq, pk, pv), at
 
 
 @functools.lru_cache(maxsize=256)
@@ -537,28 +562,27 @@ def _host_lengths(valid_len, batch):
 def ssd_delta_fwd(q, k, v, g, beta, init, valid_len, y, final_state, ws, scale=None, stream=None) -> int:
     """q, k ``[b, s, hk, r]``, v ``[b, s, h, p]`` (last axis contiguous), g, beta ``[b, s, h]``;
     scale None is ``1 / sqrt(r)``."""
-    d, qkv = _delta_args(q, k, v, scale)
+    d, qkv, at = _delta_args(q, k, v, scale)
     f, (tok, state) = torch.float32, _delta_shapes(q, v)
-    args = (_address(g, "g", f, tok), _address(beta, "beta", f, tok), _address(init, "init", f, state, False),
-            _host_lengths(valid_len, d.batch), _address(y, "y", q.dtype, v.shape),
-            _address(final_state, "final_state", f, state, False))
-    wp, wb = _ws(ws)
-    return load_library().ssd_delta_fwd(ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream, q))
+    args = (_address(g, "g", f, tok, at), _address(beta, "beta", f, tok, at),
+            _address(init, "init", f, state, at, False), _host_lengths(valid_len, d.batch),
+            _address(y, "y", q.dtype, v.shape, at), _address(final_state, "final_state", f, state, at, False))
+    wp, wb = _workspace(ws, at)
+    return _launch(load_library().ssd_delta_fwd, at, ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream, at))
 
 
 def ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, valid_len, d_q, d_k, d_v, d_g, d_beta, d_init, ws,
                   scale=None, stream=None) -> int:
-    d, qkv = _delta_args(q, k, v, scale)
+    d, qkv, at = _delta_args(q, k, v, scale)
     f, (tok, state), io = torch.float32, _delta_shapes(q, v), q.dtype
-    args = (_address(g, "g", f, tok), _address(beta, "beta", f, tok), _address(init, "init", f, state, False),
-            _host_lengths(valid_len, d.batch), _address(d_q, "d_q", io, q.shape),
-            _address(d_k, "d_k", io, q.shape), _address(d_v, "d_v", io, v.shape),
-            _address(d_g, "d_g", f, tok), _address(d_beta, "d_beta", f, tok),
-            _address(d_init, "d_init", f, state, False))
-    wp, wb = _ws(ws)
-    return load_library().ssd_delta_bwd(ctypes.byref(d), _address(dy, "dy", io, v.shape),
-                                        _address(d_final, "d_final", f, state, False), *qkv, *args, wp, wb,
-                                        _raw_stream(stream, q))
+    args = (_address(g, "g", f, tok, at), _address(beta, "beta", f, tok, at),
+            _address(init, "init", f, state, at, False), _host_lengths(valid_len, d.batch),
+            _address(d_q, "d_q", io, q.shape, at), _address(d_k, "d_k", io, q.shape, at),
+            _address(d_v, "d_v", io, v.shape, at), _address(d_g, "d_g", f, tok, at),
+            _address(d_beta, "d_beta", f, tok, at), _address(d_init, "d_init", f, state, at, False))
+    wp, wb = _workspace(ws, at)
+    return _launch(load_library().ssd_delta_bwd, at, ctypes.byref(d), _address(dy, "dy", io, v.shape, at),
+                   _address(d_final, "d_final", f, state, at, False), *qkv, *args, wp, wb, _raw_stream(stream, at))
 
 
 def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -> int:
@@ -566,31 +590,33 @@ def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -
     ``[nslots, h, p, r]`` updated in place, slots device int32 ``[b]`` or None, y like v."""
     if q.dim() != 3:
         raise ValueError("q and k must be [b, hk, r], v [b, h, p] and state [nslots, h, p, r]")
-    d, qkv = _delta_args(q, k, v, scale)
+    d, qkv, at = _delta_args(q, k, v, scale)
     f, io = torch.float32, q.dtype
     if state.dim() != 4 or state.shape[1:] != (*v.shape[1:], q.shape[2]):
         raise ValueError(f"state must be [nslots, {d.nheads}, {d.headdim}, {d.dstate}] (got {list(state.shape)})")
-    if slots is not None and not (slots.dtype == torch.int32 and slots.is_cuda and slots.is_contiguous()
-                                  and slots.numel() == d.batch):
-        raise ValueError(f"slots must be a contiguous device int32 tensor of {d.batch} elements")
+    if slots is not None and not (slots.dtype == torch.int32 and slots.get_device() == at
+                                  and slots.is_contiguous() and slots.numel() == d.batch):
+        raise ValueError(f"slots must be a contiguous int32 tensor of {d.batch} elements on q's device")
     bh = v.shape[:2]
-    return load_library().ssd_delta_step(
-        ctypes.byref(d), state.shape[0], *qkv, _address(g, "g", f, bh), _address(beta, "beta", f, bh),
-        _address(state, "state", f, state.shape), None if slots is None else slots.data_ptr(),
-        _address(y, "y", io, v.shape), _raw_stream(stream, q))
+    return _launch(
+        load_library().ssd_delta_step, at, ctypes.byref(d), state.shape[0], *qkv,
+        _address(g, "g", f, bh, at), _address(beta, "beta", f, bh, at), _address(state, "state", f, state.shape, at),
+        None if slots is None else slots.data_ptr(),
+        _address(y, "y", io, v.shape, at), _raw_stream(stream, at))
 
 
 def ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream=None) -> int:
     """x, residual, s, y ``[..., width]``, weight fp32 ``[width]``, y8 float8_e4m3fn like x, scale fp32
     ``[..., width / group]`` (group 0: one per row)."""
-    n, io = x.shape, x.dtype
-    width = n[-1]
+    n, io, tag = x.shape, x.dtype, _io_of(x, "x")
+    at, width = _device_of(x, "x"), n[-1]
     groups = width // group if group > 0 else 1
-    return load_library().ssd_rms_norm(
-        x.numel() // width if width else 0, width, _io_of(x, "x"), eps, _address(x, "x", io, n), _address(residual, "residual", io, n, False),
-        _address(weight, "weight", torch.float32, n[-1:]), int(group), _address(s, "s", io, n, False),
-        _address(y, "y", io, n, False), _address(y8, "y8", torch.float8_e4m3fn, n, False),
-        _address(scale, "scale", torch.float32, (*n[:-1], groups), False), _raw_stream(stream, x))
+    return _launch(
+        load_library().ssd_rms_norm, at, x.numel() // width if width else 0, width, tag, eps,
+        _address(x, "x", io, n, at), _address(residual, "residual", io, n, at, False),
+        _address(weight, "weight", torch.float32, n[-1:], at), int(group), _address(s, "s", io, n, at, False),
+        _address(y, "y", io, n, at, False), _address(y8, "y8", torch.float8_e4m3fn, n, at, False),
+        _address(scale, "scale", torch.float32, (*n[:-1], groups), at, False), _raw_stream(stream, at))
 
 
 def ssd_rms_norm_workspace_size(rows, width) -> int:
@@ -602,27 +628,28 @@ def ssd_rms_norm_workspace_size(rows, width) -> int:
 
 
 def ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream=None) -> int:
-    n, io = s.shape, s.dtype
-    width = n[-1]
-    wp, wb = _ws(ws)
-    return load_library().ssd_rms_norm_bwd(
-        s.numel() // width if width else 0, width, _io_of(s, "s"), eps, _address(dy, "dy", io, n), _address(s, "s", io, n),
-        _address(d_s, "d_s", io, n, False), _address(weight, "weight", torch.float32, n[-1:]),
-        _address(d_x, "d_x", io, n), _address(d_weight, "d_weight", torch.float32, n[-1:]), wp, wb,
-        _raw_stream(stream, s))
+    n, io, tag = s.shape, s.dtype, _io_of(s, "s")
+    at, width = _device_of(s, "s"), n[-1]
+    wp, wb = _workspace(ws, at)
+    return _launch(
+        load_library().ssd_rms_norm_bwd, at, s.numel() // width if width else 0, width, tag, eps,
+        _address(dy, "dy", io, n, at), _address(s, "s", io, n, at), _address(d_s, "d_s", io, n, at, False),
+        _address(weight, "weight", torch.float32, n[-1:], at),
+        _address(d_x, "d_x", io, n, at), _address(d_weight, "d_weight", torch.float32, n[-1:], at), wp, wb,
+        _raw_stream(stream, at))
 
 
 # ------------------------------------------------------------ allocating helpers
 _AS_IT_IS = contextlib.nullcontext()
 
 
-def _allocating_on(stream):
-    """Allocate on the stream the work runs on, so that memory freed after the call is reused in
-    that stream's order."""
+def _allocating_on(stream, like: torch.Tensor):
+    """Allocate on the stream the work runs on (one of `like`'s device), so that memory freed after
+    the call is reused in that stream's order."""
     if stream is None:
         return _AS_IT_IS
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     return torch.cuda.stream(stream)
 
 
@@ -803,7 +830,7 @@ def delta_rule(q, k, v, g, beta, init=None, valid_len=None, scale=None, want_fin
     fp32 or None, valid_len host int64 ``[b]`` (or a list) or None, scale None for ``1 / sqrt(r)``."""
     if q.dim() != 4:
         raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
-    with _allocating_on(stream):
+    with _allocating_on(stream, q):
         y = v.new_empty(v.shape)
         final = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), dtype=torch.float32,
                             device=q.device) if want_final else None
@@ -819,7 +846,7 @@ def delta_rule_bwd(dy, q, k, v, g, beta, init=None, d_final=None, valid_len=None
     dict(d_q, d_k, d_v, d_g, d_beta, d_init)."""
     if q.dim() != 4:
         raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
-    with _allocating_on(stream):
+    with _allocating_on(stream, q):
         new = lambda t: t.new_empty(t.shape)  # noqa: E731
         out = dict(d_q=new(q), d_k=new(k), d_v=new(v), d_g=new(g), d_beta=new(beta),
                    d_init=torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]),
@@ -835,7 +862,7 @@ def delta_step(q, k, v, g, beta, state, slots=None, scale=None, stream=None):
     """One token of the gated delta rule from cached states (see ssd_delta_step): q, k ``[b, hk, r]``,
     v ``[b, h, p]``, g, beta ``[b, h]``; state ``[nslots, h, p, r]`` is updated in place; slots (device
     int32 ``[b]``) names each row's slot, negative for an idle row.  Returns y ``[b, h, p]``."""
-    with _allocating_on(stream):
+    with _allocating_on(stream, q):
         y = v.new_empty(v.shape)
         _check(ssd_delta_step(q, k, v, g, beta, state, slots, y, scale, stream), "ssd_delta_step")
     return y
@@ -851,7 +878,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None, out8=False, group=0, want_y=Non
     y = y8 * scale.  Any number of rows, from 2^22 on in several calls."""
     want_y = not out8 if want_y is None else want_y
     width = x.shape[-1]
-    with _allocating_on(stream):
+    with _allocating_on(stream, x):
         s = torch.empty_like(x) if residual is not None else None
         y = torch.empty_like(x) if want_y else None
         y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if out8 else None
@@ -872,7 +899,7 @@ def rms_norm_bwd(dy, s, weight, eps=1e-6, d_s=None, ws=None, stream=None):
     """Gradient of ``<dy, y> + <d_s, s>`` of rms_norm at its s (x without a residual): returns
     ``(d_x, d_weight)``; d_x is the gradient of x and of the residual alike."""
     width = s.shape[-1]
-    with _allocating_on(stream):
+    with _allocating_on(stream, s):
         d_x = torch.empty_like(s)
         d_weight = torch.empty_like(weight)
         if ws is None:

@@ -94,6 +94,7 @@ def calls(monkeypatch):
     lib = Library()
     monkeypatch.setattr(ssd, "load_library", lambda: lib)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda at: 100 + at, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     return lib.calls
 
 
@@ -156,3 +157,44 @@ def test_a_sequence_entry_point_refuses_a_single_token():
         ssd.delta_rule(*a[:5])
     with pytest.raises(ValueError, match=r"\[b, s, hk, r\]"):
         ssd.delta_rule_bwd(a[5], *a[:5])
+
+
+EVERY = [(f, n) for f, a in problem().items() for n in a if isinstance(a[n], OnDevice)]
+
+
+@pytest.mark.parametrize("f,name", EVERY)
+def test_tensors_of_two_devices_are_refused(calls, f, name):
+    a = problem()[f]
+    a[name] = on(a[name], 1)
+    with pytest.raises(ValueError, match="device"):
+        getattr(ssd, f)(**a)
+    a[name] = a[name].as_subclass(torch.Tensor)  # a host tensor
+    with pytest.raises(ValueError, match="device"):
+        getattr(ssd, f)(**a)
+    assert not calls
+
+
+def test_the_launch_goes_to_the_tensors_device_and_its_current_stream(calls, monkeypatch):
+    """Tensors of device 1 while device 0 is current: the call is made with device 1 current, on its
+    current stream, and device 0 is current again afterwards."""
+    current = [0]
+
+    class Guard:
+        def __init__(self, at):
+            self.at = at
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.at
+
+        def __exit__(self, *_):
+            current[0] = self.was
+
+    seen = []
+    lib = ssd.load_library()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    for f, a in problem().items():
+        lib.__dict__[f] = lambda *args: seen.append((current[0], args[-1])) or 0
+        for at in (0, 1):
+            assert getattr(ssd, f)(**{n: on(t, at) if isinstance(t, OnDevice) else t for n, t in a.items()}) == 0
+    assert seen == [(0, 100), (1, 101)] * 5 and current == [0]
