@@ -140,15 +140,18 @@ __device__ __forceinline__ b8v join8(s4 a, s4 b) {
 // 16 bytes per lane from global memory straight into LDS at lds + 16 lane (a byte address, the
 // same in all lanes).  It counts in vmcnt; the reader waits and passes a barrier
 // (wait_barrier).  Written out because around the builtin the compiler waits for every such
-// load before any LDS read, of whatever array.
+// load before any LDS read, of whatever array.  m0, which holds the address, is the compiler's: a
+// clobber list cannot give it away, so it is put back.
 typedef __attribute__((address_space(3))) char lds_char;
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)p));
 }
 __device__ __forceinline__ void load_to_lds(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
-                 "v"(src)
-                 : "memory", "m0");
+    uint32_t was;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+                 : "=&s"(was)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+                 : "memory");
 }
 // Wait until at most N of this wave's memory operations are outstanding (they end in order) and
 // its LDS reads have returned, then for the workgroup.
