@@ -269,6 +269,7 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
                 dP[m] = mma(u, rows8<NP>(sm.v.Y, UP, LP, 16 * tau + i, 8 * g), dP[m]);
                 dA[m] = mma(u, rows8<3>(sm.v.Z, UP, LP, 16 * tau + i, 8 * g), dA[m]);
             });
+            mfma_settle();
         }
         here();
         // results D[r][t] (lane token 16 tt + i, rows r = 16 rho + 4 g + v)
