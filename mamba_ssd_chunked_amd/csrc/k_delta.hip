@@ -1213,7 +1213,6 @@ hipError_t scan_r(const DeltaShape& d, const DeltaBufs& f, ScanMode mode, int se
     const int64_t all = mode == kReverse ? 2 * tiles : tiles;
     const int W = all <= 256 || rows < 32 ? 1 : (in_parts<IO>() == 3 ? tiles : all) <= 512 || rows < 64 ? 2 : 4;
     const int TM = W <= 2 && KJ >= 2 ? 2 : 1;
-    // scan config
     if constexpr (KJ >= 2) switch (10 * W + TM) {
         case 12: return scan_w<IO, R, 1, 2>(d, f, mode, segs, st);
         case 22: return scan_w<IO, R, 2, 2>(d, f, mode, segs, st);

@@ -5,7 +5,8 @@
 //           y8 = y / scale rounded to e4m3 (4 exponent, 3 fraction bits, largest value 448).
 // Gradient: with rstd = rsqrt(mean(s^2) + eps) and n = s rstd,
 //   d_x = d_s + rstd (w dy - n mean(n w dy)),   d_w = sum over rows of dy n.
-// A row is read once and kept in registers: bound by HBM.  8192 rows of 5120 bf16 values with
+// A row is read once and kept in registers (the gradient's of more than 16384 values, or of more than
+// 8192 that are not whole vectors, partly in scratch: 92 to 376 bytes a thread): bound by HBM.  8192 rows of 5120 bf16 values with
 // residual, s and 8-bit output: 60 us, 4.9 TB/s; 8192 rows of 1536 in fp32: forward 36 us, 5.5 TB/s,
 // gradient 35 us and 5 us for joining the weight gradient; 64 rows: 5 us, a launch's latency.
 // A team of 64, 256 or 1024 threads has a row; a thread's vectors lie a team apart, so each load of a
@@ -305,11 +306,12 @@ hipError_t by_width(int width, F&& f) {
     auto vec = [&](auto ts) {
         constexpr int TS = decltype(ts)::value;
         const int nv = (width / V + TS - 1) / TS;
-        if (nv <= 1) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 1>{}, ts);
+        if constexpr (TS == 64)
+            if (nv <= 1) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 1>{}, ts);
         if (nv <= 2) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 2>{}, ts);
         if (nv <= 3) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 3>{}, ts);
         if (nv <= 4) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 4>{}, ts);
-        if constexpr (TS == 1024)
+        if constexpr (TS == 1024 && V == 4)  // bf16 rows of the widest width have four
             if (nv <= 8) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 8>{}, ts);
         return hipErrorInvalidValue;
     };
