@@ -1254,18 +1254,25 @@ hipError_t by_r(const DeltaShape& d, const DeltaBufs& f, bool prep, bool bwd, hi
 
 // Microseconds that `tiles` tiles of 16 state rows take for a chunk each (p = 64, r = 128), with
 // outputs or only carried: in one round of teams on their own, in one of teams on a CU by twos, or in
-// rounds of four tiles a CU (which scan_r goes by).
+// rounds of four tiles a CU (which scan_r goes by); of two, where rows of fewer than 64 leave a
+// workgroup no four tiles.
 static int64_t chunk_time(const DeltaShape& d, int64_t tiles, bool outputs) {
     static const int us[2][2][3] = {{{4, 4, 5}, {4, 7, 10}}, {{2, 3, 3}, {3, 3, 4}}};
     const int* t = us[d.io][outputs];
-    return tiles <= 256 ? t[0] : tiles <= 512 ? t[1] : t[2] * ((tiles + 1023) / 1024);
+    if (tiles <= 256) return t[0];
+    if ((outputs || d.P < d.R ? d.P : d.R) < 64) return t[1] * ((tiles + 511) / 512);
+    return tiles <= 512 ? t[1] : t[2] * ((tiles + 1023) / 1024);
 }
 
 // The number of segments with the shortest way: of a segment the chunks, carried and then with
-// outputs, and the joins (6 us each).  A sequence is left whole unless that saves a fifth.  Whole and
-// in segments, the whole forward (p = 64, r = 128): fp32, 2048 tokens, 1 head, 156 and 75 us; 8192
-// tokens, 24 heads, 685 and 366; 65,536 tokens, 32 heads, 4.2 and 3.5 ms; bf16, 4096 tokens, 8 heads,
-// 165 and 86 us; 16,384 tokens, 32 heads, 750 and 500.
+// outputs, and the joins (6 us each).  A sequence is left whole unless that saves a fifth.  Measured
+// on both sides, whole and in 3 to 32 segments, at 552 shapes: both io types, nine (p, r) from 16 to 128,
+// 16 to 1024 chunks, 1 to 256 tiles.  None of the 260 that the rule cuts is slower so, and the median takes
+// 0.44 of its time (p = 64, r = 128: fp32, 8 heads, 4096 tokens, 290 -> 110 us; 32 heads, 65,536 tokens,
+// 5.2 -> 3.0 ms; bf16, 8 heads, 4096 tokens, 188 -> 82 us; 32 heads, 16,384 tokens, 801 -> 504 us).  Those it
+// leaves whole would win a twelfth at the median and three quarters at most.  With rounds of four tiles for
+// narrow states too, twelve more were cut that run 4 to 25 % longer so (bf16, p = 16, r = 128, 96 heads,
+// 16,384 tokens: 1008 -> 1262 us).
 int delta_segments(const DeltaShape& d) {
     const int64_t heads = static_cast<int64_t>(d.B) * d.H, p = d.P / 16, r = d.R / 16;
     if (d.N < 16 || heads * p > 256) return 1;  // (few chunks; heads that fill the chip)

@@ -65,6 +65,21 @@ def test_scales_are_fp32_whatever_torchs_default_type(monkeypatch, default):
     assert out["scale"] is seen["scale"] and out["scale"].dtype == torch.float32 and out["scale"].shape == (3, 2)
 
 
+@pytest.mark.parametrize("b,s,h,p,r,io,cut", [
+    (1, 16384, 96, 16, 128, 1, False), (1, 4096, 96, 16, 128, 1, False), (1, 16384, 96, 32, 64, 1, False),
+    (1, 16384, 128, 32, 64, 1, False), (1, 16384, 128, 16, 16, 0, False), (1, 4096, 192, 16, 16, 1, False),
+    (1, 16384, 8, 16, 128, 1, True), (1, 4096, 8, 64, 128, 1, True), (1, 65536, 32, 64, 128, 0, True)])
+def test_narrow_states_of_many_heads_are_not_cut_into_segments(lib, b, s, h, p, r, io, cut):
+    """Where a state has few rows a workgroup takes fewer tiles, and carries of many heads take longer
+    than the outputs they shorten.  A forward in segments shows in its workspace, by what lies between
+    them."""
+    up = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    n = b * h * (s // 64)
+    whole = up(8 * b) + up(1536 * n) + up(18432 * n) + up((12288 if io else 18432) * n)
+    got = ssd.ssd_delta_workspace_size(dims(b=b, s=s, hk=h, h=h, p=p, r=r, io=io), False)
+    assert got > whole if cut else got == whole
+
+
 # ---------------------------------------------------------------------------- the binding's own checks
 class OnDevice(torch.Tensor):
     """A host tensor that says it lies on a GPU."""

@@ -74,7 +74,7 @@ def segmented(b, s, h, p, r, dtype):
 # outputs of two and four tiles to a workgroup, with carries of each kind
 @pytest.mark.parametrize("b,s,h,p,r,dtype", [
     (1, 8960, 32, 64, 128, F32), (1, 4864, 12, 128, 128, F32), (1, 4090, 20, 64, 16, F32), (1, 2560, 24, 64, 128, F32),
-    (1, 2560, 48, 32, 32, F32), (2, 2555, 20, 64, 64, BF16), (1, 6144, 12, 128, 128, BF16), (1, 1792, 32, 64, 128, BF16),
+    (1, 3580, 48, 32, 32, F32), (2, 2555, 20, 64, 64, BF16), (1, 6144, 12, 128, 128, BF16), (1, 1792, 32, 64, 128, BF16),
     (1, 1792, 20, 64, 16, BF16), (3, 1536, 1, 128, 128, BF16)])
 def test_segments_of_many_tiles(b, s, h, p, r, dtype):
     assert segmented(b, s, h, p, r, dtype)
