@@ -19,6 +19,8 @@
 //
 // Tokens past a row's length are zeros in every operand with g = beta = 0: they change no
 // state, give zero outputs and gradients, and their memory is not read.
+#include <type_traits>
+
 #include "delta_device.hpp"
 #include "ssd_launch.hpp"
 
@@ -1225,29 +1227,22 @@ hipError_t scan_r(const DeltaShape& d, const DeltaBufs& f, ScanMode mode, int se
     return hipErrorInvalidValue;
 }
 
-template <class IO, int R>
-hipError_t scans(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
-    // in place (final_state is init) the chunks run through: side by side, the last segment would write
-    // what the first may still have to read
-    const int segs = bwd || (f.init && f.init == f.final_state) ? 1 : delta_segments(d);
-    if (segs > 1) {
-        if (hipError_t e = scan_r<IO, R>(d, f, kCarry, segs, st); e != hipSuccess) return e;
-        const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * (d.P / 16)));
-        k_delta_join<R><<<grid, 256, 0, st>>>(d, f.len, f.carry, segs, (d.N + segs - 1) / segs);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    }
-    return scan_r<IO, R>(d, f, bwd ? kReverse : kOutputs, segs, st);
-}
-
-template <class IO>
-hipError_t by_r(const DeltaShape& d, const DeltaBufs& f, bool prep, bool bwd, hipStream_t st) {
+template <class F>
+hipError_t by_r(const DeltaShape& d, F&& f) {
     switch (d.R) {
-        case 16: return prep ? prep_r<IO, 16>(d, f, bwd, st) : scans<IO, 16>(d, f, bwd, st);
-        case 32: return prep ? prep_r<IO, 32>(d, f, bwd, st) : scans<IO, 32>(d, f, bwd, st);
-        case 64: return prep ? prep_r<IO, 64>(d, f, bwd, st) : scans<IO, 64>(d, f, bwd, st);
-        case 128: return prep ? prep_r<IO, 128>(d, f, bwd, st) : scans<IO, 128>(d, f, bwd, st);
+        case 16: return f(std::integral_constant<int, 16>{});
+        case 32: return f(std::integral_constant<int, 32>{});
+        case 64: return f(std::integral_constant<int, 64>{});
+        case 128: return f(std::integral_constant<int, 128>{});
         default: return hipErrorInvalidValue;
     }
+}
+
+hipError_t scan(const DeltaShape& d, const DeltaBufs& f, ScanMode mode, int segs, hipStream_t st) {
+    return by_r(d, [&](auto r) {
+        constexpr int R = decltype(r)::value;
+        return d.io == 1 ? scan_r<BF16, R>(d, f, mode, segs, st) : scan_r<F32, R>(d, f, mode, segs, st);
+    });
 }
 
 }  // namespace
@@ -1290,11 +1285,30 @@ int delta_segments(const DeltaShape& d) {
 }
 
 hipError_t launch_delta_prep(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
-    return d.io == 1 ? by_r<BF16>(d, f, true, bwd, st) : by_r<F32>(d, f, true, bwd, st);
+    return by_r(d, [&](auto r) {
+        constexpr int R = decltype(r)::value;
+        return d.io == 1 ? prep_r<BF16, R>(d, f, bwd, st) : prep_r<F32, R>(d, f, bwd, st);
+    });
 }
 
-hipError_t launch_delta_scan(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st) {
-    return d.io == 1 ? by_r<BF16>(d, f, false, bwd, st) : by_r<F32>(d, f, false, bwd, st);
+hipError_t launch_delta_carry(const DeltaShape& d, const DeltaBufs& f, int segs, hipStream_t st) {
+    return scan(d, f, kCarry, segs, st);
+}
+
+hipError_t launch_delta_join(const DeltaShape& d, const DeltaBufs& f, int segs, hipStream_t st) {
+    return by_r(d, [&](auto r) {
+        const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * (d.P / 16)));
+        k_delta_join<decltype(r)::value><<<grid, 256, 0, st>>>(d, f.len, f.carry, segs, (d.N + segs - 1) / segs);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_delta_scan(const DeltaShape& d, const DeltaBufs& f, int segs, hipStream_t st) {
+    return scan(d, f, kOutputs, segs, st);
+}
+
+hipError_t launch_delta_states(const DeltaShape& d, const DeltaBufs& f, hipStream_t st) {
+    return scan(d, f, kReverse, 1, st);
 }
 
 }  // namespace ssd

@@ -1106,7 +1106,14 @@ int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, cons
     f.y = y;
     f.final_state = final_state;
     SSD_HIP(ssd::launch_delta_prep(d, f, false, st), "k_delta_prep");
-    SSD_HIP(ssd::launch_delta_scan(d, f, false, st), "k_delta_scan");
+    // in place (final_state is init) the chunks run through: side by side, the last segment would write
+    // what the first may still have to read
+    const int segs = init && init == final_state ? 1 : ssd::delta_segments(d);
+    if (segs > 1) {
+        SSD_HIP(ssd::launch_delta_carry(d, f, segs, st), "k_delta_carry");
+        SSD_HIP(ssd::launch_delta_join(d, f, segs, st), "k_delta_join");
+    }
+    SSD_HIP(ssd::launch_delta_scan(d, f, segs, st), "k_delta_scan");
     return ok();
 }
 
@@ -1155,7 +1162,7 @@ int ssd_delta_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fin
     f.d_beta = d_beta;
     f.d_init = d_init;
     SSD_HIP(ssd::launch_delta_prep(d, f, true, st), "k_delta_prep");
-    SSD_HIP(ssd::launch_delta_scan(d, f, true, st), "k_delta_states");
+    SSD_HIP(ssd::launch_delta_states(d, f, st), "k_delta_states");
     SSD_HIP(ssd::launch_delta_grad(d, f, st), "k_delta_grad");
     return ok();
 }

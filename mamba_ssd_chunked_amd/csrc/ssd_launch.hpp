@@ -317,8 +317,13 @@ int delta_segments(const DeltaShape& d);
 
 // Decay factors and triangular operands of every chunk.
 hipError_t launch_delta_prep(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st);
-// The recurrence over chunks: y and the final state, or for the backward H, E, dH, dZ, d_init.
-hipError_t launch_delta_scan(const DeltaShape& d, const DeltaBufs& f, bool bwd, hipStream_t st);
+// The recurrence over chunks: y and the final state.  In more than one segment, what each segment does
+// to the state and the states between them come first.
+hipError_t launch_delta_carry(const DeltaShape& d, const DeltaBufs& f, int segs, hipStream_t st);
+hipError_t launch_delta_join(const DeltaShape& d, const DeltaBufs& f, int segs, hipStream_t st);
+hipError_t launch_delta_scan(const DeltaShape& d, const DeltaBufs& f, int segs, hipStream_t st);
+// The backward's two recurrences: H, E, dH, dZ, d_init.
+hipError_t launch_delta_states(const DeltaShape& d, const DeltaBufs& f, hipStream_t st);
 // The gradients of every chunk from H, E, dH, dZ.
 hipError_t launch_delta_grad(const DeltaShape& d, const DeltaBufs& f, hipStream_t st);
 

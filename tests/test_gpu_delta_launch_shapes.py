@@ -101,3 +101,18 @@ def test_segments_are_bitwise_reproducible(b, s, h, p, r, dtype):
         torch.cuda.synchronize()
         first = first or (y, final)
         assert torch.isfinite(final).all() and torch.equal(y, first[0]) and torch.equal(final, first[1])
+
+
+@pytest.mark.parametrize("s,names", [(200, {"k_delta_prep", "k_delta_scan"}),
+                                     (4096, {"k_delta_prep", "k_delta_carry", "k_delta_join", "k_delta_scan"})])
+def test_each_kernel_is_timed_under_its_name(s, names):
+    w = dev(ref.delta_inputs(1, s, 2, 2, 16, 32, seed=441, dtype=BF16))
+    say("case timed", s)
+    ssd.ssd_timing_enable(True)
+    try:
+        for _ in range(3):
+            ssd.delta_rule(*(w[n] for n in NAMES), init=w["init"])
+        got = ssd.ssd_timing_collect()
+    finally:
+        ssd.ssd_timing_enable(False)
+    assert set(got) == names and all(ms > 0 and n == 3 for ms, n in got.values())
