@@ -341,9 +341,9 @@ int ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int
  * bf16 io: the products take the bf16 inputs as they are and everything else (states, decays, the
  * triangular inverse, sums) in fp32; y, d_q, d_k, d_v are rounded to nearest even.  Results are
  * bitwise reproducible.  A NaN or an infinity among a row's tokens spreads over its chunk of 64
- * tokens and on from there, in that head (and d_q, d_k of its key head) only.  No launch exceeds
- * 2^32 work-items: batch * nheads * max(8 * (seq + 63), 16 * max(headdim, 64)) < 2^32
- * (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
+ * tokens and on from there, in that head (and d_q, d_k of its key head) only, but to no token past
+ * the row's length.  No launch exceeds 2^32 work-items: batch * nheads * max(8 * (seq + 63),
+ * 16 * max(headdim, 64)) < 2^32 (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,
  * SSD_ERR_HIP.
  */
@@ -375,7 +375,8 @@ int ssd_delta_fwd(const ssd_delta_dims* dims, const void* q, const void* k, cons
 /*
  * Gradients of <dy, y> + <d_final, final_state> from the leaves (the states are recomputed).
  * d_final and init nullable (= zero), d_init nullable (not written; it may equal d_final, but not
- * overlap it otherwise: SSD_ERR_UNSUPPORTED); the other gradients are required.  d_q and d_k are summed over the value heads that share a key head.
+ * overlap it otherwise: SSD_ERR_UNSUPPORTED); the other gradients are required.  d_q and d_k are
+ * summed over the value heads that share a key head.
  */
 int ssd_delta_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_final, const void* q,
                   const void* k, const void* v, const float* g, const float* beta,
@@ -408,8 +409,9 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
  * NULL without one; y is nullable if y8 is given; y8 and scale come together or not at all.
  * 0 <= rows < 2^22 (a launch has up to 1024 work-items per row; rows do not depend on each other, so
  * more are split over calls; SSD_ERR_UNSUPPORTED), 0 < width <= 32768, group 0 or 32, 64, 128 or 256
- * and dividing width.  Tensors are contiguous and 16-byte aligned.  s is rounded to the io dtype where it is stored; the norm is
- * taken of the fp32 sum, and y and y8 are each rounded once from fp32.
+ * and dividing width.  Tensors are contiguous and 16-byte aligned.  s is rounded to the io dtype where
+ * it is stored; the norm is taken of the fp32 sum.  y is rounded once from fp32, and y8 is the fp32
+ * quotient of that fp32 value and the stored scale (of a scale below 2^-109 the unrounded one).
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_HIP.
  */
 int ssd_rms_norm(int64_t rows, int64_t width, int io_dtype, float eps, const void* x,
@@ -422,8 +424,8 @@ int ssd_rms_norm(int64_t rows, int64_t width, int io_dtype, float eps, const voi
  *   d_x = d_s + (weight dy - n mean(n weight dy)) / sqrt(mean(s^2) + eps)   [rows, width] io dtype
  *   d_weight = sum over rows of dy n                                        [width] fp32
  * d_s is nullable (= zero); d_x may be d_s; any number of rows (rows * width up to 2^60).  The
- * workspace (ssd_rms_norm_workspace_size, 256-byte
- * aligned) holds partial sums of d_weight, which are added in a fixed order.
+ * workspace (ssd_rms_norm_workspace_size, 256-byte aligned) holds partial sums of d_weight, which are
+ * added in a fixed order.
  */
 int ssd_rms_norm_bwd(int64_t rows, int64_t width, int io_dtype, float eps, const void* dy,
                      const void* s, const void* d_s, const float* weight, void* d_x,

@@ -137,14 +137,15 @@ __device__ __forceinline__ void invert_lower(const float* C, float* X) {
 }  // namespace
 
 // Per (b, h, chunk): the chunk's decay factors (coef: e^G, e^{G_L - G}, beta, and G in base 2
-// and fp64) and its triangular matrices as bf16 parts in operand order.  Forward: M and P (rows
+// and fp64) and its triangular matrices in operand order, as bf16 parts (P of bf16 io's forward in
+// fp32).  Forward: M and P (rows
 // t, k over s); backward: M, and N^T and P^T (rows s, k over t).
 //
 // Wave w has the tokens 16 w .. + 15: their rows of K and Q stay in its registers as operands, and
 // the key rows of the others come through LDS, which the fp32 matrices take over afterwards.
 //
 // Bound by HBM: it reads q and k and writes two triangular matrices.  160 heads of 64 chunks, bf16,
-// r = 128: 0.79 GB in 139-146 us, 5.4 TB/s (with K and Q as fp32 in LDS and substitution there: 217
+// r = 128: 0.79 GB in 137-147 us, 5.7 TB/s (with K and Q as fp32 in LDS and substitution there: 217
 // us); 32 heads of 1024 chunks, fp32: 3.9 GB in 644-664 us.  A preparation of its own doubles the
 // reads of q and k, but has the inverses, long chains of dependent steps, in 10,240 workgroups at once
 // instead of in the 160 of the scan, each before the next chunk.
@@ -360,11 +361,12 @@ __host__ __device__ constexpr int scan_loaders() { return in_parts<IO>() == 1 ? 
 // (Computing waves that issued the loads themselves: bf16, 160 heads, 291 against 232 us; loads
 // into registers there: 1084 us.)
 //
-// Measured with outputs, p = 64, r = 128, a chunk in each launch shape: bf16 3.6 us (four single
-// waves, 160 workgroups on as many CUs, so that 96 of the 256 stand idle: 64 chunks 232 us); fp32
-// 3.4 us (one team), 6.1 us (two teams), 9.7 us (four waves).  Single waves in fp32 at 256 tiles: 4.9 ms for 1024 chunks
-// against 3.5 ms by teams.  A team's sums cost more than its shorter chain wins where the chip is
-// full of single waves.
+// Measured with outputs, p = 64, r = 128, a chunk in each launch shape: bf16 4.1 us (four single
+// waves, 160 workgroups on as many CUs, so that 96 of the 256 stand idle: 64 chunks 260 us; 3.6 and
+// 232 with y's operands in two parts, whose y misses the nearest bf16 value once in 400); fp32
+// 3.4 us (one team), 6.1 us (two teams), 9.7 us (four waves).  Single waves in fp32 at 256 tiles: 4.9 ms
+// for 1024 chunks against 3.5 ms by teams.  A team's sums cost more than its shorter chain wins where
+// the chip is full of single waves.
 //
 // fp32 keys and queries are cut into parts by the loading waves: written as parts by the
 // preparation they are half as large again in every read (32 heads of 1024 chunks: preparation 1314,
@@ -397,8 +399,8 @@ struct Scan {
                          oC = oV + VBYTES, oX = oC + 2 * 4 * DCF, LDS = oX + (TM > 1 ? CW * 4096 : 0);
     // loads of one loading wave
     static constexpr int per(int n) { return (n + NL - 1) / NL; }
-    static constexpr int nK = CUT ? 0 : per(QT), nQ = nK, nM = per(3 * DTRI), nP = per(PK * DTRI), nV = per(VBYTES / 1024),
-                         nC = 1;
+    static constexpr int nK = CUT ? 0 : per(QT), nQ = nK, nM = per(3 * DTRI), nP = per(PK * DTRI),
+                         nV = per(VBYTES / 1024), nC = 1;
 
     char* sm;
     const DeltaShape& d;
@@ -724,7 +726,8 @@ struct Scan {
     __device__ PTile p_tile(int tile) const {
         PTile o;
 #pragma unroll
-        for (int n = 0; n < PK; ++n) o.x[n] = at4(reinterpret_cast<const float*>(sm + oP + (n * DTRI + tile) * 1024 + lane * 16));
+        for (int n = 0; n < PK; ++n)
+            o.x[n] = at4(reinterpret_cast<const float*>(sm + oP + (n * DTRI + tile) * 1024 + lane * 16));
         return o;
     }
     __device__ static Parts<3> p_parts(const PTile& p) {

@@ -6,12 +6,12 @@
 // Gradient: with rstd = rsqrt(mean(s^2) + eps) and n = s rstd,
 //   d_x = d_s + rstd (w dy - n mean(n w dy)),   d_w = sum over rows of dy n.
 // A row is read once and kept in registers (the gradient's of more than 16384 values, or of more than
-// 8192 that are not whole vectors, partly in scratch: 92 to 376 bytes a thread): bound by HBM.  8192 rows of 5120 bf16 values with
-// residual, s and 8-bit output: 60 us, 4.9 TB/s; 8192 rows of 1536 in fp32: forward 36 us, 5.5 TB/s,
-// gradient 35 us and 5 us for joining the weight gradient; 64 rows: 5 us, a launch's latency.
-// A team of 64, 256 or 1024 threads has a row; a thread's vectors lie a team apart, so each load of a
-// team is contiguous.  Sums are
-// fp32; y is rounded once (to the io type or to 8 bits), never through the io type first.
+// 8192 that are not whole vectors, partly in scratch: 92 to 376 bytes a thread): bound by HBM.  8192
+// rows of 5120 bf16 values with residual, s and 8-bit output: 60 us, 4.9 TB/s; 8192 rows of 1536 in
+// fp32: forward 36 us, 5.5 TB/s, gradient 35 us and 5 us for joining the weight gradient; 64 rows: 6 us,
+// a launch's latency.  A team of 64, 256 or 1024 threads has a row; a thread's vectors lie a team apart,
+// so each load of a team is contiguous.  Sums are fp32; y is rounded once to the io type, and its fp32
+// values, not those, are divided for the 8 bits.
 // The weight gradient is summed per team over its rows in registers, written once per team, and
 // added up by a second kernel in team order: no atomics, bitwise reproducible.
 #include <type_traits>

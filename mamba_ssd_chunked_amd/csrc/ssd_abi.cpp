@@ -506,7 +506,8 @@ int check_delta_lens(const char* who, const ssd::DeltaShape& d, const int64_t* v
 }
 
 // Workspace of the delta rule: the lengths, then per chunk and head the coefficients and the
-// triangular operands (6 tiles of 512 bf16 values a part); the backward adds the other triangular
+// triangular operands (6 tiles of 512 bf16 values in three parts; P of a bf16 forward in fp32, the
+// bytes of two); the backward adds the other triangular
 // operands, the entry states and the gradients of the leaving states, E and dZ; a forward in
 // segments the states and transitions between them.
 size_t delta_plan(const ssd::DeltaShape& d, bool bwd, void* ws, ssd::DeltaBufs* f) {

@@ -299,7 +299,7 @@ struct DeltaShape {
 
 // Everything the delta kernels read and write.  len: device copy of valid_len, or null.
 // Workspace, per (b, h, chunk): coef; M, P (forward and backward), NT (backward) in bf16
-// parts; the backward's entry states H and leaving gradients dH [r, p], E and dZ [64, p].
+// parts, but P of a bf16 forward in fp32; the backward's entry states H and leaving gradients dH [r, p], E and dZ [64, p].
 struct DeltaBufs {
     const void *q, *k, *v, *dy;
     const float *g, *beta, *init, *d_final;
