@@ -399,6 +399,62 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
                    const int32_t* slots, void* y, void* stream);
 
 /*
+ * Linear attention with a decay for each head: a recurrence whose memory fades at a rate of the head's
+ * own, the same at every token.  Per value head, with the state H [p, r] and a = exp(log_decay[head]):
+ *   H_t = a H_{t-1} + v_t k_t^T,   y_t = scale H_t q_t,   H_{-1} = init.
+ * Layouts, strides, shared key heads, types, alignment and valid_len as of the delta rule above
+ * (ssd_delta_dims holds the same fields):
+ *   q, k         [b, s, hk, r]  io dtype, strided     v  [b, s, h, p]  io dtype, strided
+ *   log_decay, d_decay  [h]     fp32 (<= 0 for a decay; 0 forgets nothing; -inf keeps a token's own only)
+ *   y, dy, d_v   [b, s, h, p]   io dtype, contiguous  d_q, d_k  [b, s, hk, r]  io dtype, contiguous
+ *   init, final_state, d_final, d_init  [b, h, p, r]  fp32
+ * headdim and dstate in {16, 32, 64, 128}; any seq (an empty one: final = init, d_init = d_final,
+ * d_decay = 0); tokens at or past a row's valid_len are not read, leave the state alone, and give y and
+ * gradients of exactly zero.
+ * bf16 io: the products take the bf16 inputs as they are and everything else (states, decays, the
+ * causal matrix, sums) to 24 bits; y, d_q, d_k, d_v are rounded to nearest even.  Results are bitwise
+ * reproducible.  A NaN or an infinity among a row's tokens spreads over its chunk of 64 tokens and on
+ * from there (in the gradients of keys and values: back from there), in that head (and d_q, d_k of its
+ * key head, d_decay of the head) only, but to no token past the row's length.
+ * 512 * batch * nheads < 2^32 (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
+ * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,
+ * SSD_ERR_HIP.
+ */
+
+/* Workspace bytes (256-byte aligned buffer) of ssd_linear_fwd (bwd == 0) or ssd_linear_bwd. */
+int ssd_linear_workspace_size(const ssd_delta_dims* dims, int bwd, size_t* bytes);
+
+/*
+ * Outputs of a whole sequence, chunk by chunk.  final_state and init are nullable (not written; zero
+ * initial state).  final_state may equal init (updated in place), otherwise the two must not overlap
+ * (SSD_ERR_UNSUPPORTED).  Nothing is saved for the backward.
+ */
+int ssd_linear_fwd(const ssd_delta_dims* dims, const void* q, const void* k, const void* v,
+                   const float* log_decay, const float* init, const int64_t* valid_len, void* y,
+                   float* final_state, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of <dy, y> + <d_final, final_state> from the leaves (the states are recomputed).
+ * d_final and init nullable (= zero); d_init nullable (not written; it may equal d_final, but not
+ * overlap it otherwise: SSD_ERR_UNSUPPORTED); d_decay nullable (not computed: decays that are not
+ * learned); the other gradients are required.  d_q and d_k are summed over the value heads that share
+ * a key head, d_decay over the batch and all tokens.
+ */
+int ssd_linear_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_final, const void* q,
+                   const void* k, const void* v, const float* log_decay, const float* init,
+                   const int64_t* valid_len, void* d_q, void* d_k, void* d_v, float* d_decay,
+                   float* d_init, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One token from cached states, updated in place (decoding), with slots as ssd_delta_step's: state
+ * [nslots, h, p, r] fp32, q, k [b, hk, r], v [b, h, p] strided, log_decay [h], y [b, h, p].
+ * No workspace; may be captured into a graph.
+ */
+int ssd_linear_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, const void* k,
+                    const void* v, const float* log_decay, float* state, const int32_t* slots, void* y,
+                    void* stream);
+
+/*
  * Root-mean-square norm over rows, with the residual's addition and an 8-bit output:
  *   s = x + residual (s = x without one),   n = s / sqrt(mean(s^2) + eps),   y = n weight
  *   8 bits: per group of `group` values of a row (0: the row), scale = max|y| / 448, or 1 where y

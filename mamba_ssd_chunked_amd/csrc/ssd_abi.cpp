@@ -453,7 +453,10 @@ bool overlap_unequal(const float* x, const float* y, size_t n) {
 }
 
 // ------------------------------------------------------------ gated delta rule, norm
-int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape* d) {
+// Dims of the delta rule and of linear attention; per_bh: the largest launch's work-items for each batch
+// row and head, given the dims.
+template <class F>
+int validate_heads(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape* d, F&& per_bh) {
     if (!dims) return fail(SSD_ERR_NULL, "%s: dims is NULL", who);
     if (dims->io_dtype != SSD_F32 && dims->io_dtype != SSD_BF16)
         return fail(SSD_ERR_DTYPE, "%s: io_dtype must be SSD_F32 (0) or SSD_BF16 (1) (got %d)", who, dims->io_dtype);
@@ -466,12 +469,8 @@ int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape*
     if (!pow2_in(dims->headdim, 16, 128) || !pow2_in(dims->dstate, 16, 128))
         return fail(SSD_ERR_UNSUPPORTED, "%s: headdim and dstate must be 16, 32, 64 or 128 (got %lld, %lld)", who,
                     (long long)dims->headdim, (long long)dims->dstate);
-    // a workgroup of at most 512 work-items per chunk of 64 tokens and head; the two recurrences of
-    // the backward, 512 each for 64 value columns (or fewer) of a head
-    const double per_bh =
-        std::max(8.0 * ((double)dims->seq + 63.0), 16.0 * std::max((double)dims->headdim, 64.0));
     if (dims->batch > (1 << 30) || dims->seq > (1 << 30) || dims->nheads > (1 << 30) ||
-        (double)dims->batch * dims->nheads * per_bh > ssd::kMaxGridItems)
+        (double)dims->batch * dims->nheads * per_bh(*dims) > ssd::kMaxGridItems)
         return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch would exceed 2^32 work-items "
                     "(split the batch or the heads)", who);
     const int64_t unit = dims->io_dtype == SSD_BF16 ? 8 : 4;  // 16 bytes
@@ -494,6 +493,62 @@ int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape*
     d->N = (int)((dims->seq + 63) / 64);
     d->scale = dims->scale;
     return SSD_OK;
+}
+
+int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape* d) {
+    // a workgroup of at most 512 work-items per chunk of 64 tokens and head; the two recurrences of
+    // the backward, 512 each for 64 value columns (or fewer) of a head
+    return validate_heads(who, dims, d, [](const ssd_delta_dims& n) {
+        return std::max(8.0 * ((double)n.seq + 63.0), 16.0 * std::max((double)n.headdim, 64.0));
+    });
+}
+
+// Linear attention: two workgroups of 256 at most for each head (many only where heads are few).
+int validate_linear(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape* d) {
+    return validate_heads(who, dims, d, [](const ssd_delta_dims&) { return 512.0; });
+}
+
+ssd::LinearShape linear_shape(const ssd::DeltaShape& d, const float* log_decay, int jobs) {
+    const int c = ssd::linear_chunk(d.io);
+    ssd::LinearShape s{d.B, d.S, d.H, d.P, d.R, d.io, (d.S + c - 1) / c, 1, 0, nullptr, log_decay};
+    s.segs = ssd::linear_segments(s, jobs);
+    s.seg_chunks = (s.N + s.segs - 1) / s.segs;
+    return s;
+}
+
+// Workspace of linear attention: the lengths; in segments their entry states (the backward: of both
+// directions, and of the derivative along the decay); the backward's per-head d_q and d_k where
+// key heads are shared, and the sums of the decay's gradient.
+struct LinearBufs {
+    int64_t* len;
+    float *H, *G, *dq, *dk;
+    double* dots;
+};
+size_t linear_plan(const ssd::DeltaShape& d, const ssd::LinearShape& s, bool bwd, void* ws, LinearBufs* f) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char* at = static_cast<char*>(ws) + off;
+        off += round_up(bytes);
+        return at;
+    };
+    const size_t states = s.segs > 1 ? 4 * static_cast<size_t>(s.B) * s.H * s.segs * s.P * s.R : 0;
+    const size_t rows = 4 * static_cast<size_t>(s.B) * s.S * s.H * s.R;
+    f->len = reinterpret_cast<int64_t*>(take(8 * static_cast<size_t>(s.B)));
+    f->H = reinterpret_cast<float*>(take(bwd ? 2 * states : states));
+    if (bwd) {
+        f->G = reinterpret_cast<float*>(take(states));
+        f->dq = reinterpret_cast<float*>(take(d.H != d.HK ? rows : 0));
+        f->dk = reinterpret_cast<float*>(take(d.H != d.HK ? rows : 0));
+        f->dots = reinterpret_cast<double*>(take(8 * static_cast<size_t>(s.H) * ssd::linear_dots(s)));
+    }
+    return off;
+}
+
+void set_strides(int64_t (&to)[3], const int64_t (&from)[3]) { std::copy(from, from + 3, to); }
+void dense_strides(int64_t (&to)[3], const ssd::DeltaShape& d, int64_t heads, int64_t width) {
+    to[0] = d.S * heads * width;
+    to[1] = heads * width;
+    to[2] = width;
 }
 
 int check_delta_lens(const char* who, const ssd::DeltaShape& d, const int64_t* valid_len) {
@@ -557,6 +612,18 @@ int validate_norm(const char* who, int64_t rows, int64_t width, int io_dtype, fl
         return fail(SSD_ERR_UNSUPPORTED, "%s: rows * width must be at most 2^60 (got %lld, %lld)", who, (long long)rows,
                     (long long)width);
     *n = ssd::NormShape{rows, (int)width, (int)width, io_dtype, eps};
+    return SSD_OK;
+}
+
+// one workgroup of 256 work-items per (b, h)
+int check_step(const char* who, const ssd::DeltaShape& d, int64_t nslots, const int32_t* slots) {
+    if (d.S != 1) return fail(SSD_ERR_SHAPE, "%s: seq must be 1 (got %d)", who, d.S);
+    if (nslots < 0 || nslots > INT32_MAX || (!slots && nslots < d.B))
+        return fail(SSD_ERR_SHAPE, "%s: nslots = %lld: need at least one slot per row without slots", who,
+                    (long long)nslots);
+    if ((double)d.B * d.H * 256.0 > ssd::kMaxGridItems)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch would exceed 2^32 work-items "
+                    "(split the batch)", who);
     return SSD_OK;
 }
 
@@ -1173,20 +1240,232 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
     const char* who = "ssd_delta_step";
     ssd::DeltaShape d;
     if (int rc = validate_delta(who, dims, &d)) return rc;
-    if (d.S != 1) return fail(SSD_ERR_SHAPE, "%s: seq must be 1 (got %d)", who, d.S);
-    if (nslots < 0 || nslots > INT32_MAX || (!slots && nslots < d.B))
-        return fail(SSD_ERR_SHAPE, "%s: nslots = %lld: need at least one slot per row without slots", who,
-                    (long long)nslots);
-    // one workgroup of 256 work-items per (b, h)
-    if ((double)d.B * d.H * 256.0 > ssd::kMaxGridItems)
-        return fail(SSD_ERR_UNSUPPORTED, "%s: problem too large for one call: a launch would exceed 2^32 work-items "
-                    "(split the batch)", who);
+    if (int rc = check_step(who, d, nslots, slots)) return rc;
     if (d.B == 0) return ok();
     if (!q || !k || !v || !g || !beta || !y || (!state && nslots > 0))
         return fail(SSD_ERR_NULL, "%s: q, k, v, g, beta, state and y are required", who);
     if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {state, "state"}})) return rc;
     hipStream_t st = static_cast<hipStream_t>(stream);
     SSD_HIP(ssd::launch_delta_step(d, (int)nslots, q, k, v, g, beta, state, slots, y, st), "k_delta_step");
+    return ok();
+}
+
+int ssd_linear_workspace_size(const ssd_delta_dims* dims, int bwd, size_t* bytes) {
+    ssd::DeltaShape d;
+    if (int rc = validate_linear("ssd_linear_workspace_size", dims, &d)) return rc;
+    if (!bytes) return fail(SSD_ERR_NULL, "ssd_linear_workspace_size: bytes is NULL");
+    LinearBufs f{};
+    *bytes = linear_plan(d, linear_shape(d, nullptr, bwd ? 2 : 1), bwd != 0, nullptr, &f);
+    return ok();
+}
+
+int ssd_linear_fwd(const ssd_delta_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                   const float* init, const int64_t* valid_len, void* y, float* final_state, void* ws, size_t ws_bytes,
+                   void* stream) {
+    const char* who = "ssd_linear_fwd";
+    ssd::DeltaShape d;
+    if (int rc = validate_linear(who, dims, &d)) return rc;
+    const bool tok = d.B > 0 && d.S > 0;
+    if (tok && (!q || !k || !v || !log_decay || !y))
+        return fail(SSD_ERR_NULL, "%s: q, k, v, log_decay and y are required", who);
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {y, "y"}, {init, "init"}, {final_state, "final_state"}})) return rc;
+    if (overlap_unequal(init, final_state, (size_t)d.B * d.H * d.P * d.R))
+        return fail(SSD_ERR_UNSUPPORTED, "%s: init and final_state overlap without being equal", who);
+    if (int rc = check_delta_lens(who, d, valid_len)) return rc;
+    ssd::LinearShape s = linear_shape(d, log_decay, 1);
+    LinearBufs f{};
+    const size_t need = linear_plan(d, s, false, ws, &f);
+    if (tok)
+        if (int rc = check_delta_ws(who, need, ws, ws_bytes)) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (!tok) {
+        const int64_t nstate = static_cast<int64_t>(d.B) * d.H * d.P * d.R;
+        if (final_state) SSD_HIP(ssd::launch_copy_or_zero(final_state, init, nstate, st), "copy init");
+        return ok();
+    }
+    if (valid_len) {
+        SSD_HIP(ssd::launch_set_i64(f.len, valid_len, d.S, d.B, st), "set_i64");
+        s.len = f.len;
+    }
+    ssd::LinearJobs jobs{};
+    jobs.n = 1;
+    ssd::LinearJob& j = jobs.job[0];
+    j.q = q;
+    j.k = k;
+    j.v = v;
+    j.dst = y;
+    j.init = init;
+    j.fin = final_state;
+    j.carry = f.H;
+    set_strides(j.qs, d.qs);
+    set_strides(j.ks, d.ks);
+    set_strides(j.vs, d.vs);
+    dense_strides(j.os, d, d.H, d.P);
+    j.csc = d.R;
+    j.csr = 1;
+    j.cstep = static_cast<int64_t>(d.P) * d.R;
+    j.out = d.scale;
+    j.in = 1.0f;
+    j.qdiv = j.kdiv = d.H / d.HK;
+    j.vdiv = 1;
+    if (s.segs > 1) {
+        SSD_HIP(ssd::launch_linear_carry(s, jobs, false, st), "k_linear_carry");
+        SSD_HIP(ssd::launch_linear_join(s, jobs, false, st), "k_linear_join");
+    }
+    SSD_HIP(ssd::launch_linear_scan(s, jobs, st), "k_linear");
+    return ok();
+}
+
+int ssd_linear_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_final, const void* q, const void* k,
+                   const void* v, const float* log_decay, const float* init, const int64_t* valid_len, void* d_q,
+                   void* d_k, void* d_v, float* d_decay, float* d_init, void* ws, size_t ws_bytes, void* stream) {
+    const char* who = "ssd_linear_bwd";
+    ssd::DeltaShape d;
+    if (int rc = validate_linear(who, dims, &d)) return rc;
+    const bool tok = d.B > 0 && d.S > 0;
+    if (tok && (!dy || !q || !k || !v || !log_decay || !d_q || !d_k || !d_v))
+        return fail(SSD_ERR_NULL, "%s: dy, q, k, v, log_decay, d_q, d_k and d_v are required", who);
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {dy, "dy"}, {d_q, "d_q"}, {d_k, "d_k"}, {d_v, "d_v"},
+                                  {init, "init"}, {d_final, "d_final"}, {d_init, "d_init"}}))
+        return rc;
+    if (overlap_unequal(d_final, d_init, (size_t)d.B * d.H * d.P * d.R))
+        return fail(SSD_ERR_UNSUPPORTED, "%s: d_final and d_init overlap without being equal", who);
+    if (int rc = check_delta_lens(who, d, valid_len)) return rc;
+    ssd::LinearShape s = linear_shape(d, log_decay, 2);
+    LinearBufs f{};
+    const size_t need = linear_plan(d, s, true, ws, &f);
+    if (tok)
+        if (int rc = check_delta_ws(who, need, ws, ws_bytes)) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (!tok) {
+        const int64_t nstate = static_cast<int64_t>(d.B) * d.H * d.P * d.R;
+        if (d_init) SSD_HIP(ssd::launch_copy_or_zero(d_init, d_final, nstate, st), "copy d_final");
+        if (d_decay) SSD_HIP(ssd::launch_copy_or_zero(d_decay, nullptr, d.H, st), "zero d_decay");
+        return ok();
+    }
+    if (valid_len) {
+        SSD_HIP(ssd::launch_set_i64(f.len, valid_len, d.S, d.B, st), "set_i64");
+        s.len = f.len;
+    }
+    const int grp = d.H / d.HK;
+    const int64_t size = static_cast<int64_t>(d.P) * d.R;
+    // what all of them share, and the states in the forward's order: columns p, rows r
+    ssd::LinearJob fwd{}, rev{};
+    fwd.init = init;
+    fwd.carry = f.H;
+    fwd.cstep = d_decay ? 2 * size : size;
+    rev.init = d_final;
+    rev.carry = f.G;
+    rev.cstep = size;
+    rev.rev = 1;
+    for (ssd::LinearJob* j : {&fwd, &rev}) {
+        j->csc = d.R;
+        j->csr = 1;
+        j->out = j->in = 1.0f;
+        j->qdiv = j->kdiv = j->vdiv = 1;
+    }
+    ssd::LinearJob tan = fwd, dv = rev;
+    tan.q = q;
+    tan.k = k;
+    tan.v = v;
+    tan.dst = const_cast<void*>(dy);
+    tan.d_final = d_final;
+    tan.dots = f.dots;
+    set_strides(tan.qs, d.qs);
+    set_strides(tan.ks, d.ks);
+    set_strides(tan.vs, d.vs);
+    dense_strides(tan.os, d, d.H, d.P);
+    tan.out = d.scale;
+    tan.qdiv = tan.kdiv = grp;
+    dv.q = k;
+    dv.k = q;
+    dv.v = dy;
+    dv.dst = d_v;
+    dv.fin = d_init;
+    set_strides(dv.qs, d.ks);
+    set_strides(dv.ks, d.qs);
+    dense_strides(dv.vs, d, d.H, d.P);
+    dense_strides(dv.os, d, d.H, d.P);
+    dv.in = d.scale;
+    dv.qdiv = dv.kdiv = grp;
+    // d_q and d_k: rows of the state are p, its columns r
+    ssd::LinearShape t = s;
+    t.P = d.R;
+    t.R = d.P;
+    ssd::LinearJobs two{};
+    two.n = 2;
+    two.job[0] = fwd;
+    two.job[1] = rev;
+    for (ssd::LinearJob& j : two.job) {
+        j.csc = 1;
+        j.csr = d.R;
+        j.vdiv = grp;
+        j.wide = grp > 1;
+        dense_strides(j.os, d, d.H, d.R);
+    }
+    ssd::LinearJob &dq = two.job[0], &dk = two.job[1];
+    dq.q = dy;
+    dq.k = v;
+    dq.v = k;
+    dq.dst = grp > 1 ? f.dq : d_q;
+    dense_strides(dq.qs, d, d.H, d.P);
+    set_strides(dq.ks, d.vs);
+    set_strides(dq.vs, d.ks);
+    dq.out = d.scale;
+    dk.q = v;
+    dk.k = dy;
+    dk.v = q;
+    dk.dst = grp > 1 ? f.dk : d_k;
+    set_strides(dk.qs, d.vs);
+    dense_strides(dk.ks, d, d.H, d.P);
+    set_strides(dk.vs, d.qs);
+    dk.in = d.scale;
+    ssd::LinearJobs one{};
+    one.n = 1;
+    if (s.segs > 1) {
+        ssd::LinearJobs both{};
+        both.n = 2;
+        both.job[0] = tan;
+        both.job[1] = dv;
+        if (d_decay) {
+            one.job[0] = tan;
+            SSD_HIP(ssd::launch_linear_carry(s, one, true, st), "k_linear_carry");
+            SSD_HIP(ssd::launch_linear_join(s, one, true, st), "k_linear_join");
+            one.job[0] = dv;
+            SSD_HIP(ssd::launch_linear_carry(s, one, false, st), "k_linear_carry");
+            SSD_HIP(ssd::launch_linear_join(s, one, false, st), "k_linear_join");
+        } else {
+            SSD_HIP(ssd::launch_linear_carry(s, both, false, st), "k_linear_carry");
+            SSD_HIP(ssd::launch_linear_join(s, both, false, st), "k_linear_join");
+        }
+    }
+    if (d_decay) {  // before d_init, which may lie in d_final's place
+        one.job[0] = tan;
+        SSD_HIP(ssd::launch_linear_tangent(s, one, st), "k_linear_tangent");
+        SSD_HIP(ssd::launch_linear_decay(s, f.dots, d_decay, st), "k_linear_decay");
+    }
+    SSD_HIP(ssd::launch_linear_scan(t, two, st), "k_linear");
+    one.job[0] = dv;
+    SSD_HIP(ssd::launch_linear_scan(s, one, st), "k_linear");
+    if (grp > 1) {
+        SSD_HIP(ssd::launch_linear_share(s, d.HK, d.R, f.dq, d_q, st), "k_linear_share");
+        SSD_HIP(ssd::launch_linear_share(s, d.HK, d.R, f.dk, d_k, st), "k_linear_share");
+    }
+    return ok();
+}
+
+int ssd_linear_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, const void* k, const void* v,
+                    const float* log_decay, float* state, const int32_t* slots, void* y, void* stream) {
+    const char* who = "ssd_linear_step";
+    ssd::DeltaShape d;
+    if (int rc = validate_linear(who, dims, &d)) return rc;
+    if (int rc = check_step(who, d, nslots, slots)) return rc;
+    if (d.B == 0) return ok();
+    if (!q || !k || !v || !log_decay || !y || (!state && nslots > 0))
+        return fail(SSD_ERR_NULL, "%s: q, k, v, log_decay, state and y are required", who);
+    if (int rc = check_aligned16({{q, "q"}, {k, "k"}, {v, "v"}, {state, "state"}})) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    SSD_HIP(ssd::launch_linear_step(d, (int)nslots, q, k, v, log_decay, state, slots, y, st), "k_linear_step");
     return ok();
 }
 

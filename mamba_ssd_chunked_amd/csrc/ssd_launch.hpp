@@ -332,6 +332,56 @@ hipError_t launch_delta_step(const DeltaShape& d, int nslots, const void* q, con
                              const float* g, const float* beta, float* state, const int32_t* slots, void* y,
                              hipStream_t st);
 
+// ---------------------------------------------------------------- linear attention
+// One scan (k_linear.hip) with its roles named for the forward: queries q, keys k (rows of width R),
+// values v and outputs dst (rows of width P).
+struct LinearShape {
+    int B, S, H, P, R;  // batch, tokens, heads, widths of the values and of the keys
+    int io;             // 0 = fp32, 1 = bf16
+    int N;              // chunks of linear_chunk(io) tokens
+    int segs, seg_chunks;  // segments of the chunk axis, and their chunks
+    const int64_t* len;    // device, null: all S
+    const float* log_decay;
+};
+struct LinearJob {
+    const void *q, *k, *v;
+    void* dst;               // outputs (kTangent: what they are multiplied by, read)
+    const float* init;       // entry state, null: zero
+    const float* d_final;    // kTangent: gradient of the final state, or null
+    float* fin;              // final state, or null
+    float* carry;            // [b, h, segments] slots of cstep floats: entry states
+    double* dots;            // kTangent: sums of the workgroups
+    int64_t qs[3], ks[3], vs[3], os[3];  // element strides (batch, token, head) of q, k, v, dst
+    int64_t csc, csr;        // strides of a state's columns (P) and rows (R) in memory
+    int64_t cstep;
+    float out, in;           // scales of the outputs and of what a token adds to the state
+    int qdiv, kdiv, vdiv;    // heads that share a head of q, k, v
+    int rev;                 // 1: from the last token to the first
+    int wide;                // 1: dst is fp32 whatever the io type
+};
+struct LinearJobs {
+    unsigned n;
+    LinearJob job[2];
+};
+int linear_chunk(int io);
+// Segments of the chunk axis to run side by side (1: it runs through).
+int linear_segments(const LinearShape& d, int jobs);
+// Outputs and final states; what each segment but the last adds to a state (and to its tangent); the
+// states the segments start from; the derivative along the decay, dotted with dst.
+hipError_t launch_linear_scan(const LinearShape& d, const LinearJobs& jobs, hipStream_t st);
+hipError_t launch_linear_carry(const LinearShape& d, const LinearJobs& jobs, bool tangent, hipStream_t st);
+hipError_t launch_linear_join(const LinearShape& d, const LinearJobs& jobs, bool tangent, hipStream_t st);
+hipError_t launch_linear_tangent(const LinearShape& d, const LinearJobs& jobs, hipStream_t st);
+// Sums per head that launch_linear_tangent leaves, and their total.
+int linear_dots(const LinearShape& d);
+hipError_t launch_linear_decay(const LinearShape& d, const double* dots, float* d_decay, hipStream_t st);
+// dst [b, s, kheads, r] = src [b, s, h, r] fp32 summed over the heads that share one.
+hipError_t launch_linear_share(const LinearShape& d, int kheads, int r, const float* src, void* dst, hipStream_t st);
+
+// One token from the states of a pool of nslots; slots (device, may be null) picks each row's.
+hipError_t launch_linear_step(const DeltaShape& d, int nslots, const void* q, const void* k, const void* v,
+                              const float* log_decay, float* state, const int32_t* slots, void* y, hipStream_t st);
+
 // ---------------------------------------------------------------- root-mean-square norm
 struct NormShape {
     int64_t rows;

@@ -35,7 +35,8 @@ EXPORTS = ("ssd_workspace_size", "ssd_fwd", "ssd_fwd_noalloc", "ssd_bwd", "ssd_s
            "ssd_state_moments_bwd", "ssd_moments_pr", "ssd_moments_pr_bwd", "ssd_y_diag",
            "ssd_y_diag_bwd", "ssd_quat_scan", "ssd_quat_scan_bwd", "ssd_quat_workspace_size",
            "ssd_step", "ssd_delta_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd",
-           "ssd_delta_step", "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size",
+           "ssd_delta_step", "ssd_linear_workspace_size", "ssd_linear_fwd", "ssd_linear_bwd",
+           "ssd_linear_step", "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size",
            "ssd_last_error", "ssd_debug_enable", "ssd_timing_enable",
            "ssd_timing_collect", "ssd_bwd_partial_region", "ssd_stream_probe")
 
@@ -101,10 +102,15 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_delta_fwd.argtypes = [E] + [P] * 10 + [SZ, P]
     lib.ssd_delta_bwd.argtypes = [E] + [P] * 16 + [SZ, P]
     lib.ssd_delta_step.argtypes = [E, I64] + [P] * 9
+    lib.ssd_linear_workspace_size.argtypes = [E, ctypes.c_int, ctypes.POINTER(SZ)]
+    lib.ssd_linear_fwd.argtypes = [E] + [P] * 9 + [SZ, P]
+    lib.ssd_linear_bwd.argtypes = [E] + [P] * 14 + [SZ, P]
+    lib.ssd_linear_step.argtypes = [E, I64] + [P] * 8
     lib.ssd_rms_norm.argtypes = [I64, I64, ctypes.c_int, F] + [P] * 3 + [I64] + [P] * 5
     lib.ssd_rms_norm_bwd.argtypes = [I64, I64, ctypes.c_int, F] + [P] * 7 + [SZ, P]
     lib.ssd_rms_norm_workspace_size.argtypes = [I64, I64, ctypes.POINTER(SZ)]
     for f in ("ssd_delta_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd", "ssd_delta_step",
+              "ssd_linear_workspace_size", "ssd_linear_fwd", "ssd_linear_bwd", "ssd_linear_step",
               "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("ssd_workspace_size", "ssd_fwd", "ssd_fwd_noalloc", "ssd_bwd", "ssd_state_moments",
@@ -534,18 +540,18 @@ def _delta_args(q, k, v, scale):
 
 
 @functools.lru_cache(maxsize=256)
-def _delta_bytes(b, s, hk, h, p, r, io, bwd):
+def _heads_bytes(entry, b, s, hk, h, p, r, io, bwd):
     d = ssd_delta_dims(b, s, hk, h, p, r, *[0] * 9, 1.0, io)
     n = ctypes.c_size_t(0)
-    rc = load_library().ssd_delta_workspace_size(ctypes.byref(d), bwd, ctypes.byref(n))
+    rc = getattr(load_library(), entry)(ctypes.byref(d), bwd, ctypes.byref(n))
     if rc:
-        raise SsdError(rc, "ssd_delta_workspace_size", ssd_last_error())
+        raise SsdError(rc, entry, ssd_last_error())
     return int(n.value)
 
 
 def ssd_delta_workspace_size(dims: ssd_delta_dims, bwd: bool) -> int:
-    return _delta_bytes(dims.batch, dims.seq, dims.kheads, dims.nheads, dims.headdim, dims.dstate,
-                        dims.io_dtype, int(bool(bwd)))
+    return _heads_bytes("ssd_delta_workspace_size", dims.batch, dims.seq, dims.kheads, dims.nheads,
+                        dims.headdim, dims.dstate, dims.io_dtype, int(bool(bwd)))
 
 
 def _delta_shapes(q, v):
@@ -585,24 +591,72 @@ def ssd_delta_bwd(dy, d_final, q, k, v, g, beta, init, valid_len, d_q, d_k, d_v,
                    _address(d_final, "d_final", f, state, at, False), *qkv, *args, wp, wb, _raw_stream(stream, at))
 
 
-def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -> int:
-    """q, k ``[b, hk, r]``, v ``[b, h, p]`` (last axis contiguous), g, beta ``[b, h]``, state
-    ``[nslots, h, p, r]`` updated in place, slots device int32 ``[b]`` or None, y like v."""
+def _step_args(q, k, v, state, slots, scale):
+    """_delta_args of one token, and what its pool of states and its slots have to be like."""
     if q.dim() != 3:
         raise ValueError("q and k must be [b, hk, r], v [b, h, p] and state [nslots, h, p, r]")
     d, qkv, at = _delta_args(q, k, v, scale)
-    f, io = torch.float32, q.dtype
     if state.dim() != 4 or state.shape[1:] != (*v.shape[1:], q.shape[2]):
         raise ValueError(f"state must be [nslots, {d.nheads}, {d.headdim}, {d.dstate}] (got {list(state.shape)})")
     if slots is not None and not (slots.dtype == torch.int32 and slots.get_device() == at
                                   and slots.is_contiguous() and slots.numel() == d.batch):
         raise ValueError(f"slots must be a contiguous int32 tensor of {d.batch} elements on q's device")
-    bh = v.shape[:2]
+    return d, qkv, at
+
+
+def ssd_delta_step(q, k, v, g, beta, state, slots, y, scale=None, stream=None) -> int:
+    """q, k ``[b, hk, r]``, v ``[b, h, p]`` (last axis contiguous), g, beta ``[b, h]``, state
+    ``[nslots, h, p, r]`` updated in place, slots device int32 ``[b]`` or None, y like v."""
+    d, qkv, at = _step_args(q, k, v, state, slots, scale)
+    f, io, bh = torch.float32, q.dtype, v.shape[:2]
     return _launch(
         load_library().ssd_delta_step, at, ctypes.byref(d), state.shape[0], *qkv,
         _address(g, "g", f, bh, at), _address(beta, "beta", f, bh, at), _address(state, "state", f, state.shape, at),
         None if slots is None else slots.data_ptr(),
         _address(y, "y", io, v.shape, at), _raw_stream(stream, at))
+
+
+def ssd_linear_workspace_size(dims: ssd_delta_dims, bwd: bool) -> int:
+    return _heads_bytes("ssd_linear_workspace_size", dims.batch, dims.seq, dims.kheads, dims.nheads,
+                        dims.headdim, dims.dstate, dims.io_dtype, int(bool(bwd)))
+
+
+def ssd_linear_fwd(q, k, v, log_decay, init, valid_len, y, final_state, ws, scale=None, stream=None) -> int:
+    """q, k ``[b, s, hk, r]``, v ``[b, s, h, p]`` (last axis contiguous), log_decay ``[h]``; scale None is
+    ``1 / sqrt(r)``."""
+    d, qkv, at = _delta_args(q, k, v, scale)
+    f, (_, state) = torch.float32, _delta_shapes(q, v)
+    args = (_address(log_decay, "log_decay", f, v.shape[-2:-1], at),
+            _address(init, "init", f, state, at, False), _host_lengths(valid_len, d.batch),
+            _address(y, "y", q.dtype, v.shape, at), _address(final_state, "final_state", f, state, at, False))
+    wp, wb = _workspace(ws, at)
+    return _launch(load_library().ssd_linear_fwd, at, ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream, at))
+
+
+def ssd_linear_bwd(dy, d_final, q, k, v, log_decay, init, valid_len, d_q, d_k, d_v, d_decay, d_init, ws,
+                   scale=None, stream=None) -> int:
+    d, qkv, at = _delta_args(q, k, v, scale)
+    f, (_, state), io, h = torch.float32, _delta_shapes(q, v), q.dtype, v.shape[-2:-1]
+    args = (_address(log_decay, "log_decay", f, h, at),
+            _address(init, "init", f, state, at, False), _host_lengths(valid_len, d.batch),
+            _address(d_q, "d_q", io, q.shape, at), _address(d_k, "d_k", io, q.shape, at),
+            _address(d_v, "d_v", io, v.shape, at), _address(d_decay, "d_decay", f, h, at, False),
+            _address(d_init, "d_init", f, state, at, False))
+    wp, wb = _workspace(ws, at)
+    return _launch(load_library().ssd_linear_bwd, at, ctypes.byref(d), _address(dy, "dy", io, v.shape, at),
+                   _address(d_final, "d_final", f, state, at, False), *qkv, *args, wp, wb, _raw_stream(stream, at))
+
+
+def ssd_linear_step(q, k, v, log_decay, state, slots, y, scale=None, stream=None) -> int:
+    """q, k ``[b, hk, r]``, v ``[b, h, p]`` (last axis contiguous), log_decay ``[h]``, state
+    ``[nslots, h, p, r]`` updated in place, slots device int32 ``[b]`` or None, y like v."""
+    d, qkv, at = _step_args(q, k, v, state, slots, scale)
+    f = torch.float32
+    return _launch(
+        load_library().ssd_linear_step, at, ctypes.byref(d), state.shape[0], *qkv,
+        _address(log_decay, "log_decay", f, v.shape[1:2], at), _address(state, "state", f, state.shape, at),
+        None if slots is None else slots.data_ptr(),
+        _address(y, "y", q.dtype, v.shape, at), _raw_stream(stream, at))
 
 
 def ssd_rms_norm(x, residual, weight, eps, group, s, y, y8, scale, stream=None) -> int:
@@ -865,6 +919,61 @@ def delta_step(q, k, v, g, beta, state, slots=None, scale=None, stream=None):
     with _allocating_on(stream, q):
         y = v.new_empty(v.shape)
         _check(ssd_delta_step(q, k, v, g, beta, state, slots, y, scale, stream), "ssd_delta_step")
+    return y
+
+
+def linear_workspace(q, k, v, bwd: bool) -> torch.Tensor:
+    """Workspace of linear_attention (bwd False) or linear_attention_bwd for tensors of these shapes."""
+    n = ssd_linear_workspace_size(_delta_args(q, k, v, None)[0], bwd)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def linear_attention(q, k, v, log_decay, init=None, valid_len=None, scale=None, want_final=True, ws=None,
+                     stream=None):
+    """Linear attention with a decay for each head over a sequence (see ssd_linear_fwd): returns
+    ``(y, final_state)``.
+
+    q, k ``[b, s, hk, r]`` and v ``[b, s, h, p]`` (fp32 or bf16; slices of one projection's output
+    are read in place), log_decay ``[h]`` fp32 (the same at every token), init ``[b, h, p, r]`` fp32 or
+    None, valid_len host int64 ``[b]`` (or a list) or None, scale None for ``1 / sqrt(r)``."""
+    if q.dim() != 4:
+        raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
+    with _allocating_on(stream, q):
+        y = v.new_empty(v.shape)
+        final = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), dtype=torch.float32,
+                            device=q.device) if want_final else None
+        ws = linear_workspace(q, k, v, False) if ws is None else ws
+        _check(ssd_linear_fwd(q, k, v, log_decay, init, _lengths(valid_len), y, final, ws, scale, stream),
+               "ssd_linear_fwd")
+    return y, final
+
+
+def linear_attention_bwd(dy, q, k, v, log_decay, init=None, d_final=None, valid_len=None, scale=None,
+                         want_d_init=True, want_d_decay=True, ws=None, stream=None):
+    """Gradients of ``<dy, y> + <d_final, final_state>`` of linear_attention, from its inputs: returns
+    dict(d_q, d_k, d_v, d_decay, d_init); d_decay, that of log_decay, None unless wanted (it takes a
+    scan of its own, which fixed decays save)."""
+    if q.dim() != 4:
+        raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
+    with _allocating_on(stream, q):
+        new = lambda t: t.new_empty(t.shape)  # noqa: E731
+        out = dict(d_q=new(q), d_k=new(k), d_v=new(v), d_decay=new(log_decay) if want_d_decay else None,
+                   d_init=torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]),
+                                      dtype=torch.float32, device=q.device) if want_d_init else None)
+        ws = linear_workspace(q, k, v, True) if ws is None else ws
+        _check(ssd_linear_bwd(dy, d_final, q, k, v, log_decay, init, _lengths(valid_len), out["d_q"],
+                              out["d_k"], out["d_v"], out["d_decay"], out["d_init"], ws, scale, stream),
+               "ssd_linear_bwd")
+    return out
+
+
+def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None, stream=None):
+    """One token of linear attention from cached states (see ssd_linear_step): q, k ``[b, hk, r]``,
+    v ``[b, h, p]``, log_decay ``[h]``; state ``[nslots, h, p, r]`` is updated in place; slots (device
+    int32 ``[b]``) names each row's slot, negative for an idle row.  Returns y ``[b, h, p]``."""
+    with _allocating_on(stream, q):
+        y = v.new_empty(v.shape)
+        _check(ssd_linear_step(q, k, v, log_decay, state, slots, y, scale, stream), "ssd_linear_step")
     return y
 
 
