@@ -488,6 +488,54 @@ int ssd_rms_norm_bwd(int64_t rows, int64_t width, int io_dtype, float eps, const
                      float* d_weight, void* ws, size_t ws_bytes, void* stream);
 int ssd_rms_norm_workspace_size(int64_t rows, int64_t width, size_t* bytes);
 
+/*
+ * Group norm over channels-last data, with an activation or a gate: mean and variance are those of all
+ * positions of a sample and of the channels of a group (channels / groups neighbours).
+ *   m = (x - mean) / sqrt(var + eps),   u = m weight + bias   (per channel),
+ *   y = u, or u sigmoid(u) (SSD_ACT_SILU), or with a gate u gate sigmoid(gate)
+ *   x, gate        [batch, positions, channels]  io dtype, strided by position (x_stride, gate_stride
+ *                  elements; a sample's positions follow the sample's before)
+ *   y, dy, d_x, d_gate   the same, contiguous    weight, bias, d_weight, d_bias  [channels] fp32
+ *   stats          [batch, groups, 2] fp32: mean and 1 / sqrt(var + eps)
+ * Tokens that are normalised each by itself are samples of one position (the heads of an attention's
+ * output as groups: batch = tokens, positions = 1, groups = heads, the gate a slice of the projection).
+ * batch >= 0, positions > 0, 0 < channels < 2^20, groups dividing channels, values of a group < 2^31,
+ * strides >= 0; batch * positions * (channels or the strides) < 2^60.  Base addresses 16-byte aligned;
+ * strides need no alignment, but the loads are as wide as channels / groups and the strides allow.
+ * weight (NULL = 1), bias (NULL = 0) and gate are nullable; act must be SSD_ACT_NONE with a gate.
+ * Sums are fp32 (variances about a value of the data, joined by the differences of the means) and y is
+ * rounded once.  No atomics: bitwise reproducible.  A NaN or an infinity stays in its sample's group
+ * (and, in d_weight and d_bias, its channels; d_x and y elsewhere are not touched).
+ * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,
+ * SSD_ERR_HIP.
+ */
+enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 };
+typedef struct ssd_group_norm_dims {
+    int64_t batch, positions, channels, groups;
+    int64_t x_stride, gate_stride; /* elements between positions */
+    float eps;
+    int32_t act;
+    int32_t io_dtype;
+} ssd_group_norm_dims;
+
+/* Workspace bytes (256-byte aligned buffer) of ssd_group_norm (bwd == 0) or ssd_group_norm_bwd; may be 0. */
+int ssd_group_norm_workspace_size(const ssd_group_norm_dims* dims, int bwd, size_t* bytes);
+
+/* y and stats are nullable, one of them is required (y NULL: gate, weight and bias are not read). */
+int ssd_group_norm(const ssd_group_norm_dims* dims, const void* x, const float* weight,
+                   const float* bias, const void* gate, void* y, float* stats, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of <dy, y> from x, gate and the forward's stats.  d_weight and d_bias are nullable (not
+ * computed) and summed over batch and positions; d_gate is required with a gate and must be NULL without
+ * one.  Outputs overlap no input.
+ */
+int ssd_group_norm_bwd(const ssd_group_norm_dims* dims, const void* dy, const void* x,
+                       const float* weight, const float* bias, const void* gate, const float* stats,
+                       void* d_x, float* d_weight, float* d_bias, void* d_gate, void* ws,
+                       size_t ws_bytes, void* stream);
+
 /* Message for the last nonzero status returned on this thread ("" if none). */
 const char* ssd_last_error(void);
 

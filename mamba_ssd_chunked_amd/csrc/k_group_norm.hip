@@ -1,0 +1,767 @@
+// Group norm over channels-last data with an activation or a gate.
+//
+// x [n, s, c], groups of c / groups neighbouring channels; mean and variance over the s positions and the
+// channels of a group, of each sample:
+//   m = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  u = m w + b,
+//   y = u, silu(u), or u silu(gate).
+// Gradient, with du the gradient of u and N the values of a group:
+//   d_b = sum du,  d_w = sum du m  (over samples and positions, per channel),
+//   d_x = rstd (w du - mean_N(w du) - m mean_N(w du m)),  d_gate = dy u silu'(gate).
+//
+// Where every position is a sample of its own (s = 1: tokens), a group's values lie side by side: a team
+// of 1 to 64 lanes holds one in registers, and x is read once.  Otherwise a thread has one vector of EV
+// channels for its whole life and walks down positions: one kernel leaves sums per block of positions,
+// the next joins them in its first lines and writes the outputs, reading x again.  Variances are summed
+// about a value of the thread's own data and joined with the differences of the means, so no square of a
+// mean is ever subtracted.  No atomics: sums are joined in a fixed order.
+// EV is the widest vector of 16 bytes or less that a group's channels divide into.
+#include <type_traits>
+
+#include "ssd_device.hpp"
+#include "ssd_launch.hpp"
+
+namespace ssd {
+
+namespace {
+
+template <class IO, int EV>
+__device__ __forceinline__ void ldv(const typename IO::T* p, float (&x)[EV]) {
+    typedef typename IO::T vec __attribute__((ext_vector_type(EV)));
+    if constexpr (sizeof(typename IO::T) == 4) {
+        const vec w = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+        for (int e = 0; e < EV; ++e) x[e] = w[e];
+    } else if constexpr (EV == 1) {
+        x[0] = bf16_to_f32(p[0]);
+    } else {
+        typedef uint32_t words __attribute__((ext_vector_type(EV / 2)));
+        const words w = *reinterpret_cast<const words*>(p);
+#pragma unroll
+        for (int e = 0; e < EV / 2; ++e) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+    }
+}
+template <class IO, int EV>
+__device__ __forceinline__ void stv(typename IO::T* p, const float (&x)[EV]) {
+    if constexpr (sizeof(typename IO::T) == 4) {
+        typedef float vec __attribute__((ext_vector_type(EV)));
+        vec w;
+#pragma unroll
+        for (int e = 0; e < EV; ++e) w[e] = x[e];
+        *reinterpret_cast<vec*>(p) = w;
+    } else if constexpr (EV == 1) {
+        p[0] = f32_to_bf16(x[0]);
+    } else {
+        typedef uint32_t words __attribute__((ext_vector_type(EV / 2)));
+        words w;
+#pragma unroll
+        for (int e = 0; e < EV / 2; ++e) w[e] = f32x2_to_bf16x2(x[2 * e], x[2 * e + 1]);
+        *reinterpret_cast<words*>(p) = w;
+    }
+}
+// weight or bias of EV channels, or `none` without one
+template <int EV>
+__device__ __forceinline__ void ld_chan(const float* p, int64_t at, float none, float (&x)[EV]) {
+#pragma unroll
+    for (int e = 0; e < EV; ++e) x[e] = none;
+    if (p) {
+        typedef float vec __attribute__((ext_vector_type(EV < 4 ? EV : 4)));
+        constexpr int W = EV < 4 ? EV : 4;
+#pragma unroll
+        for (int m = 0; m < EV; m += W) {
+            const vec w = *reinterpret_cast<const vec*>(p + at + m);
+#pragma unroll
+            for (int e = 0; e < W; ++e) x[m + e] = w[e];
+        }
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// The output for the normalised value m, and what its gradient needs.
+struct Act {
+    int act;
+    bool gated;
+    __device__ __forceinline__ float out(float u, float gate) const {
+        return gated ? u * (gate * sigmoid(gate)) : act ? u * sigmoid(u) : u;
+    }
+    // the gradient of u for the gradient dy of the output; dg: that of the gate
+    __device__ __forceinline__ float back(float dy, float u, float gate, float& dg) const {
+        if (!gated && !act) return dy;
+        const float z = gated ? gate : u, sg = sigmoid(z), rise = sg * (1.0f + z * (1.0f - sg));
+        dg = dy * u * rise;
+        return gated ? dy * (z * sg) : dy * rise;
+    }
+};
+
+template <int TS>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < TS; o <<= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// lanes of sums over LDS entries
+constexpr int SUB = 8;
+
+}  // namespace
+
+// ------------------------------------------------------------------ tokens: s = 1
+// Teams of TS lanes with NV vectors each, a group a team.
+template <class IO, int EV, int NV, int TS>
+__global__ __launch_bounds__(256) void k_group_norm_rows(GroupShape d, const typename IO::T* __restrict__ x,
+                                                         const float* __restrict__ weight,
+                                                         const float* __restrict__ bias,
+                                                         const typename IO::T* __restrict__ gate,
+                                                         typename IO::T* __restrict__ y, float* __restrict__ stats) {
+    constexpr int TEAMS = 256 / TS;
+    const Act act{d.act, gate != nullptr};
+    const int lane = threadIdx.x % TS;
+    const int64_t teams = d.n * d.groups;
+    for (int64_t team = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TS; team < teams;
+         team += static_cast<int64_t>(gridDim.x) * TEAMS) {
+        const int64_t row = team / d.groups;
+        const int ch = static_cast<int>(team % d.groups) * d.cg;
+        float v[NV][EV], w[NV][EV], b[NV][EV], z[NV][EV];
+        float sum = 0.0f;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int col = (lane + m * TS) * EV;
+#pragma unroll
+            for (int e = 0; e < EV; ++e) v[m][e] = 0.0f;
+            if (col < d.cg) {
+                ldv<IO, EV>(x + row * d.x_stride + ch + col, v[m]);
+                if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch + col, z[m]);
+                ld_chan<EV>(weight, ch + col, 1.0f, w[m]);
+                ld_chan<EV>(bias, ch + col, 0.0f, b[m]);
+            }
+#pragma unroll
+            for (int e = 0; e < EV; ++e) sum += v[m][e];
+        }
+        const float mean = team_sum<TS>(sum) * d.inv_count;
+        float sq = 0.0f;
+#pragma unroll
+        for (int m = 0; m < NV; ++m)
+            if ((lane + m * TS) * EV < d.cg) {
+#pragma unroll
+                for (int e = 0; e < EV; ++e) {
+                    v[m][e] -= mean;
+                    sq += v[m][e] * v[m][e];
+                }
+            }
+        const float rstd = 1.0f / sqrtf(team_sum<TS>(sq) * d.inv_count + d.eps);
+        if (stats && lane == 0) {
+            stats[2 * team] = mean;
+            stats[2 * team + 1] = rstd;
+        }
+        if (y) {
+#pragma unroll
+            for (int m = 0; m < NV; ++m) {
+                const int col = (lane + m * TS) * EV;
+                if (col < d.cg) {
+#pragma unroll
+                    for (int e = 0; e < EV; ++e)
+                        v[m][e] = act.out(v[m][e] * rstd * w[m][e] + b[m][e], gate ? z[m][e] : 0.0f);
+                    stv<IO, EV>(y + row * d.c + ch + col, v[m]);
+                }
+            }
+        }
+    }
+}
+
+// Team slot t of a workgroup keeps its group and walks down the rows; part [rows' parts, 2, c] holds what
+// each leaves of d_weight and d_bias.
+template <class IO, int EV, int NV, int TS>
+__global__ __launch_bounds__(256) void k_group_norm_rows_bwd(
+    GroupShape d, const typename IO::T* __restrict__ dy, const typename IO::T* __restrict__ x,
+    const float* __restrict__ weight, const float* __restrict__ bias, const typename IO::T* __restrict__ gate,
+    const float* __restrict__ stats, typename IO::T* __restrict__ d_x, typename IO::T* __restrict__ d_gate,
+    float* __restrict__ part) {
+    const Act act{d.act, gate != nullptr};
+    const int lane = threadIdx.x % TS, slot = threadIdx.x / TS;
+    const int slab = static_cast<int>(blockIdx.x % d.slabs), block = static_cast<int>(blockIdx.x / d.slabs);
+    const int g = slab * d.slab_groups + slot % d.slab_groups, rl = slot / d.slab_groups;
+    if (rl >= d.lanes || g >= d.groups) return;  // a whole team
+    const int64_t p = static_cast<int64_t>(block) * d.lanes + rl, parts = static_cast<int64_t>(d.blocks) * d.lanes;
+    const int ch = g * d.cg;
+    float w[NV][EV], b[NV][EV], dw[NV][EV], db[NV][EV];
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        const int col = (lane + m * TS) * EV;
+        if (col < d.cg) {
+            ld_chan<EV>(weight, ch + col, 1.0f, w[m]);
+            ld_chan<EV>(bias, ch + col, 0.0f, b[m]);
+        }
+#pragma unroll
+        for (int e = 0; e < EV; ++e) dw[m][e] = db[m][e] = 0.0f;
+    }
+    for (int64_t row = p; row < d.n; row += parts) {
+        const float mean = stats[2 * (row * d.groups + g)], rstd = stats[2 * (row * d.groups + g) + 1];
+        float v[NV][EV], du[NV][EV];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int col = (lane + m * TS) * EV;
+            if (col < d.cg) {
+                float z[EV], dg[EV];
+                ldv<IO, EV>(x + row * d.x_stride + ch + col, v[m]);
+                ldv<IO, EV>(dy + row * d.c + ch + col, du[m]);
+                if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch + col, z);
+#pragma unroll
+                for (int e = 0; e < EV; ++e) {
+                    v[m][e] = (v[m][e] - mean) * rstd;
+                    du[m][e] = act.back(du[m][e], v[m][e] * w[m][e] + b[m][e], gate ? z[e] : 0.0f, dg[e]);
+                    dw[m][e] += du[m][e] * v[m][e];
+                    db[m][e] += du[m][e];
+                    du[m][e] *= w[m][e];
+                    s1 += du[m][e];
+                    s2 += du[m][e] * v[m][e];
+                }
+                if (gate) stv<IO, EV>(d_gate + row * d.c + ch + col, dg);
+            }
+        }
+        s1 = team_sum<TS>(s1) * d.inv_count;
+        s2 = team_sum<TS>(s2) * d.inv_count;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int col = (lane + m * TS) * EV;
+            if (col < d.cg) {
+#pragma unroll
+                for (int e = 0; e < EV; ++e) v[m][e] = rstd * (du[m][e] - s1 - v[m][e] * s2);
+                stv<IO, EV>(d_x + row * d.c + ch + col, v[m]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        const int col = (lane + m * TS) * EV;
+        if (col < d.cg) {
+            stv<F32, EV < 4 ? EV : 4>(part + (2 * p) * d.c + ch + col, *reinterpret_cast<float(*)[EV < 4 ? EV : 4]>(dw[m]));
+            stv<F32, EV < 4 ? EV : 4>(part + (2 * p + 1) * d.c + ch + col,
+                                      *reinterpret_cast<float(*)[EV < 4 ? EV : 4]>(db[m]));
+            if constexpr (EV == 8) {
+                stv<F32, 4>(part + (2 * p) * d.c + ch + col + 4, *reinterpret_cast<float(*)[4]>(dw[m] + 4));
+                stv<F32, 4>(part + (2 * p + 1) * d.c + ch + col + 4, *reinterpret_cast<float(*)[4]>(db[m] + 4));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ positions: s > 1, or wide groups
+namespace {
+
+// A workgroup's piece: a block of the positions of one sample, and a slab of whole groups (or, of a group
+// wider than 256 vectors, all of it, 256 vectors at a time).  Thread t has the vector t % cv of the
+// slab's, and every lanes-th position from t / cv on.
+struct Piece {
+    int64_t n;
+    int block, g0, ng, col, rl, cv;
+    int64_t r0, r1;
+    bool on;
+    __device__ Piece(const GroupShape& d, int64_t item, int EV) {
+        const int slab = static_cast<int>(item % d.slabs);
+        block = static_cast<int>(item / d.slabs % d.blocks);
+        n = item / d.slabs / d.blocks;
+        g0 = slab * d.slab_groups;
+        ng = d.groups - g0 < d.slab_groups ? d.groups - g0 : d.slab_groups;
+        const int cgv = d.cg / EV;
+        cv = d.slab_groups * cgv < 256 ? d.slab_groups * cgv : 256;
+        col = threadIdx.x % cv;
+        rl = threadIdx.x / cv;
+        on = rl < d.lanes && (cgv > 256 || col < ng * cgv);
+        r0 = static_cast<int64_t>(block) * d.rows;
+        r1 = r0 + d.rows < d.s ? r0 + d.rows : d.s;
+    }
+};
+
+// Join (mean, M2) records of counts cnt(k), k < K, over SUB lanes, in a fixed order.
+template <class REC, class CNT>
+__device__ __forceinline__ void join_moments(int K, REC&& rec, CNT&& cnt, float total, float& mean, float& m2) {
+    const int l = threadIdx.x % SUB;
+    float s = 0.0f;
+    for (int k = l; k < K; k += SUB) s += cnt(k) * rec(k).x;
+    mean = team_sum<SUB>(s) / total;
+    s = 0.0f;
+    for (int k = l; k < K; k += SUB) {
+        const float2 r = rec(k);
+        const float off = r.x - mean;
+        s += r.y + cnt(k) * off * off;
+    }
+    m2 = team_sum<SUB>(s);
+}
+
+}  // namespace
+
+// Mean and sum of squared differences of every (sample, group, block of positions): rec [n, groups, blocks].
+template <class IO, int EV>
+__global__ __launch_bounds__(256) void k_group_norm_stats(GroupShape d, const typename IO::T* __restrict__ x,
+                                                          float2* __restrict__ rec) {
+    __shared__ float2 sh[256];
+    const int64_t items = d.n * d.blocks * d.slabs;
+    const int cgv = d.cg / EV;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Piece p(d, item, EV);
+        const typename IO::T* at = x + (p.n * d.s) * d.x_stride + static_cast<int64_t>(p.g0) * d.cg;
+        float mean = 0.0f, m2 = 0.0f;
+        const int64_t mine = p.on && p.r0 + p.rl < p.r1 ? (p.r1 - p.r0 - p.rl + d.lanes - 1) / d.lanes : 0;
+        float count = 0.0f;
+        if (mine > 0) {
+            float first[EV], s1 = 0.0f, s2 = 0.0f, shift = 0.0f;
+            ldv<IO, EV>(at + (p.r0 + p.rl) * d.x_stride + p.col * EV, first);
+#pragma unroll
+            for (int e = 0; e < EV; ++e) shift += first[e];
+            shift *= 1.0f / EV;
+            for (int col = p.col; col < (cgv > 256 ? cgv : p.col + 1); col += 256) {
+                const typename IO::T* c = at + col * EV;
+#pragma unroll 4
+                for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
+                    float v[EV];
+                    ldv<IO, EV>(c + r * d.x_stride, v);
+#pragma unroll
+                    for (int e = 0; e < EV; ++e) {
+                        const float o = v[e] - shift;
+                        s1 += o;
+                        s2 += o * o;
+                    }
+                }
+                count += static_cast<float>(mine * EV);
+            }
+            mean = shift + s1 / count;
+            m2 = fmaxf(s2 - s1 * (s1 / count), 0.0f);
+        }
+        __syncthreads();
+        sh[threadIdx.x] = make_float2(mean, m2);
+        __syncthreads();
+        const int per = cgv < 256 ? cgv : 256;  // threads of a group in a row lane
+        const float rows = static_cast<float>(p.r1 - p.r0);
+        for (int g = threadIdx.x / SUB; g < p.ng; g += 256 / SUB) {
+            auto row_lane = [&](int k) { return k / per; };
+            auto cnt = [&](int k) {
+                const int rl = row_lane(k), c = k % per;
+                const int64_t n = p.r0 + rl < p.r1 ? (p.r1 - p.r0 - rl + d.lanes - 1) / d.lanes : 0;
+                const int vecs = cgv > 256 ? (cgv - c + 255) / 256 : 1;
+                return static_cast<float>(n * vecs * EV);
+            };
+            auto r = [&](int k) { return sh[row_lane(k) * p.cv + g * per + k % per]; };
+            float mu, q;
+            join_moments(d.lanes * per, r, cnt, rows * static_cast<float>(d.cg), mu, q);
+            if (threadIdx.x % SUB == 0) rec[(p.n * d.groups + p.g0 + g) * d.blocks + p.block] = make_float2(mu, q);
+        }
+    }
+}
+
+// y from the records, and the statistics where they are wanted.
+template <class IO, int EV>
+__global__ __launch_bounds__(256) void k_group_norm_apply(GroupShape d, const typename IO::T* __restrict__ x,
+                                                          const float* __restrict__ weight,
+                                                          const float* __restrict__ bias,
+                                                          const typename IO::T* __restrict__ gate,
+                                                          const float2* __restrict__ rec,
+                                                          typename IO::T* __restrict__ y, float* __restrict__ stats) {
+    __shared__ float2 sh[256];
+    const Act act{d.act, gate != nullptr};
+    const int64_t items = d.n * (y ? d.blocks : 1) * d.slabs;
+    const int cgv = d.cg / EV;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        // without y one workgroup joins a slab's records
+        const Piece p(d, y ? item : item / d.slabs * d.blocks * d.slabs + item % d.slabs, EV);
+        __syncthreads();
+        for (int g = threadIdx.x / SUB; g < p.ng; g += 256 / SUB) {
+            const float2* from = rec + (p.n * d.groups + p.g0 + g) * d.blocks;
+            auto cnt = [&](int k) {
+                const int64_t r0 = static_cast<int64_t>(k) * d.rows;
+                return static_cast<float>((r0 + d.rows < d.s ? d.rows : d.s - r0) * d.cg);
+            };
+            float mu, q;
+            join_moments(d.blocks, [&](int k) { return from[k]; }, cnt, d.count, mu, q);
+            if (threadIdx.x % SUB == 0) {
+                const float2 st = make_float2(mu, 1.0f / sqrtf(q * d.inv_count + d.eps));
+                sh[g] = st;
+                if (stats && p.block == 0) reinterpret_cast<float2*>(stats)[p.n * d.groups + p.g0 + g] = st;
+            }
+        }
+        __syncthreads();
+        if (!p.on || !y) continue;
+        for (int col = p.col; col < (cgv > 256 ? cgv : p.col + 1); col += 256) {
+            const float2 st = sh[cgv > 256 ? 0 : col / cgv];
+            const int ch = p.g0 * d.cg + col * EV;
+            float w[EV], b[EV];
+            ld_chan<EV>(weight, ch, 1.0f, w);
+            ld_chan<EV>(bias, ch, 0.0f, b);
+#pragma unroll
+            for (int e = 0; e < EV; ++e) w[e] *= st.y;
+#pragma unroll 4
+            for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
+                const int64_t row = p.n * d.s + r;
+                float v[EV], z[EV];
+                ldv<IO, EV>(x + row * d.x_stride + ch, v);
+                if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
+#pragma unroll
+                for (int e = 0; e < EV; ++e) v[e] = act.out((v[e] - st.x) * w[e] + b[e], gate ? z[e] : 0.0f);
+                stv<IO, EV>(y + row * d.c + ch, v);
+            }
+        }
+    }
+}
+
+// Per channel, the sums of du and du m over a block of positions: part [n, blocks, 2, c].
+template <class IO, int EV>
+__global__ __launch_bounds__(256) void k_group_norm_sums(GroupShape d, const typename IO::T* __restrict__ dy,
+                                                         const typename IO::T* __restrict__ x,
+                                                         const float* __restrict__ weight,
+                                                         const float* __restrict__ bias,
+                                                         const typename IO::T* __restrict__ gate,
+                                                         const float* __restrict__ stats, float* __restrict__ part) {
+    __shared__ float sh[2 * EV][256];
+    const Act act{d.act, gate != nullptr};
+    const int64_t items = d.n * d.blocks * d.slabs;
+    const int cgv = d.cg / EV;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Piece p(d, item, EV);
+        for (int c0 = 0; c0 < (cgv > 256 ? cgv : 1); c0 += 256) {
+            const int col = c0 + p.col;
+            const bool on = p.on && (cgv <= 256 || col < cgv);
+            float s1[EV], s2[EV];
+#pragma unroll
+            for (int e = 0; e < EV; ++e) s1[e] = s2[e] = 0.0f;
+            const int ch = p.g0 * d.cg + col * EV;
+            if (on) {
+                const float2 st = reinterpret_cast<const float2*>(stats)[p.n * d.groups + p.g0 + (cgv > 256 ? 0 : col / cgv)];
+                float w[EV], b[EV];
+                ld_chan<EV>(weight, ch, 1.0f, w);
+                ld_chan<EV>(bias, ch, 0.0f, b);
+#pragma unroll 2
+                for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
+                    const int64_t row = p.n * d.s + r;
+                    float v[EV], g[EV], z[EV], dg;
+                    ldv<IO, EV>(x + row * d.x_stride + ch, v);
+                    ldv<IO, EV>(dy + row * d.c + ch, g);
+                    if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
+#pragma unroll
+                    for (int e = 0; e < EV; ++e) {
+                        const float m = (v[e] - st.x) * st.y;
+                        const float du = act.back(g[e], m * w[e] + b[e], gate ? z[e] : 0.0f, dg);
+                        s1[e] += du;
+                        s2[e] += du * m;
+                    }
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < EV; ++e) {
+                sh[e][threadIdx.x] = s1[e];
+                sh[EV + e][threadIdx.x] = s2[e];
+            }
+            __syncthreads();
+            for (int k = threadIdx.x; k < 2 * EV * p.cv; k += 256) {
+                const int e = k / p.cv, at = k % p.cv;
+                if (cgv > 256 ? c0 + at >= cgv : at >= p.ng * cgv) continue;
+                float sum = 0.0f;
+                for (int l = 0; l < d.lanes; ++l) sum += sh[e][l * p.cv + at];
+                part[((p.n * d.blocks + p.block) * 2 + e / EV) * d.c + p.g0 * d.cg + (c0 + at) * EV + e % EV] = sum;
+            }
+        }
+    }
+}
+
+// Joins the blocks of a (sample, group): chan [n, 2, c] = sums per channel, mean [n, groups] the means of
+// w du and w du m over the group.
+__global__ __launch_bounds__(256) void k_group_norm_means(GroupShape d, const float* __restrict__ part,
+                                                          const float* __restrict__ weight, float* __restrict__ chan,
+                                                          float2* __restrict__ mean) {
+    __shared__ float sh[2][256];
+    int cw = 1;  // channels at a time, as many lanes as are left for each
+    while (cw < d.cg && cw < 256) cw *= 2;
+    const int lanes = 256 / cw, lc = threadIdx.x % cw, bl = threadIdx.x / cw;
+    for (int64_t item = blockIdx.x; item < d.n * d.groups; item += gridDim.x) {
+        const int64_t n = item / d.groups;
+        const int g = static_cast<int>(item % d.groups);
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int c0 = 0; c0 < d.cg; c0 += cw) {
+            const int c = c0 + lc, ch = g * d.cg + c;
+            float a = 0.0f, b = 0.0f;
+            if (c < d.cg) {
+#pragma unroll 4
+                for (int k = bl; k < d.blocks; k += lanes) {
+                    a += part[((n * d.blocks + k) * 2) * d.c + ch];
+                    b += part[((n * d.blocks + k) * 2 + 1) * d.c + ch];
+                }
+            }
+            __syncthreads();
+            sh[0][threadIdx.x] = a;
+            sh[1][threadIdx.x] = b;
+            __syncthreads();
+            if (bl == 0 && c < d.cg) {
+                for (int l = 1; l < lanes; ++l) {
+                    a += sh[0][l * cw + lc];
+                    b += sh[1][l * cw + lc];
+                }
+                chan[(2 * n) * d.c + ch] = b;
+                chan[(2 * n + 1) * d.c + ch] = a;
+                const float w = weight ? weight[ch] : 1.0f;
+                s1 += w * a;
+                s2 += w * b;
+            }
+        }
+        s1 = team_sum<64>(s1);
+        s2 = team_sum<64>(s2);
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) {
+            sh[0][threadIdx.x >> 6] = s1;
+            sh[1][threadIdx.x >> 6] = s2;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0)
+            mean[item] = make_float2((sh[0][0] + sh[0][1] + sh[0][2] + sh[0][3]) * d.inv_count,
+                                     (sh[1][0] + sh[1][1] + sh[1][2] + sh[1][3]) * d.inv_count);
+    }
+}
+
+template <class IO, int EV>
+__global__ __launch_bounds__(256) void k_group_norm_grad(GroupShape d, const typename IO::T* __restrict__ dy,
+                                                         const typename IO::T* __restrict__ x,
+                                                         const float* __restrict__ weight,
+                                                         const float* __restrict__ bias,
+                                                         const typename IO::T* __restrict__ gate,
+                                                         const float* __restrict__ stats,
+                                                         const float2* __restrict__ mean,
+                                                         typename IO::T* __restrict__ d_x,
+                                                         typename IO::T* __restrict__ d_gate) {
+    const Act act{d.act, gate != nullptr};
+    const int64_t items = d.n * d.blocks * d.slabs;
+    const int cgv = d.cg / EV;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Piece p(d, item, EV);
+        if (!p.on) continue;
+        for (int col = p.col; col < (cgv > 256 ? cgv : p.col + 1); col += 256) {
+            const int64_t at = p.n * d.groups + p.g0 + (cgv > 256 ? 0 : col / cgv);
+            const float2 st = reinterpret_cast<const float2*>(stats)[at], mn = mean[at];
+            const int ch = p.g0 * d.cg + col * EV;
+            float w[EV], b[EV];
+            ld_chan<EV>(weight, ch, 1.0f, w);
+            ld_chan<EV>(bias, ch, 0.0f, b);
+#pragma unroll 2
+            for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
+                const int64_t row = p.n * d.s + r;
+                float v[EV], g[EV], z[EV], dg[EV];
+                ldv<IO, EV>(x + row * d.x_stride + ch, v);
+                ldv<IO, EV>(dy + row * d.c + ch, g);
+                if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
+#pragma unroll
+                for (int e = 0; e < EV; ++e) {
+                    const float m = (v[e] - st.x) * st.y;
+                    const float du = act.back(g[e], m * w[e] + b[e], gate ? z[e] : 0.0f, dg[e]);
+                    v[e] = st.y * (w[e] * du - mn.x - m * mn.y);
+                }
+                stv<IO, EV>(d_x + row * d.c + ch, v);
+                if (gate) stv<IO, EV>(d_gate + row * d.c + ch, dg);
+            }
+        }
+    }
+}
+
+// d_weight, d_bias [c] = sums over parts of part [parts, 2, c]: 32 columns x 32 interleaved runs of parts.
+__global__ __launch_bounds__(1024) void k_group_norm_weight(const float* __restrict__ part, int64_t parts, int c,
+                                                            float* __restrict__ d_weight, float* __restrict__ d_bias) {
+    __shared__ float sh[32][33];
+    const int l = threadIdx.x & 31, run = threadIdx.x >> 5;
+    const int col = static_cast<int>(blockIdx.x) * 32 + l;
+    float* to = blockIdx.y ? d_bias : d_weight;
+    if (!to) return;
+    float acc = 0.0f;
+    if (col < c) {
+#pragma unroll 8  // as many loads under way
+        for (int64_t t = run; t < parts; t += 32) acc += part[(2 * t + blockIdx.y) * c + col];
+    }
+    sh[run][l] = acc;
+    __syncthreads();
+    if (run == 0 && col < c) {
+        acc = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 32; ++m) acc += sh[m][l];
+        to[col] = acc;
+    }
+}
+
+namespace {
+
+constexpr int64_t kMaxGroups = 1 << 20;  // workgroups of a launch; more work goes round in it
+unsigned grid_of(int64_t items) { return static_cast<unsigned>(items < kMaxGroups ? items : kMaxGroups); }
+
+template <class IO, class F>
+hipError_t by_vector(const GroupShape& d, F&& f) {
+    if constexpr (sizeof(typename IO::T) == 2)
+        if (d.ev == 8) return f(std::integral_constant<int, 8>{});
+    if (d.ev == 4) return f(std::integral_constant<int, 4>{});
+    if (d.ev == 2) return f(std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 1>{});
+}
+// The smallest team whose lanes hold a vector each; 64 lanes with up to eight for wider groups.
+template <class F>
+hipError_t by_team(int cgv, F&& f) {
+    const std::integral_constant<int, 1> one;
+    if (cgv <= 1) return f(one, std::integral_constant<int, 1>{});
+    if (cgv <= 2) return f(one, std::integral_constant<int, 2>{});
+    if (cgv <= 4) return f(one, std::integral_constant<int, 4>{});
+    if (cgv <= 8) return f(one, std::integral_constant<int, 8>{});
+    if (cgv <= 16) return f(one, std::integral_constant<int, 16>{});
+    if (cgv <= 32) return f(one, std::integral_constant<int, 32>{});
+    const std::integral_constant<int, 64> wave;
+    if (cgv <= 64) return f(one, wave);
+    if (cgv <= 128) return f(std::integral_constant<int, 2>{}, wave);
+    if (cgv <= 256) return f(std::integral_constant<int, 4>{}, wave);
+    return f(std::integral_constant<int, 8>{}, wave);
+}
+int team_of(int cgv) {
+    int t = 1;
+    while (t < cgv && t < 64) t *= 2;
+    return t;
+}
+
+template <class F>
+hipError_t by_io(const GroupShape& d, F&& f) {
+    return d.io == 1 ? f(BF16{}) : f(F32{});
+}
+
+}  // namespace
+
+// Which way, and how the work is cut up.
+void group_norm_plan(GroupShape* d, bool bwd) {
+    const int V = d->io == 1 ? 8 : 4;
+    d->ev = V;
+    while (d->cg % d->ev || d->x_stride % d->ev || d->gate_stride % d->ev) d->ev /= 2;
+    const int cgv = d->cg / d->ev;
+    d->tokens = d->s == 1 && cgv <= 512;
+    if (d->tokens) {
+        if (!bwd) return;
+        const int teams = 256 / team_of(cgv);
+        d->slab_groups = d->groups < teams ? d->groups : teams;
+        d->lanes = teams / d->slab_groups;
+        d->slabs = (d->groups + d->slab_groups - 1) / d->slab_groups;
+        int64_t b = 2048 / d->slabs;
+        const int64_t most = (d->n + d->lanes - 1) / d->lanes;
+        if (b > 1024 / d->lanes) b = 1024 / d->lanes;
+        if (b > most) b = most;
+        d->blocks = static_cast<int>(b < 1 ? 1 : b);
+        return;
+    }
+    d->slab_groups = cgv >= 256 ? 1 : 256 / cgv;
+    if (d->slab_groups > d->groups) d->slab_groups = d->groups;
+    d->slabs = (d->groups + d->slab_groups - 1) / d->slab_groups;
+    const int cv = d->slab_groups * cgv < 256 ? d->slab_groups * cgv : 256;
+    d->lanes = 256 / cv;
+    int64_t b = 2048 / (d->n * d->slabs), most = (d->s + 4 * d->lanes - 1) / (4 * d->lanes);
+    if (b > 256) b = 256;
+    if (b > most) b = most;
+    if (b < 1) b = 1;
+    d->rows = (d->s + b - 1) / b;
+    d->blocks = static_cast<int>((d->s + d->rows - 1) / d->rows);
+}
+
+hipError_t launch_group_norm(const GroupShape& d, const void* x, const float* weight, const float* bias,
+                             const void* gate, void* y, float* stats, hipStream_t st) {
+    return by_io(d, [&](auto io_) {
+        using IO = decltype(io_);
+        using T = typename IO::T;
+        return by_vector<IO>(d, [&](auto ev) {
+            constexpr int EV = decltype(ev)::value;
+            return by_team(d.cg / EV, [&](auto nv, auto ts) {
+                constexpr int NV = decltype(nv)::value, TS = decltype(ts)::value;
+                const int64_t per = 256 / TS;
+                k_group_norm_rows<IO, EV, NV, TS><<<grid_of((d.n * d.groups + per - 1) / per), 256, 0, st>>>(
+                    d, static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate), static_cast<T*>(y), stats);
+                return hipGetLastError();
+            });
+        });
+    });
+}
+
+hipError_t launch_group_norm_stats(const GroupShape& d, const void* x, float* rec, hipStream_t st) {
+    return by_io(d, [&](auto io_) {
+        using IO = decltype(io_);
+        return by_vector<IO>(d, [&](auto ev) {
+            k_group_norm_stats<IO, decltype(ev)::value><<<grid_of(d.n * d.blocks * d.slabs), 256, 0, st>>>(
+                d, static_cast<const typename IO::T*>(x), reinterpret_cast<float2*>(rec));
+            return hipGetLastError();
+        });
+    });
+}
+
+hipError_t launch_group_norm_apply(const GroupShape& d, const void* x, const float* weight, const float* bias,
+                                   const void* gate, const float* rec, void* y, float* stats, hipStream_t st) {
+    return by_io(d, [&](auto io_) {
+        using IO = decltype(io_);
+        using T = typename IO::T;
+        return by_vector<IO>(d, [&](auto ev) {
+            k_group_norm_apply<IO, decltype(ev)::value><<<grid_of(d.n * (y ? d.blocks : 1) * d.slabs), 256, 0, st>>>(
+                d, static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
+                reinterpret_cast<const float2*>(rec), static_cast<T*>(y), stats);
+            return hipGetLastError();
+        });
+    });
+}
+
+hipError_t launch_group_norm_rows_bwd(const GroupShape& d, const void* dy, const void* x, const float* weight,
+                                      const float* bias, const void* gate, const float* stats, void* d_x,
+                                      void* d_gate, float* part, hipStream_t st) {
+    return by_io(d, [&](auto io_) {
+        using IO = decltype(io_);
+        using T = typename IO::T;
+        return by_vector<IO>(d, [&](auto ev) {
+            constexpr int EV = decltype(ev)::value;
+            return by_team(d.cg / EV, [&](auto nv, auto ts) {
+                constexpr int NV = decltype(nv)::value, TS = decltype(ts)::value;
+                k_group_norm_rows_bwd<IO, EV, NV, TS><<<static_cast<unsigned>(d.blocks * d.slabs), 256, 0, st>>>(
+                    d, static_cast<const T*>(dy), static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
+                    stats, static_cast<T*>(d_x), static_cast<T*>(d_gate), part);
+                return hipGetLastError();
+            });
+        });
+    });
+}
+
+hipError_t launch_group_norm_sums(const GroupShape& d, const void* dy, const void* x, const float* weight,
+                                  const float* bias, const void* gate, const float* stats, float* part,
+                                  hipStream_t st) {
+    return by_io(d, [&](auto io_) {
+        using IO = decltype(io_);
+        using T = typename IO::T;
+        return by_vector<IO>(d, [&](auto ev) {
+            k_group_norm_sums<IO, decltype(ev)::value><<<grid_of(d.n * d.blocks * d.slabs), 256, 0, st>>>(
+                d, static_cast<const T*>(dy), static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
+                stats, part);
+            return hipGetLastError();
+        });
+    });
+}
+
+hipError_t launch_group_norm_means(const GroupShape& d, const float* part, const float* weight, float* chan,
+                                   float* mean, hipStream_t st) {
+    k_group_norm_means<<<grid_of(d.n * d.groups), 256, 0, st>>>(d, part, weight, chan, reinterpret_cast<float2*>(mean));
+    return hipGetLastError();
+}
+
+hipError_t launch_group_norm_grad(const GroupShape& d, const void* dy, const void* x, const float* weight,
+                                  const float* bias, const void* gate, const float* stats, const float* mean,
+                                  void* d_x, void* d_gate, hipStream_t st) {
+    return by_io(d, [&](auto io_) {
+        using IO = decltype(io_);
+        using T = typename IO::T;
+        return by_vector<IO>(d, [&](auto ev) {
+            k_group_norm_grad<IO, decltype(ev)::value><<<grid_of(d.n * d.blocks * d.slabs), 256, 0, st>>>(
+                d, static_cast<const T*>(dy), static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
+                stats, reinterpret_cast<const float2*>(mean), static_cast<T*>(d_x), static_cast<T*>(d_gate));
+            return hipGetLastError();
+        });
+    });
+}
+
+hipError_t launch_group_norm_weight(const GroupShape& d, const float* part, int64_t parts, float* d_weight,
+                                    float* d_bias, hipStream_t st) {
+    k_group_norm_weight<<<dim3((d.c + 31) / 32, 2), 1024, 0, st>>>(part, parts, d.c, d_weight, d_bias);
+    return hipGetLastError();
+}
+
+}  // namespace ssd

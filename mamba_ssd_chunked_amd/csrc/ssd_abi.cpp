@@ -633,6 +633,68 @@ int check_aligned16(std::initializer_list<std::pair<const void*, const char*>> p
     return SSD_OK;
 }
 
+// ------------------------------------------------------------ group norm
+int validate_group_norm(const char* who, const ssd_group_norm_dims* n, ssd::GroupShape* d, bool bwd) {
+    if (!n) return fail(SSD_ERR_NULL, "%s: dims is NULL", who);
+    if (n->io_dtype != SSD_F32 && n->io_dtype != SSD_BF16)
+        return fail(SSD_ERR_DTYPE, "%s: io_dtype must be SSD_F32 (0) or SSD_BF16 (1) (got %d)", who, n->io_dtype);
+    if (n->act != SSD_ACT_NONE && n->act != SSD_ACT_SILU)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: act must be SSD_ACT_NONE (0) or SSD_ACT_SILU (1) (got %d)", who, n->act);
+    if (n->batch < 0 || n->positions <= 0 || n->channels <= 0 || n->groups <= 0 || n->channels % n->groups != 0 ||
+        n->x_stride < 0 || n->gate_stride < 0 || !(n->eps >= 0.0f))
+        return fail(SSD_ERR_SHAPE, "%s: need batch >= 0, positions, channels > 0, groups dividing channels, strides >= 0 "
+                    "and eps >= 0 (got %lld, %lld, %lld, %lld groups, strides %lld, %lld, %g)", who, (long long)n->batch,
+                    (long long)n->positions, (long long)n->channels, (long long)n->groups, (long long)n->x_stride,
+                    (long long)n->gate_stride, (double)n->eps);
+    const double cg = (double)(n->channels / n->groups);
+    const double rows = (double)n->batch * (double)n->positions;
+    const double wide = std::max({(double)n->channels, (double)n->x_stride, (double)n->gate_stride});
+    if (n->channels >= (1 << 20) || cg * (double)n->positions >= 2147483648.0 || rows * wide >= 1152921504606846976.0)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: channels must be below 2^20, the values of a group below 2^31 and the "
+                    "tensors below 2^60 elements", who);
+    *d = ssd::GroupShape{};
+    d->n = n->batch;
+    d->s = n->positions;
+    d->c = (int)n->channels;
+    d->groups = (int)n->groups;
+    d->cg = (int)cg;
+    d->x_stride = n->x_stride;
+    d->gate_stride = n->gate_stride;
+    d->io = n->io_dtype;
+    d->act = n->act;
+    d->eps = n->eps;
+    d->count = (float)(cg * (double)n->positions);
+    d->inv_count = (float)(1.0 / (cg * (double)n->positions));
+    if (d->n > 0) ssd::group_norm_plan(d, bwd);
+    return SSD_OK;
+}
+
+// Workspace of the group norm.  Forward: the records of the blocks of positions (none for tokens).
+// Backward: sums per part and channel; but for tokens also their totals per sample and the groups' means.
+struct GroupBufs {
+    float *part, *chan, *mean;
+};
+size_t group_norm_bytes(const ssd::GroupShape& d, bool bwd, void* ws, GroupBufs* f) {
+    size_t off = 0;
+    auto take = [&](size_t floats) {
+        char* at = static_cast<char*>(ws) + off;
+        off += round_up(4 * floats);
+        return reinterpret_cast<float*>(at);
+    };
+    if (d.n == 0) return 0;
+    const size_t n = static_cast<size_t>(d.n), c = static_cast<size_t>(d.c), g = static_cast<size_t>(d.groups);
+    if (!bwd) {
+        if (!d.tokens) f->part = take(2 * n * g * d.blocks);
+    } else if (d.tokens) {
+        f->part = take(2 * static_cast<size_t>(d.blocks) * d.lanes * c);
+    } else {
+        f->part = take(2 * n * d.blocks * c);
+        f->chan = take(2 * n * c);
+        f->mean = take(2 * n * g);
+    }
+    return off;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1522,6 +1584,83 @@ int ssd_rms_norm_bwd(int64_t rows, int64_t width, int io_dtype, float eps, const
     float* part = at<float>(ws, 0);
     SSD_HIP(ssd::launch_rms_norm_bwd(n, dy, s, d_s, weight, d_x, part, st), "k_rms_norm_bwd");
     SSD_HIP(ssd::launch_rms_norm_weight(n, part, d_weight, st), "k_rms_norm_weight");
+    return ok();
+}
+
+int ssd_group_norm_workspace_size(const ssd_group_norm_dims* dims, int bwd, size_t* bytes) {
+    ssd::GroupShape d;
+    if (int rc = validate_group_norm("ssd_group_norm_workspace_size", dims, &d, bwd != 0)) return rc;
+    if (!bytes) return fail(SSD_ERR_NULL, "ssd_group_norm_workspace_size: bytes is NULL");
+    GroupBufs f{};
+    *bytes = group_norm_bytes(d, bwd != 0, nullptr, &f);
+    return ok();
+}
+
+int ssd_group_norm(const ssd_group_norm_dims* dims, const void* x, const float* weight, const float* bias,
+                   const void* gate, void* y, float* stats, void* ws, size_t ws_bytes, void* stream) {
+    const char* who = "ssd_group_norm";
+    ssd::GroupShape d;
+    if (int rc = validate_group_norm(who, dims, &d, false)) return rc;
+    if (gate && d.act != SSD_ACT_NONE)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: with a gate, act must be SSD_ACT_NONE (0)", who);
+    if (d.n == 0) return ok();
+    if (!x || (!y && !stats)) return fail(SSD_ERR_NULL, "%s: x and one of y and stats are required", who);
+    if (int rc = check_aligned16({{x, "x"}, {weight, "weight"}, {bias, "bias"}, {gate, "gate"}, {y, "y"}, {stats, "stats"}}))
+        return rc;
+    if (!y) weight = bias = nullptr;
+    if (!y) gate = nullptr;
+    GroupBufs f{};
+    const size_t need = group_norm_bytes(d, false, ws, &f);
+    if (need > 0)
+        if (int rc = check_delta_ws(who, need, ws, ws_bytes)) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (d.tokens) {
+        SSD_HIP(ssd::launch_group_norm(d, x, weight, bias, gate, y, stats, st), "k_group_norm_rows");
+        return ok();
+    }
+    SSD_HIP(ssd::launch_group_norm_stats(d, x, f.part, st), "k_group_norm_stats");
+    SSD_HIP(ssd::launch_group_norm_apply(d, x, weight, bias, gate, f.part, y, stats, st), "k_group_norm_apply");
+    return ok();
+}
+
+int ssd_group_norm_bwd(const ssd_group_norm_dims* dims, const void* dy, const void* x, const float* weight,
+                       const float* bias, const void* gate, const float* stats, void* d_x, float* d_weight,
+                       float* d_bias, void* d_gate, void* ws, size_t ws_bytes, void* stream) {
+    const char* who = "ssd_group_norm_bwd";
+    ssd::GroupShape d;
+    if (int rc = validate_group_norm(who, dims, &d, true)) return rc;
+    if (gate && d.act != SSD_ACT_NONE)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: with a gate, act must be SSD_ACT_NONE (0)", who);
+    if (d.n > 0 && (!dy || !x || !stats || !d_x))
+        return fail(SSD_ERR_NULL, "%s: dy, x, stats and d_x are required", who);
+    if (d.n > 0 && !gate != !d_gate) return fail(SSD_ERR_NULL, "%s: gate and d_gate come together or not at all", who);
+    if (int rc = check_aligned16({{dy, "dy"}, {x, "x"}, {weight, "weight"}, {bias, "bias"}, {gate, "gate"},
+                                  {stats, "stats"}, {d_x, "d_x"}, {d_weight, "d_weight"}, {d_bias, "d_bias"},
+                                  {d_gate, "d_gate"}}))
+        return rc;
+    GroupBufs f{};
+    const size_t need = group_norm_bytes(d, true, ws, &f);
+    if (need > 0)
+        if (int rc = check_delta_ws(who, need, ws, ws_bytes)) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (d.n == 0) {
+        if (d_weight) SSD_HIP(ssd::launch_copy_or_zero(d_weight, nullptr, d.c, st), "zero d_weight");
+        if (d_bias) SSD_HIP(ssd::launch_copy_or_zero(d_bias, nullptr, d.c, st), "zero d_bias");
+        return ok();
+    }
+    const float* sums = d.tokens ? f.part : f.chan;
+    const int64_t parts = d.tokens ? static_cast<int64_t>(d.blocks) * d.lanes : d.n;
+    if (d.tokens) {
+        SSD_HIP(ssd::launch_group_norm_rows_bwd(d, dy, x, weight, bias, gate, stats, d_x, d_gate, f.part, st),
+                "k_group_norm_rows_bwd");
+    } else {
+        SSD_HIP(ssd::launch_group_norm_sums(d, dy, x, weight, bias, gate, stats, f.part, st), "k_group_norm_sums");
+        SSD_HIP(ssd::launch_group_norm_means(d, f.part, weight, f.chan, f.mean, st), "k_group_norm_means");
+        SSD_HIP(ssd::launch_group_norm_grad(d, dy, x, weight, bias, gate, stats, f.mean, d_x, d_gate, st),
+                "k_group_norm_grad");
+    }
+    if (d_weight || d_bias)
+        SSD_HIP(ssd::launch_group_norm_weight(d, sums, parts, d_weight, d_bias, st), "k_group_norm_weight");
     return ok();
 }
 

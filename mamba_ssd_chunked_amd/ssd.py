@@ -37,7 +37,7 @@ EXPORTS = ("ssd_workspace_size", "ssd_fwd", "ssd_fwd_noalloc", "ssd_bwd", "ssd_s
            "ssd_step", "ssd_delta_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd",
            "ssd_delta_step", "ssd_linear_workspace_size", "ssd_linear_fwd", "ssd_linear_bwd",
            "ssd_linear_step", "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size",
-           "ssd_last_error", "ssd_debug_enable", "ssd_timing_enable",
+           "ssd_group_norm_workspace_size", "ssd_group_norm", "ssd_group_norm_bwd", "ssd_last_error", "ssd_debug_enable", "ssd_timing_enable",
            "ssd_timing_collect", "ssd_bwd_partial_region", "ssd_stream_probe")
 
 
@@ -59,6 +59,12 @@ class ssd_delta_dims(ctypes.Structure):
                 *[(f"{t}_stride_{axis}", ctypes.c_int64) for t in "qkv"
                   for axis in ("batch", "token", "head")],
                 ("scale", ctypes.c_float), ("io_dtype", ctypes.c_int32)]
+
+
+class ssd_group_norm_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("positions", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("act", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
 
 
 class SsdError(RuntimeError):
@@ -109,9 +115,14 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_rms_norm.argtypes = [I64, I64, ctypes.c_int, F] + [P] * 3 + [I64] + [P] * 5
     lib.ssd_rms_norm_bwd.argtypes = [I64, I64, ctypes.c_int, F] + [P] * 7 + [SZ, P]
     lib.ssd_rms_norm_workspace_size.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+    M = ctypes.POINTER(ssd_group_norm_dims)
+    lib.ssd_group_norm_workspace_size.argtypes = [M, ctypes.c_int, ctypes.POINTER(SZ)]
+    lib.ssd_group_norm.argtypes = [M] + [P] * 7 + [SZ, P]
+    lib.ssd_group_norm_bwd.argtypes = [M] + [P] * 11 + [SZ, P]
     for f in ("ssd_delta_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd", "ssd_delta_step",
               "ssd_linear_workspace_size", "ssd_linear_fwd", "ssd_linear_bwd", "ssd_linear_step",
-              "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size"):
+              "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size",
+              "ssd_group_norm_workspace_size", "ssd_group_norm", "ssd_group_norm_bwd"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("ssd_workspace_size", "ssd_fwd", "ssd_fwd_noalloc", "ssd_bwd", "ssd_state_moments",
               "ssd_state_moments_bwd", "ssd_moments_pr", "ssd_moments_pr_bwd", "ssd_y_diag",
@@ -693,6 +704,92 @@ def ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream=None) ->
         _raw_stream(stream, at))
 
 
+_ACT = {"none": 0, "silu": 1}
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, at: int):
+    """(address, elements between positions) of a tensor ``[..., channels]`` whose channels are contiguous
+    and whose positions are evenly spaced."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    if t.get_device() != at:
+        raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on device {at}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    step, count = None, 1
+    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1:
+            step = st if step is None else step
+            if st != step * count:
+                raise ValueError(f"{name} must have evenly spaced positions (strides {list(t.stride())})")
+            count *= n
+    if t.stride()[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return t.data_ptr(), shape[-1] if step is None else step
+
+
+def _group_norm_args(x, groups, eps, act, gate):
+    """(dims, addresses of x and gate, x's device) for x ``[n, ..., channels]``."""
+    if x.dim() < 2:
+        raise ValueError("x must be [n, ..., channels]")
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
+    tag, at = _io_of(x, "x"), _device_of(x, "x")
+    px, sx = _rows(x, "x", x.dtype, x.shape, at)
+    pg, sg = (None, 0) if gate is None else _rows(gate, "gate", x.dtype, x.shape, at)
+    n, *positions, c = x.shape
+    return ssd_group_norm_dims(n, math.prod(positions), c, groups, sx, sg, eps, _ACT[act], tag), px, pg, at
+
+
+@functools.lru_cache(maxsize=256)
+def _group_norm_bytes(*args):
+    *fields, bwd = args
+    n = ctypes.c_size_t(0)
+    rc = load_library().ssd_group_norm_workspace_size(ctypes.byref(ssd_group_norm_dims(*fields)), bwd,
+                                                      ctypes.byref(n))
+    if rc:
+        raise SsdError(rc, "ssd_group_norm_workspace_size", ssd_last_error())
+    return int(n.value)
+
+
+def ssd_group_norm_workspace_size(dims: ssd_group_norm_dims, bwd: bool) -> int:
+    return _group_norm_bytes(dims.batch, dims.positions, dims.channels, dims.groups, dims.x_stride,
+                             dims.gate_stride, dims.eps, dims.act, dims.io_dtype, int(bool(bwd)))
+
+
+def _group_stats(x, groups):
+    return x.shape[0], groups, 2
+
+
+def ssd_group_norm(x, groups, weight, bias, eps, act, gate, y, stats, ws, stream=None) -> int:
+    """x, gate ``[n, ..., channels]`` (positions evenly spaced), y like x (contiguous), weight, bias fp32
+    ``[channels]`` or None, stats fp32 ``[n, groups, 2]``; act "none" or "silu"."""
+    d, px, pg, at = _group_norm_args(x, groups, eps, act, gate)
+    f, c = torch.float32, x.shape[-1:]
+    args = (px, _address(weight, "weight", f, c, at, False), _address(bias, "bias", f, c, at, False), pg,
+            _address(y, "y", x.dtype, x.shape, at, False),
+            _address(stats, "stats", f, _group_stats(x, groups), at, False))
+    wp, wb = _workspace(ws, at)
+    return _launch(load_library().ssd_group_norm, at, ctypes.byref(d), *args, wp, wb, _raw_stream(stream, at))
+
+
+def ssd_group_norm_bwd(dy, x, groups, weight, bias, eps, act, gate, stats, d_x, d_weight, d_bias, d_gate, ws,
+                       stream=None) -> int:
+    d, px, pg, at = _group_norm_args(x, groups, eps, act, gate)
+    f, c, io = torch.float32, x.shape[-1:], x.dtype
+    args = (_address(dy, "dy", io, x.shape, at), px, _address(weight, "weight", f, c, at, False),
+            _address(bias, "bias", f, c, at, False), pg,
+            _address(stats, "stats", f, _group_stats(x, groups), at), _address(d_x, "d_x", io, x.shape, at),
+            _address(d_weight, "d_weight", f, c, at, False), _address(d_bias, "d_bias", f, c, at, False),
+            _address(d_gate, "d_gate", io, x.shape, at, False))
+    wp, wb = _workspace(ws, at)
+    return _launch(load_library().ssd_group_norm_bwd, at, ctypes.byref(d), *args, wp, wb, _raw_stream(stream, at))
+
+
 # ------------------------------------------------------------ allocating helpers
 _AS_IT_IS = contextlib.nullcontext()
 
@@ -1016,3 +1113,43 @@ def rms_norm_bwd(dy, s, weight, eps=1e-6, d_s=None, ws=None, stream=None):
             ws = torch.empty(max(n, 256), dtype=torch.uint8, device=s.device)
         _check(ssd_rms_norm_bwd(dy, s, d_s, weight, eps, d_x, d_weight, ws, stream), "ssd_rms_norm_bwd")
     return d_x, d_weight
+
+
+def group_norm_workspace(x, groups, gate=None, bwd=False) -> torch.Tensor:
+    """Workspace of group_norm (bwd False) or group_norm_bwd for tensors of these shapes."""
+    n = ssd_group_norm_workspace_size(_group_norm_args(x, groups, 0.0, "none", gate)[0], bwd)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
+
+
+def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act="none", gate=None, want_y=True,
+               want_stats=False, ws=None, stream=None):
+    """Group norm of x ``[n, ..., channels]`` (fp32 or bf16; see ssd_group_norm): each sample's positions and
+    the channels of a group are normalised together, so tokens ``[n, channels]`` each by itself.  act
+    "silu" is taken of the result; a gate like x multiplies it by its SiLU instead.  x and gate may be
+    slices of wider rows.  Returns a dict of ``y`` (like x, contiguous) and, where wanted, ``stats`` (fp32
+    ``[n, groups, 2]``, the mean and 1 / sqrt(var + eps)), which group_norm_bwd takes."""
+    with _allocating_on(stream, x):
+        y = x.new_empty(x.shape) if want_y else None
+        stats = torch.empty(_group_stats(x, groups), dtype=torch.float32, device=x.device) if want_stats else None
+        ws = group_norm_workspace(x, groups, gate) if ws is None else ws
+        _check(ssd_group_norm(x, groups, weight, bias, eps, act, gate, y, stats, ws, stream), "ssd_group_norm")
+    return {k: t for k, t in (("y", y), ("stats", stats)) if t is not None}
+
+
+def group_norm_bwd(dy, x, groups, weight=None, bias=None, eps=1e-5, act="none", gate=None, stats=None,
+                   want_weights=True, ws=None, stream=None):
+    """Gradient of ``<dy, y>`` of group_norm: returns dict(d_x, d_weight, d_bias, d_gate), d_weight and
+    d_bias None unless wanted, d_gate None without a gate.  stats as group_norm left them (None: taken of x
+    again)."""
+    with _allocating_on(stream, x):
+        if stats is None:
+            stats = group_norm(x, groups, eps=eps, want_y=False, want_stats=True, stream=stream)["stats"]
+        c = x.shape[-1:]
+        d_weight, d_bias = (torch.empty(c, dtype=torch.float32, device=x.device) if want_weights else None
+                            for _ in range(2))
+        out = dict(d_x=x.new_empty(x.shape), d_weight=d_weight, d_bias=d_bias,
+                   d_gate=None if gate is None else x.new_empty(x.shape))
+        ws = group_norm_workspace(x, groups, gate, True) if ws is None else ws
+        _check(ssd_group_norm_bwd(dy, x, groups, weight, bias, eps, act, gate, stats, out["d_x"], d_weight, d_bias,
+                                  out["d_gate"], ws, stream), "ssd_group_norm_bwd")
+    return out

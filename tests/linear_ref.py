@@ -99,3 +99,65 @@ def linear_inputs(b, s, hk, h, p, r, seed, dtype=torch.float32, init=True, slowe
                 log_decay=-torch.exp2(slowest * torch.rand(h, generator=gen)),
                 init=rn(b, h, p, r) if init else None, dy=rn(b, s, h, p).to(dtype),
                 d_final=rn(b, h, p, r) if init else None)
+
+
+# ------------------------------------------------------------------------------------ group norm
+def _grouped(t, groups):
+    """[n, ..., c] -> [n, positions, groups, c / groups]"""
+    return t.reshape(t.shape[0], -1, groups, t.shape[-1] // groups)
+
+
+def _channels(t, groups, none, like):
+    return (torch.full_like(like[0, 0], none) if t is None else t.detach().double().cpu().reshape(groups, -1))
+
+
+def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act="none", gate=None):
+    """(y, stats [n, groups, 2])"""
+    shape, (x, gate) = x.shape, _f64(x, gate)
+    x = _grouped(x, groups)
+    w, b = _channels(weight, groups, 1.0, x), _channels(bias, groups, 0.0, x)
+    mean = x.mean((1, 3), keepdim=True)
+    rstd = ((x - mean).square().mean((1, 3), keepdim=True) + eps).rsqrt()
+    u = (x - mean) * rstd * w + b
+    if gate is not None:
+        u = u * torch.nn.functional.silu(_grouped(gate, groups))
+    elif act == "silu":
+        u = torch.nn.functional.silu(u)
+    return u.reshape(shape), torch.stack([mean.reshape(-1, groups), rstd.reshape(-1, groups)], -1)
+
+
+def group_norm_bwd(dy, x, groups, weight=None, bias=None, eps=1e-5, act="none", gate=None):
+    """The formula's gradient (not autograd's)."""
+    shape = x.shape
+    _, stats = group_norm(x, groups, weight, bias, eps)
+    dy, x, gate = _f64(dy, x, gate)
+    dy, x = _grouped(dy, groups), _grouped(x, groups)
+    w, b = _channels(weight, groups, 1.0, x), _channels(bias, groups, 0.0, x)
+    rstd = stats[:, None, :, 1:]
+    m = (x - stats[:, None, :, :1]) * rstd
+    u, out, du = m * w + b, {}, dy
+    if gate is not None or act == "silu":
+        z = _grouped(gate, groups) if gate is not None else u
+        sg = torch.sigmoid(z)
+        rise = sg * (1 + z * (1 - sg))
+        du = dy * (z * sg if gate is not None else rise)
+        if gate is not None:
+            out["d_gate"] = (dy * u * rise).reshape(shape)
+    out["d_weight"], out["d_bias"] = (du * m).sum((0, 1)).flatten(), du.sum((0, 1)).flatten()
+    dm = du * w
+    d_x = rstd * (dm - dm.mean((1, 3), keepdim=True) - m * (dm * m).mean((1, 3), keepdim=True))
+    return out | {"d_x": d_x.reshape(shape)}
+
+
+def group_norm_inputs(shape, seed, dtype=torch.float32, gate=False):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *sh: torch.randn(*sh, generator=gen)  # noqa: E731
+    c = shape[-1]
+    return dict(x=(rn(*shape) * (0.5 + rn(c).abs()) + rn(c)).to(dtype), weight=1 + 0.3 * rn(c), bias=0.3 * rn(c),
+                gate=rn(*shape).to(dtype) if gate else None, dy=rn(*shape).to(dtype))
+
+
+def rel(a, b):
+    a, b = a.detach().double().cpu().reshape(-1), b.detach().double().cpu().reshape(-1)
+    n = b.norm().item()
+    return float("inf") if not torch.isfinite(a).all() else (a - b).norm().item() / (n if n > 0 else 1.0)
