@@ -78,7 +78,17 @@ __device__ __forceinline__ void ld_chan(const float* p, int64_t at, float none, 
     }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// 1 / (1 + e^-x) from the hardware's base-2 exponential and reciprocal, about 1 ulp each.  The product
+// with log2 e is carried to twice 24 bits: rounded once, it would cost |x| half steps of e^-x.  (With expf
+// and a full division the outputs, not their bytes, bounded the kernels: 4 x 16384 positions x 512
+// channels bf16 53 us.)
+__device__ __forceinline__ float sigmoid(float x) {
+    constexpr float kHi = -1.44269502162933349609375f, kLo = -1.92596303e-8f;  // -log2 e
+    const float t = x * kHi, lo = fmaf(x, kHi, -t) + x * kLo;
+    const float e = __builtin_amdgcn_exp2f(t);
+    // 2^lo - 1 = lo ln 2 to first order, |lo| < 2^-16; an infinite e stays infinite
+    return __builtin_amdgcn_rcpf(1.0f + fmaf(e, lo * 0.693147182f, e));
+}
 
 // The output for the normalised value m, and what its gradient needs.
 struct Act {
@@ -103,8 +113,7 @@ __device__ __forceinline__ float team_sum(float v) {
     return v;
 }
 
-// lanes of sums over LDS entries
-constexpr int SUB = 8;
+constexpr int MAXREC = 128;  // records of a group at most (cuts alone reach it)
 
 }  // namespace
 
@@ -181,10 +190,10 @@ __global__ __launch_bounds__(256) void k_group_norm_rows_bwd(
     float* __restrict__ part) {
     const Act act{d.act, gate != nullptr};
     const int lane = threadIdx.x % TS, slot = threadIdx.x / TS;
-    const int slab = static_cast<int>(blockIdx.x % d.slabs), block = static_cast<int>(blockIdx.x / d.slabs);
-    const int g = slab * d.slab_groups + slot % d.slab_groups, rl = slot / d.slab_groups;
-    if (rl >= d.lanes || g >= d.groups) return;  // a whole team
-    const int64_t p = static_cast<int64_t>(block) * d.lanes + rl, parts = static_cast<int64_t>(d.blocks) * d.lanes;
+    const int slab = static_cast<int>(blockIdx.x % d.sums.slabs), block = static_cast<int>(blockIdx.x / d.sums.slabs);
+    const int g = slab * d.sums.slab_groups + slot % d.sums.slab_groups, rl = slot / d.sums.slab_groups;
+    if (rl >= d.sums.lanes || g >= d.groups) return;  // a whole team
+    const int64_t p = static_cast<int64_t>(block) * d.sums.lanes + rl, parts = static_cast<int64_t>(d.sums.blocks) * d.sums.lanes;
     const int ch = g * d.cg;
     float w[NV][EV], b[NV][EV], dw[NV][EV], db[NV][EV];
 #pragma unroll
@@ -252,157 +261,233 @@ __global__ __launch_bounds__(256) void k_group_norm_rows_bwd(
 // ------------------------------------------------------------------ positions: s > 1, or wide groups
 namespace {
 
-// A workgroup's piece: a block of the positions of one sample, and a slab of whole groups (or, of a group
-// wider than 256 vectors, all of it, 256 vectors at a time).  Thread t has the vector t % cv of the
-// slab's, and every lanes-th position from t / cv on.
+// A workgroup's piece: a block of the positions of one sample, and a slab of channels: whole groups, or
+// one of the `cuts` parts of a group wider than 256 vectors.  Thread t has the vector t % cv of the
+// slab's, and every lanes-th position from t / cv on.  A vector may reach over groups.
+template <int EV>
 struct Piece {
-    int64_t n;
-    int block, g0, ng, col, rl, cv;
-    int64_t r0, r1;
+    int64_t n, r0, r1;
+    int block, g0, ng, cut, ch0, nch, cv, col, rl, lanes;
     bool on;
-    __device__ Piece(const GroupShape& d, int64_t item, int EV) {
-        const int slab = static_cast<int>(item % d.slabs);
-        block = static_cast<int>(item / d.slabs % d.blocks);
-        n = item / d.slabs / d.blocks;
-        g0 = slab * d.slab_groups;
-        ng = d.groups - g0 < d.slab_groups ? d.groups - g0 : d.slab_groups;
-        const int cgv = d.cg / EV;
-        cv = d.slab_groups * cgv < 256 ? d.slab_groups * cgv : 256;
+    __device__ Piece(const GroupShape& d, const GroupCut& c, int64_t item) {
+        const int slab = static_cast<int>(item % c.slabs);
+        block = static_cast<int>(item / c.slabs % c.blocks);
+        n = item / c.slabs / c.blocks;
+        lanes = c.lanes;
+        if (c.cuts == 1) {
+            cut = 0;
+            g0 = slab * c.slab_groups;
+            ng = d.groups - g0 < c.slab_groups ? d.groups - g0 : c.slab_groups;
+            ch0 = g0 * d.cg;
+            nch = ng * d.cg;
+            cv = c.slab_groups * d.cg / EV;
+        } else {
+            cut = slab % c.cuts;
+            g0 = slab / c.cuts;
+            ng = 1;
+            ch0 = g0 * d.cg + cut * 256 * EV;
+            nch = d.cg - cut * 256 * EV < 256 * EV ? d.cg - cut * 256 * EV : 256 * EV;
+            cv = 256;
+        }
         col = threadIdx.x % cv;
         rl = threadIdx.x / cv;
-        on = rl < d.lanes && (cgv > 256 || col < ng * cgv);
-        r0 = static_cast<int64_t>(block) * d.rows;
-        r1 = r0 + d.rows < d.s ? r0 + d.rows : d.s;
+        on = rl < lanes && col * EV < nch;
+        r0 = static_cast<int64_t>(block) * c.rows;
+        r1 = r0 + c.rows < d.s ? r0 + c.rows : d.s;
     }
+    __device__ int channel() const { return ch0 + col * EV; }
 };
 
-// Join (mean, M2) records of counts cnt(k), k < K, over SUB lanes, in a fixed order.
-template <class REC, class CNT>
-__device__ __forceinline__ void join_moments(int K, REC&& rec, CNT&& cnt, float total, float& mean, float& m2) {
-    const int l = threadIdx.x % SUB;
-    float s = 0.0f;
-    for (int k = l; k < K; k += SUB) s += cnt(k) * rec(k).x;
-    mean = team_sum<SUB>(s) / total;
-    s = 0.0f;
-    for (int k = l; k < K; k += SUB) {
-        const float2 r = rec(k);
-        const float off = r.x - mean;
-        s += r.y + cnt(k) * off * off;
-    }
-    m2 = team_sum<SUB>(s);
+// Positions that row lane rl of `lanes` has of those in [r0, r1).
+__device__ __forceinline__ int64_t lane_rows(int64_t r0, int64_t r1, int rl, int lanes) {
+    return r0 + rl < r1 ? (r1 - r0 - rl + lanes - 1) / lanes : 0;
 }
 
 }  // namespace
 
-// Mean and sum of squared differences of every (sample, group, block of positions): rec [n, groups, blocks].
-template <class IO, int EV>
-__global__ __launch_bounds__(256) void k_group_norm_stats(GroupShape d, const typename IO::T* __restrict__ x,
-                                                          float2* __restrict__ rec) {
-    __shared__ float2 sh[256];
-    const int64_t items = d.n * d.blocks * d.slabs;
-    const int cgv = d.cg / EV;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const Piece p(d, item, EV);
-        const typename IO::T* at = x + (p.n * d.s) * d.x_stride + static_cast<int64_t>(p.g0) * d.cg;
-        float mean = 0.0f, m2 = 0.0f;
-        const int64_t mine = p.on && p.r0 + p.rl < p.r1 ? (p.r1 - p.r0 - p.rl + d.lanes - 1) / d.lanes : 0;
-        float count = 0.0f;
-        if (mine > 0) {
-            float first[EV], s1 = 0.0f, s2 = 0.0f, shift = 0.0f;
-            ldv<IO, EV>(at + (p.r0 + p.rl) * d.x_stride + p.col * EV, first);
+namespace {
+
+// Mean and sum of squared differences of a piece's groups over its positions: f(group of the slab, mean,
+// squares) in one lane.  sh: free again after the next barrier.
+template <class IO, int EV, class F>
+__device__ __forceinline__ void piece_moments(const GroupShape& d, const Piece<EV>& p, const typename IO::T* x,
+                                              float2 (&sh)[EV][256], F&& f) {
+    float mean[EV], m2[EV];
 #pragma unroll
-            for (int e = 0; e < EV; ++e) shift += first[e];
-            shift *= 1.0f / EV;
-            for (int col = p.col; col < (cgv > 256 ? cgv : p.col + 1); col += 256) {
-                const typename IO::T* c = at + col * EV;
-#pragma unroll 4
-                for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
-                    float v[EV];
-                    ldv<IO, EV>(c + r * d.x_stride, v);
+    for (int e = 0; e < EV; ++e) mean[e] = m2[e] = 0.0f;
+    if (p.on && p.r0 + p.rl < p.r1) {
+        const typename IO::T* at = x + (p.n * d.s + p.r0 + p.rl) * d.x_stride + p.channel();
+        float first[EV], s1[EV], s2[EV];
+        ldv<IO, EV>(at, first);
 #pragma unroll
-                    for (int e = 0; e < EV; ++e) {
-                        const float o = v[e] - shift;
-                        s1 += o;
-                        s2 += o * o;
-                    }
-                }
-                count += static_cast<float>(mine * EV);
+        for (int e = 0; e < EV; ++e) s1[e] = s2[e] = 0.0f;
+        const int64_t rows = lane_rows(p.r0, p.r1, p.rl, p.lanes), step = p.lanes * d.x_stride;
+#pragma unroll 8
+        for (int64_t r = 1; r < rows; ++r) {
+            float v[EV];
+            ldv<IO, EV>(at + r * step, v);
+#pragma unroll
+            for (int e = 0; e < EV; ++e) {
+                const float o = v[e] - first[e];
+                s1[e] += o;
+                s2[e] += o * o;
             }
-            mean = shift + s1 / count;
-            m2 = fmaxf(s2 - s1 * (s1 / count), 0.0f);
         }
-        __syncthreads();
-        sh[threadIdx.x] = make_float2(mean, m2);
-        __syncthreads();
-        const int per = cgv < 256 ? cgv : 256;  // threads of a group in a row lane
-        const float rows = static_cast<float>(p.r1 - p.r0);
-        for (int g = threadIdx.x / SUB; g < p.ng; g += 256 / SUB) {
-            auto row_lane = [&](int k) { return k / per; };
-            auto cnt = [&](int k) {
-                const int rl = row_lane(k), c = k % per;
-                const int64_t n = p.r0 + rl < p.r1 ? (p.r1 - p.r0 - rl + d.lanes - 1) / d.lanes : 0;
-                const int vecs = cgv > 256 ? (cgv - c + 255) / 256 : 1;
-                return static_cast<float>(n * vecs * EV);
-            };
-            auto r = [&](int k) { return sh[row_lane(k) * p.cv + g * per + k % per]; };
-            float mu, q;
-            join_moments(d.lanes * per, r, cnt, rows * static_cast<float>(d.cg), mu, q);
-            if (threadIdx.x % SUB == 0) rec[(p.n * d.groups + p.g0 + g) * d.blocks + p.block] = make_float2(mu, q);
+        const float cnt = static_cast<float>(rows), inv = 1.0f / cnt;
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+            mean[e] = first[e] + s1[e] * inv;
+            m2[e] = fmaxf(s2[e] - s1[e] * (s1[e] * inv), 0.0f);
         }
+        // channels of one group, `sub` at a time, by halves of equal counts
+#pragma unroll
+        for (int wide = 1; wide < EV; wide *= 2)
+            if (wide < d.sub) {
+#pragma unroll
+                for (int e = 0; e < EV; e += 2 * wide) {
+                    const float off = mean[e + wide] - mean[e];
+                    m2[e] += m2[e + wide] + off * off * (0.5f * cnt * static_cast<float>(wide));
+                    mean[e] += 0.5f * off;
+                }
+            }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EV; ++e) sh[e][threadIdx.x] = make_float2(mean[e], m2[e]);
+    __syncthreads();
+    // per group: its records of every row lane, joined by a power of two of lanes
+    const int per = p.nch / (p.ng * d.sub), R = static_cast<int>(p.r1 - p.r0), base = R / p.lanes, more = R % p.lanes;
+    const float total = static_cast<float>(R) * static_cast<float>(per * d.sub);
+    int lanes = 64;
+    while (lanes > 8 && lanes * p.ng > 256) lanes /= 2;
+    auto team = [&](float v) {
+        for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor(v, o);
+        return v;
+    };
+    const int l = threadIdx.x % lanes;
+    for (int g = threadIdx.x / lanes; g < p.ng; g += 256 / lanes) {
+        auto each = [&](auto&& f) {
+            float sum = 0.0f;
+            for (int k = l; k < p.lanes * per; k += lanes) {
+                const int rl = k / per, c = (g * per + k - rl * per) * d.sub;
+                sum += f(sh[c % EV][rl * p.cv + c / EV], static_cast<float>((base + (rl < more)) * d.sub));
+            }
+            return team(sum);
+        };
+        const float mu = each([](float2 r, float cnt) { return cnt * r.x; }) / total;
+        const float sum = each([&](float2 r, float cnt) { return r.y + cnt * (r.x - mu) * (r.x - mu); });
+        if (l == 0) f(g, mu, sum);
     }
 }
 
-// y from the records, and the statistics where they are wanted.
+// y of a piece; stat(group): its mean and 1 / sqrt(var + eps).
+template <class IO, int EV, class F>
+__device__ __forceinline__ void piece_outputs(const GroupShape& d, const Piece<EV>& p, const typename IO::T* x,
+                                              const float* weight, const float* bias, const typename IO::T* gate,
+                                              F&& stat, typename IO::T* y) {
+    if (!p.on) return;
+    const Act act{d.act, gate != nullptr};
+    const int ch = p.channel();
+    float mean[EV], w[EV], b[EV];
+    ld_chan<EV>(weight, ch, 1.0f, w);
+    ld_chan<EV>(bias, ch, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < EV; ++e) {
+        const float2 t = stat((ch + e) / d.cg);
+        mean[e] = t.x;
+        w[e] *= t.y;
+    }
+#pragma unroll 4
+    for (int64_t r = p.r0 + p.rl; r < p.r1; r += p.lanes) {
+        const int64_t row = p.n * d.s + r;
+        float v[EV], z[EV];
+        ldv<IO, EV>(x + row * d.x_stride + ch, v);
+        if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
+#pragma unroll
+        for (int e = 0; e < EV; ++e) v[e] = act.out((v[e] - mean[e]) * w[e] + b[e], gate ? z[e] : 0.0f);
+        stv<IO, EV>(y + row * d.c + ch, v);
+    }
+}
+
+}  // namespace
+
+// Everything of a slab's groups of one sample.
+template <class IO, int EV>
+__global__ __launch_bounds__(256) void k_group_norm_whole(GroupShape d, const typename IO::T* __restrict__ x,
+                                                          const float* __restrict__ weight,
+                                                          const float* __restrict__ bias,
+                                                          const typename IO::T* __restrict__ gate,
+                                                          typename IO::T* __restrict__ y, float* __restrict__ stats) {
+    __shared__ float2 sh[EV][256], st[256];
+    const int64_t items = d.n * d.sums.slabs;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Piece<EV> p(d, d.sums, item);
+        piece_moments<IO, EV>(d, p, x, sh, [&](int g, float mu, float sum) {
+            st[g] = make_float2(mu, 1.0f / sqrtf(sum * d.inv_count + d.eps));
+            if (stats) reinterpret_cast<float2*>(stats)[p.n * d.groups + p.g0 + g] = st[g];
+        });
+        __syncthreads();
+        if (y) piece_outputs<IO, EV>(d, p, x, weight, bias, gate, [&](int g) { return st[g - p.g0]; }, y);
+    }
+}
+
+// Mean and sum of squared differences of every (sample, group, block of positions, cut):
+// rec [n, groups, blocks, cuts].
+template <class IO, int EV>
+__global__ __launch_bounds__(256) void k_group_norm_stats(GroupShape d, const typename IO::T* __restrict__ x,
+                                                          float2* __restrict__ rec) {
+    __shared__ float2 sh[EV][256];
+    const int64_t items = d.n * d.sums.blocks * d.sums.slabs;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Piece<EV> p(d, d.sums, item);
+        piece_moments<IO, EV>(d, p, x, sh, [&](int g, float mu, float sum) {
+            rec[((p.n * d.groups + p.g0 + g) * d.sums.blocks + p.block) * d.sums.cuts + p.cut] = make_float2(mu, sum);
+        });
+    }
+}
+
+// The statistics of a (sample, group) from its records, a wave each.
+__global__ __launch_bounds__(256) void k_group_norm_join(GroupShape d, const float2* __restrict__ rec,
+                                                         float2* __restrict__ stats) {
+    const int K = d.sums.blocks * d.sums.cuts, l = threadIdx.x & 63;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); at < d.n * d.groups;
+         at += static_cast<int64_t>(gridDim.x) * 4) {
+        float2 r[MAXREC / 64];
+        float cnt[MAXREC / 64], sum = 0.0f;
+#pragma unroll
+        for (int m = 0; m < MAXREC / 64; ++m) {
+            const int k = l + m * 64;
+            r[m] = make_float2(0.0f, 0.0f);
+            cnt[m] = 0.0f;
+            if (k < K) {
+                r[m] = rec[at * K + k];
+                const int64_t r0 = static_cast<int64_t>(k / d.sums.cuts) * d.sums.rows;
+                const int wide = d.cg - k % d.sums.cuts * 256 * d.ev;
+                cnt[m] = static_cast<float>((r0 + d.sums.rows < d.s ? d.sums.rows : d.s - r0) *
+                                            (d.sums.cuts > 1 && wide > 256 * d.ev ? 256 * d.ev : wide));
+            }
+            sum += cnt[m] * r[m].x;
+        }
+        const float mu = team_sum<64>(sum) * d.inv_count;
+        sum = 0.0f;
+#pragma unroll
+        for (int m = 0; m < MAXREC / 64; ++m) sum += r[m].y + cnt[m] * (r[m].x - mu) * (r[m].x - mu);
+        sum = team_sum<64>(sum);
+        if (l == 0) stats[at] = make_float2(mu, 1.0f / sqrtf(sum * d.inv_count + d.eps));
+    }
+}
+
 template <class IO, int EV>
 __global__ __launch_bounds__(256) void k_group_norm_apply(GroupShape d, const typename IO::T* __restrict__ x,
                                                           const float* __restrict__ weight,
                                                           const float* __restrict__ bias,
                                                           const typename IO::T* __restrict__ gate,
-                                                          const float2* __restrict__ rec,
-                                                          typename IO::T* __restrict__ y, float* __restrict__ stats) {
-    __shared__ float2 sh[256];
-    const Act act{d.act, gate != nullptr};
-    const int64_t items = d.n * (y ? d.blocks : 1) * d.slabs;
-    const int cgv = d.cg / EV;
+                                                          const float2* __restrict__ stats,
+                                                          typename IO::T* __restrict__ y) {
+    const int64_t items = d.n * d.outs.blocks * d.outs.slabs;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        // without y one workgroup joins a slab's records
-        const Piece p(d, y ? item : item / d.slabs * d.blocks * d.slabs + item % d.slabs, EV);
-        __syncthreads();
-        for (int g = threadIdx.x / SUB; g < p.ng; g += 256 / SUB) {
-            const float2* from = rec + (p.n * d.groups + p.g0 + g) * d.blocks;
-            auto cnt = [&](int k) {
-                const int64_t r0 = static_cast<int64_t>(k) * d.rows;
-                return static_cast<float>((r0 + d.rows < d.s ? d.rows : d.s - r0) * d.cg);
-            };
-            float mu, q;
-            join_moments(d.blocks, [&](int k) { return from[k]; }, cnt, d.count, mu, q);
-            if (threadIdx.x % SUB == 0) {
-                const float2 st = make_float2(mu, 1.0f / sqrtf(q * d.inv_count + d.eps));
-                sh[g] = st;
-                if (stats && p.block == 0) reinterpret_cast<float2*>(stats)[p.n * d.groups + p.g0 + g] = st;
-            }
-        }
-        __syncthreads();
-        if (!p.on || !y) continue;
-        for (int col = p.col; col < (cgv > 256 ? cgv : p.col + 1); col += 256) {
-            const float2 st = sh[cgv > 256 ? 0 : col / cgv];
-            const int ch = p.g0 * d.cg + col * EV;
-            float w[EV], b[EV];
-            ld_chan<EV>(weight, ch, 1.0f, w);
-            ld_chan<EV>(bias, ch, 0.0f, b);
-#pragma unroll
-            for (int e = 0; e < EV; ++e) w[e] *= st.y;
-#pragma unroll 4
-            for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
-                const int64_t row = p.n * d.s + r;
-                float v[EV], z[EV];
-                ldv<IO, EV>(x + row * d.x_stride + ch, v);
-                if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
-#pragma unroll
-                for (int e = 0; e < EV; ++e) v[e] = act.out((v[e] - st.x) * w[e] + b[e], gate ? z[e] : 0.0f);
-                stv<IO, EV>(y + row * d.c + ch, v);
-            }
-        }
+        const Piece<EV> p(d, d.outs, item);
+        piece_outputs<IO, EV>(d, p, x, weight, bias, gate, [&](int g) { return stats[p.n * d.groups + g]; }, y);
     }
 }
 
@@ -416,52 +501,51 @@ __global__ __launch_bounds__(256) void k_group_norm_sums(GroupShape d, const typ
                                                          const float* __restrict__ stats, float* __restrict__ part) {
     __shared__ float sh[2 * EV][256];
     const Act act{d.act, gate != nullptr};
-    const int64_t items = d.n * d.blocks * d.slabs;
-    const int cgv = d.cg / EV;
+    const int64_t items = d.n * d.sums.blocks * d.sums.slabs;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const Piece p(d, item, EV);
-        for (int c0 = 0; c0 < (cgv > 256 ? cgv : 1); c0 += 256) {
-            const int col = c0 + p.col;
-            const bool on = p.on && (cgv <= 256 || col < cgv);
-            float s1[EV], s2[EV];
+        const Piece<EV> p(d, d.sums, item);
+        float s1[EV], s2[EV];
 #pragma unroll
-            for (int e = 0; e < EV; ++e) s1[e] = s2[e] = 0.0f;
-            const int ch = p.g0 * d.cg + col * EV;
-            if (on) {
-                const float2 st = reinterpret_cast<const float2*>(stats)[p.n * d.groups + p.g0 + (cgv > 256 ? 0 : col / cgv)];
-                float w[EV], b[EV];
-                ld_chan<EV>(weight, ch, 1.0f, w);
-                ld_chan<EV>(bias, ch, 0.0f, b);
-#pragma unroll 2
-                for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
-                    const int64_t row = p.n * d.s + r;
-                    float v[EV], g[EV], z[EV], dg;
-                    ldv<IO, EV>(x + row * d.x_stride + ch, v);
-                    ldv<IO, EV>(dy + row * d.c + ch, g);
-                    if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
-#pragma unroll
-                    for (int e = 0; e < EV; ++e) {
-                        const float m = (v[e] - st.x) * st.y;
-                        const float du = act.back(g[e], m * w[e] + b[e], gate ? z[e] : 0.0f, dg);
-                        s1[e] += du;
-                        s2[e] += du * m;
-                    }
-                }
-            }
-            __syncthreads();
+        for (int e = 0; e < EV; ++e) s1[e] = s2[e] = 0.0f;
+        if (p.on) {
+            const int ch = p.channel();
+            float w[EV], b[EV], mean[EV], rstd[EV];
+            ld_chan<EV>(weight, ch, 1.0f, w);
+            ld_chan<EV>(bias, ch, 0.0f, b);
 #pragma unroll
             for (int e = 0; e < EV; ++e) {
-                sh[e][threadIdx.x] = s1[e];
-                sh[EV + e][threadIdx.x] = s2[e];
+                const float2 st = reinterpret_cast<const float2*>(stats)[p.n * d.groups + (ch + e) / d.cg];
+                mean[e] = st.x;
+                rstd[e] = st.y;
             }
-            __syncthreads();
-            for (int k = threadIdx.x; k < 2 * EV * p.cv; k += 256) {
-                const int e = k / p.cv, at = k % p.cv;
-                if (cgv > 256 ? c0 + at >= cgv : at >= p.ng * cgv) continue;
-                float sum = 0.0f;
-                for (int l = 0; l < d.lanes; ++l) sum += sh[e][l * p.cv + at];
-                part[((p.n * d.blocks + p.block) * 2 + e / EV) * d.c + p.g0 * d.cg + (c0 + at) * EV + e % EV] = sum;
+#pragma unroll 4
+            for (int64_t r = p.r0 + p.rl; r < p.r1; r += p.lanes) {
+                const int64_t row = p.n * d.s + r;
+                float v[EV], g[EV], z[EV], dg;
+                ldv<IO, EV>(x + row * d.x_stride + ch, v);
+                ldv<IO, EV>(dy + row * d.c + ch, g);
+                if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
+#pragma unroll
+                for (int e = 0; e < EV; ++e) {
+                    const float m = (v[e] - mean[e]) * rstd[e];
+                    const float du = act.back(g[e], m * w[e] + b[e], gate ? z[e] : 0.0f, dg);
+                    s1[e] += du;
+                    s2[e] += du * m;
+                }
             }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+            sh[e][threadIdx.x] = s1[e];
+            sh[EV + e][threadIdx.x] = s2[e];
+        }
+        __syncthreads();
+        for (int k = threadIdx.x; k < 2 * p.nch; k += 256) {
+            const int which = k >= p.nch, c = k - which * p.nch;
+            float sum = 0.0f;
+            for (int l = 0; l < p.lanes; ++l) sum += sh[which * EV + c % EV][l * p.cv + c / EV];
+            part[((p.n * d.sums.blocks + p.block) * 2 + which) * d.c + p.ch0 + c] = sum;
         }
     }
 }
@@ -484,9 +568,9 @@ __global__ __launch_bounds__(256) void k_group_norm_means(GroupShape d, const fl
             float a = 0.0f, b = 0.0f;
             if (c < d.cg) {
 #pragma unroll 4
-                for (int k = bl; k < d.blocks; k += lanes) {
-                    a += part[((n * d.blocks + k) * 2) * d.c + ch];
-                    b += part[((n * d.blocks + k) * 2 + 1) * d.c + ch];
+                for (int k = bl; k < d.sums.blocks; k += lanes) {
+                    a += part[((n * d.sums.blocks + k) * 2) * d.c + ch];
+                    b += part[((n * d.sums.blocks + k) * 2 + 1) * d.c + ch];
                 }
             }
             __syncthreads();
@@ -530,34 +614,38 @@ __global__ __launch_bounds__(256) void k_group_norm_grad(GroupShape d, const typ
                                                          typename IO::T* __restrict__ d_x,
                                                          typename IO::T* __restrict__ d_gate) {
     const Act act{d.act, gate != nullptr};
-    const int64_t items = d.n * d.blocks * d.slabs;
-    const int cgv = d.cg / EV;
+    const int64_t items = d.n * d.outs.blocks * d.outs.slabs;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const Piece p(d, item, EV);
+        const Piece<EV> p(d, d.outs, item);
         if (!p.on) continue;
-        for (int col = p.col; col < (cgv > 256 ? cgv : p.col + 1); col += 256) {
-            const int64_t at = p.n * d.groups + p.g0 + (cgv > 256 ? 0 : col / cgv);
-            const float2 st = reinterpret_cast<const float2*>(stats)[at], mn = mean[at];
-            const int ch = p.g0 * d.cg + col * EV;
-            float w[EV], b[EV];
-            ld_chan<EV>(weight, ch, 1.0f, w);
-            ld_chan<EV>(bias, ch, 0.0f, b);
-#pragma unroll 2
-            for (int64_t r = p.r0 + p.rl; r < p.r1; r += d.lanes) {
-                const int64_t row = p.n * d.s + r;
-                float v[EV], g[EV], z[EV], dg[EV];
-                ldv<IO, EV>(x + row * d.x_stride + ch, v);
-                ldv<IO, EV>(dy + row * d.c + ch, g);
-                if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
+        const int ch = p.channel();
+        float w[EV], b[EV], mu[EV], rstd[EV], m1[EV], m2[EV];
+        ld_chan<EV>(weight, ch, 1.0f, w);
+        ld_chan<EV>(bias, ch, 0.0f, b);
 #pragma unroll
-                for (int e = 0; e < EV; ++e) {
-                    const float m = (v[e] - st.x) * st.y;
-                    const float du = act.back(g[e], m * w[e] + b[e], gate ? z[e] : 0.0f, dg[e]);
-                    v[e] = st.y * (w[e] * du - mn.x - m * mn.y);
-                }
-                stv<IO, EV>(d_x + row * d.c + ch, v);
-                if (gate) stv<IO, EV>(d_gate + row * d.c + ch, dg);
+        for (int e = 0; e < EV; ++e) {
+            const int64_t at = p.n * d.groups + (ch + e) / d.cg;
+            const float2 st = reinterpret_cast<const float2*>(stats)[at], mn = mean[at];
+            mu[e] = st.x;
+            rstd[e] = st.y;
+            m1[e] = mn.x;
+            m2[e] = mn.y;
+        }
+#pragma unroll 4
+        for (int64_t r = p.r0 + p.rl; r < p.r1; r += p.lanes) {
+            const int64_t row = p.n * d.s + r;
+            float v[EV], g[EV], z[EV], dg[EV];
+            ldv<IO, EV>(x + row * d.x_stride + ch, v);
+            ldv<IO, EV>(dy + row * d.c + ch, g);
+            if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch, z);
+#pragma unroll
+            for (int e = 0; e < EV; ++e) {
+                const float m = (v[e] - mu[e]) * rstd[e];
+                const float du = act.back(g[e], m * w[e] + b[e], gate ? z[e] : 0.0f, dg[e]);
+                v[e] = rstd[e] * (w[e] * du - m1[e] - m * m2[e]);
             }
+            stv<IO, EV>(d_x + row * d.c + ch, v);
+            if (gate) stv<IO, EV>(d_gate + row * d.c + ch, dg);
         }
     }
 }
@@ -630,34 +718,63 @@ hipError_t by_io(const GroupShape& d, F&& f) {
 // Which way, and how the work is cut up.
 void group_norm_plan(GroupShape* d, bool bwd) {
     const int V = d->io == 1 ? 8 : 4;
-    d->ev = V;
-    while (d->cg % d->ev || d->x_stride % d->ev || d->gate_stride % d->ev) d->ev /= 2;
+    auto widest = [&](int of) {
+        int ev = V;
+        while (of % ev || d->x_stride % ev || d->gate_stride % ev) ev /= 2;
+        return ev;
+    };
+    d->ev = widest(d->cg);
     const int cgv = d->cg / d->ev;
     d->tokens = d->s == 1 && cgv <= 512;
     if (d->tokens) {
         if (!bwd) return;
+        GroupCut& c = d->sums;
         const int teams = 256 / team_of(cgv);
-        d->slab_groups = d->groups < teams ? d->groups : teams;
-        d->lanes = teams / d->slab_groups;
-        d->slabs = (d->groups + d->slab_groups - 1) / d->slab_groups;
-        int64_t b = 2048 / d->slabs;
-        const int64_t most = (d->n + d->lanes - 1) / d->lanes;
-        if (b > 1024 / d->lanes) b = 1024 / d->lanes;
+        c.slab_groups = d->groups < teams ? d->groups : teams;
+        c.lanes = teams / c.slab_groups;
+        c.slabs = (d->groups + c.slab_groups - 1) / c.slab_groups;
+        int64_t b = 2048 / c.slabs;
+        const int64_t most = (d->n + c.lanes - 1) / c.lanes;
+        if (b > 1024 / c.lanes) b = 1024 / c.lanes;
         if (b > most) b = most;
-        d->blocks = static_cast<int>(b < 1 ? 1 : b);
+        c.blocks = static_cast<int>(b < 1 ? 1 : b);
         return;
     }
-    d->slab_groups = cgv >= 256 ? 1 : 256 / cgv;
-    if (d->slab_groups > d->groups) d->slab_groups = d->groups;
-    d->slabs = (d->groups + d->slab_groups - 1) / d->slab_groups;
-    const int cv = d->slab_groups * cgv < 256 ? d->slab_groups * cgv : 256;
-    d->lanes = 256 / cv;
-    int64_t b = 2048 / (d->n * d->slabs), most = (d->s + 4 * d->lanes - 1) / (4 * d->lanes);
-    if (b > 256) b = 256;
-    if (b > most) b = most;
-    if (b < 1) b = 1;
-    d->rows = (d->s + b - 1) / b;
-    d->blocks = static_cast<int>((d->s + d->rows - 1) / d->rows);
+    // vectors that reach over groups, where a slab of whole groups is whole vectors (ten channels of
+    // bf16: vectors of eight over slabs of a multiple of four groups)
+    const int wide = widest(d->c);
+    int unit = 1;  // groups of whole vectors
+    while (unit * d->cg % wide) unit *= 2;
+    if (wide > d->ev && unit * d->cg / wide <= 256)
+        d->ev = wide;
+    else
+        unit = 1;
+    d->sub = 1;
+    while (2 * d->sub <= d->ev && d->cg % (2 * d->sub) == 0) d->sub *= 2;
+    const int unit_vectors = unit * d->cg / d->ev;
+    auto cut = [&](int units, int each, int most) {
+        GroupCut c{};
+        c.cuts = unit_vectors > 256 ? (unit_vectors + 255) / 256 : 1;
+        c.slab_groups = units < 2 ? unit : units * unit;
+        if (c.slab_groups > 256) c.slab_groups = 256;  // (a whole number of units, at most eight groups)
+        if (c.slab_groups > d->groups) c.slab_groups = d->groups;
+        c.slabs = (d->groups + c.slab_groups - 1) / c.slab_groups * c.cuts;
+        c.lanes = c.cuts > 1 ? 1 : 256 / (c.slab_groups * d->cg / d->ev);
+        // blocks of positions: workgroups for the chip, at least `each` positions a thread
+        int64_t b = 2048 / (d->n * c.slabs);
+        const int64_t whole = (d->s + each * c.lanes - 1) / (each * c.lanes);
+        if (b > most / c.cuts) b = most / c.cuts;
+        if (b > whole) b = whole;
+        if (b < 1) b = 1;
+        c.rows = (d->s + b - 1) / b;
+        c.blocks = static_cast<int>((d->s + c.rows - 1) / c.rows);
+        return c;
+    };
+    // sums: about 256 bytes of neighbouring channels, which leave many positions to a workgroup and few
+    // records to a group; outputs: whole rows
+    d->sums = cut((15 + unit_vectors) / unit_vectors, 8, MAXREC);
+    d->outs = cut(256 / unit_vectors, 4, 1 << 20);
+    d->whole = d->sums.blocks == 1 && d->sums.cuts == 1;
 }
 
 hipError_t launch_group_norm(const GroupShape& d, const void* x, const float* weight, const float* bias,
@@ -678,26 +795,45 @@ hipError_t launch_group_norm(const GroupShape& d, const void* x, const float* we
     });
 }
 
+hipError_t launch_group_norm_whole(const GroupShape& d, const void* x, const float* weight, const float* bias,
+                                   const void* gate, void* y, float* stats, hipStream_t st) {
+    return by_io(d, [&](auto io_) {
+        using IO = decltype(io_);
+        using T = typename IO::T;
+        return by_vector<IO>(d, [&](auto ev) {
+            k_group_norm_whole<IO, decltype(ev)::value><<<grid_of(d.n * d.sums.slabs), 256, 0, st>>>(
+                d, static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate), static_cast<T*>(y), stats);
+            return hipGetLastError();
+        });
+    });
+}
+
 hipError_t launch_group_norm_stats(const GroupShape& d, const void* x, float* rec, hipStream_t st) {
     return by_io(d, [&](auto io_) {
         using IO = decltype(io_);
         return by_vector<IO>(d, [&](auto ev) {
-            k_group_norm_stats<IO, decltype(ev)::value><<<grid_of(d.n * d.blocks * d.slabs), 256, 0, st>>>(
+            k_group_norm_stats<IO, decltype(ev)::value><<<grid_of(d.n * d.sums.blocks * d.sums.slabs), 256, 0, st>>>(
                 d, static_cast<const typename IO::T*>(x), reinterpret_cast<float2*>(rec));
             return hipGetLastError();
         });
     });
 }
 
+hipError_t launch_group_norm_join(const GroupShape& d, const float* rec, float* stats, hipStream_t st) {
+    k_group_norm_join<<<grid_of((d.n * d.groups + 3) / 4), 256, 0, st>>>(d, reinterpret_cast<const float2*>(rec),
+                                                                         reinterpret_cast<float2*>(stats));
+    return hipGetLastError();
+}
+
 hipError_t launch_group_norm_apply(const GroupShape& d, const void* x, const float* weight, const float* bias,
-                                   const void* gate, const float* rec, void* y, float* stats, hipStream_t st) {
+                                   const void* gate, const float* stats, void* y, hipStream_t st) {
     return by_io(d, [&](auto io_) {
         using IO = decltype(io_);
         using T = typename IO::T;
         return by_vector<IO>(d, [&](auto ev) {
-            k_group_norm_apply<IO, decltype(ev)::value><<<grid_of(d.n * (y ? d.blocks : 1) * d.slabs), 256, 0, st>>>(
+            k_group_norm_apply<IO, decltype(ev)::value><<<grid_of(d.n * d.outs.blocks * d.outs.slabs), 256, 0, st>>>(
                 d, static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
-                reinterpret_cast<const float2*>(rec), static_cast<T*>(y), stats);
+                reinterpret_cast<const float2*>(stats), static_cast<T*>(y));
             return hipGetLastError();
         });
     });
@@ -713,7 +849,7 @@ hipError_t launch_group_norm_rows_bwd(const GroupShape& d, const void* dy, const
             constexpr int EV = decltype(ev)::value;
             return by_team(d.cg / EV, [&](auto nv, auto ts) {
                 constexpr int NV = decltype(nv)::value, TS = decltype(ts)::value;
-                k_group_norm_rows_bwd<IO, EV, NV, TS><<<static_cast<unsigned>(d.blocks * d.slabs), 256, 0, st>>>(
+                k_group_norm_rows_bwd<IO, EV, NV, TS><<<static_cast<unsigned>(d.sums.blocks * d.sums.slabs), 256, 0, st>>>(
                     d, static_cast<const T*>(dy), static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
                     stats, static_cast<T*>(d_x), static_cast<T*>(d_gate), part);
                 return hipGetLastError();
@@ -729,7 +865,7 @@ hipError_t launch_group_norm_sums(const GroupShape& d, const void* dy, const voi
         using IO = decltype(io_);
         using T = typename IO::T;
         return by_vector<IO>(d, [&](auto ev) {
-            k_group_norm_sums<IO, decltype(ev)::value><<<grid_of(d.n * d.blocks * d.slabs), 256, 0, st>>>(
+            k_group_norm_sums<IO, decltype(ev)::value><<<grid_of(d.n * d.sums.blocks * d.sums.slabs), 256, 0, st>>>(
                 d, static_cast<const T*>(dy), static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
                 stats, part);
             return hipGetLastError();
@@ -750,7 +886,7 @@ hipError_t launch_group_norm_grad(const GroupShape& d, const void* dy, const voi
         using IO = decltype(io_);
         using T = typename IO::T;
         return by_vector<IO>(d, [&](auto ev) {
-            k_group_norm_grad<IO, decltype(ev)::value><<<grid_of(d.n * d.blocks * d.slabs), 256, 0, st>>>(
+            k_group_norm_grad<IO, decltype(ev)::value><<<grid_of(d.n * d.outs.blocks * d.outs.slabs), 256, 0, st>>>(
                 d, static_cast<const T*>(dy), static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
                 stats, reinterpret_cast<const float2*>(mean), static_cast<T*>(d_x), static_cast<T*>(d_gate));
             return hipGetLastError();

@@ -649,9 +649,9 @@ int validate_group_norm(const char* who, const ssd_group_norm_dims* n, ssd::Grou
     const double cg = (double)(n->channels / n->groups);
     const double rows = (double)n->batch * (double)n->positions;
     const double wide = std::max({(double)n->channels, (double)n->x_stride, (double)n->gate_stride});
-    if (n->channels >= (1 << 20) || cg * (double)n->positions >= 2147483648.0 || rows * wide >= 1152921504606846976.0)
-        return fail(SSD_ERR_UNSUPPORTED, "%s: channels must be below 2^20, the values of a group below 2^31 and the "
-                    "tensors below 2^60 elements", who);
+    if (n->channels >= (1 << 20) || cg > 32768.0 || cg * (double)n->positions >= 2147483648.0 || rows * wide >= 1152921504606846976.0)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: channels must be below 2^20, those of a group at most 32768, its values "
+                    "below 2^31 and the tensors below 2^60 elements", who);
     *d = ssd::GroupShape{};
     d->n = n->batch;
     d->s = n->positions;
@@ -669,10 +669,11 @@ int validate_group_norm(const char* who, const ssd_group_norm_dims* n, ssd::Grou
     return SSD_OK;
 }
 
-// Workspace of the group norm.  Forward: the records of the blocks of positions (none for tokens).
+// Workspace of the group norm.  Forward: the records of the blocks of positions and the
+// statistics (none for tokens, or where one launch does it all).
 // Backward: sums per part and channel; but for tokens also their totals per sample and the groups' means.
 struct GroupBufs {
-    float *part, *chan, *mean;
+    float *part, *chan, *mean, *stats;
 };
 size_t group_norm_bytes(const ssd::GroupShape& d, bool bwd, void* ws, GroupBufs* f) {
     size_t off = 0;
@@ -684,11 +685,14 @@ size_t group_norm_bytes(const ssd::GroupShape& d, bool bwd, void* ws, GroupBufs*
     if (d.n == 0) return 0;
     const size_t n = static_cast<size_t>(d.n), c = static_cast<size_t>(d.c), g = static_cast<size_t>(d.groups);
     if (!bwd) {
-        if (!d.tokens) f->part = take(2 * n * g * d.blocks);
+        if (!d.tokens && !d.whole) {
+            f->part = take(2 * n * g * d.sums.blocks * d.sums.cuts);
+            f->stats = take(2 * n * g);
+        }
     } else if (d.tokens) {
-        f->part = take(2 * static_cast<size_t>(d.blocks) * d.lanes * c);
+        f->part = take(2 * static_cast<size_t>(d.sums.blocks) * d.sums.lanes * c);
     } else {
-        f->part = take(2 * n * d.blocks * c);
+        f->part = take(2 * n * d.sums.blocks * c);
         f->chan = take(2 * n * c);
         f->mean = take(2 * n * g);
     }
@@ -1618,8 +1622,14 @@ int ssd_group_norm(const ssd_group_norm_dims* dims, const void* x, const float* 
         SSD_HIP(ssd::launch_group_norm(d, x, weight, bias, gate, y, stats, st), "k_group_norm_rows");
         return ok();
     }
+    if (d.whole) {
+        SSD_HIP(ssd::launch_group_norm_whole(d, x, weight, bias, gate, y, stats, st), "k_group_norm_whole");
+        return ok();
+    }
     SSD_HIP(ssd::launch_group_norm_stats(d, x, f.part, st), "k_group_norm_stats");
-    SSD_HIP(ssd::launch_group_norm_apply(d, x, weight, bias, gate, f.part, y, stats, st), "k_group_norm_apply");
+    if (!stats) stats = f.stats;
+    SSD_HIP(ssd::launch_group_norm_join(d, f.part, stats, st), "k_group_norm_join");
+    if (y) SSD_HIP(ssd::launch_group_norm_apply(d, x, weight, bias, gate, stats, y, st), "k_group_norm_apply");
     return ok();
 }
 
@@ -1649,7 +1659,7 @@ int ssd_group_norm_bwd(const ssd_group_norm_dims* dims, const void* dy, const vo
         return ok();
     }
     const float* sums = d.tokens ? f.part : f.chan;
-    const int64_t parts = d.tokens ? static_cast<int64_t>(d.blocks) * d.lanes : d.n;
+    const int64_t parts = d.tokens ? static_cast<int64_t>(d.sums.blocks) * d.sums.lanes : d.n;
     if (d.tokens) {
         SSD_HIP(ssd::launch_group_norm_rows_bwd(d, dy, x, weight, bias, gate, stats, d_x, d_gate, f.part, st),
                 "k_group_norm_rows_bwd");

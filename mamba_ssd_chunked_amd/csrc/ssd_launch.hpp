@@ -398,25 +398,34 @@ hipError_t launch_rms_norm_bwd(const NormShape& n, const void* dy, const void* s
 hipError_t launch_rms_norm_weight(const NormShape& n, const float* part, float* d_weight, hipStream_t st);
 
 // ---------------------------------------------------------------- group norm
+// Slabs of whole groups (or cuts of a group wider than 256 vectors), positions a workgroup takes at a time
+// (lanes), blocks of `rows` positions (tokens: blocks of tokens).
+struct GroupCut {
+    int slab_groups, cuts, slabs, lanes, blocks;
+    int64_t rows;
+};
 struct GroupShape {
     int64_t n, s;           // samples, positions of each
     int c, groups, cg;      // channels, groups, channels of a group
     int64_t x_stride, gate_stride;  // elements between positions
     int io, act;
     float eps, count, inv_count;    // count: values of a group
-    // the plan: vector width; whether each position is a sample of its own (tokens); groups of a slab,
-    // slabs, positions a workgroup takes at a time, blocks of positions (of rows each) or of tokens
-    int ev, tokens, slab_groups, slabs, lanes, blocks;
-    int64_t rows;
+    // the plan: vector width, and its channels sure to share a group; whether each position is a sample of
+    // its own (tokens), or one workgroup has a slab of a sample (whole); how sums and outputs are cut up
+    int ev, sub, tokens, whole;
+    GroupCut sums, outs;
 };
 void group_norm_plan(GroupShape* d, bool bwd);
-// tokens: everything at once; otherwise records of the moments (stats), then the outputs (apply; y null: only
-// the statistics)
+// tokens, whole: everything at once; otherwise records of the moments (stats), the statistics (join) and the
+// outputs (apply)
 hipError_t launch_group_norm(const GroupShape& d, const void* x, const float* weight, const float* bias,
                              const void* gate, void* y, float* stats, hipStream_t st);
+hipError_t launch_group_norm_whole(const GroupShape& d, const void* x, const float* weight, const float* bias,
+                                   const void* gate, void* y, float* stats, hipStream_t st);
 hipError_t launch_group_norm_stats(const GroupShape& d, const void* x, float* rec, hipStream_t st);
+hipError_t launch_group_norm_join(const GroupShape& d, const float* rec, float* stats, hipStream_t st);
 hipError_t launch_group_norm_apply(const GroupShape& d, const void* x, const float* weight, const float* bias,
-                                   const void* gate, const float* rec, void* y, float* stats, hipStream_t st);
+                                   const void* gate, const float* stats, void* y, hipStream_t st);
 // tokens: d_x, d_gate and part [blocks * lanes, 2, c] for launch_group_norm_weight; otherwise channel sums of
 // the blocks, their totals chan [n, 2, c] (also for it) and the groups' means, then d_x and d_gate
 hipError_t launch_group_norm_rows_bwd(const GroupShape& d, const void* dy, const void* x, const float* weight,

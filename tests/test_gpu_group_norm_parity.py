@@ -47,7 +47,8 @@ def test_tokens(io, act, gate, groups, cg):
 @pytest.mark.parametrize("io", IOS)
 @pytest.mark.parametrize("act,gate", CHOICES)
 @pytest.mark.parametrize("shape,groups", [((2, 64, 256), 32), ((3, 5, 7, 320), 32), ((1, 4087, 20), 2), ((2, 2, 30), 1),
-                                          ((40, 3, 96), 4), ((2, 33, 2500), 2), ((1, 700, 8), 8), ((2, 9, 4000), 1),
+                                          ((40, 3, 96), 4), ((2, 33, 2500), 2), ((1, 700, 8), 8), ((2, 9, 4000), 1), ((2, 6, 900), 900), ((1, 11, 2056), 1028), ((1, 3, 32768), 1),
+                                          ((1, 300, 4099), 1),
                                           ((1, 5000, 14), 2)])
 def test_positions(io, act, gate, shape, groups):
     t = ref.group_norm_inputs(shape, sum(shape), io, gate)
