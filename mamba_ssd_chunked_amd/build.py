@@ -20,7 +20,7 @@ LIB = os.path.join(OUT_DIR, "libmamba_ssd_hip.so")
 SOURCES = ["ssd_abi.cpp", "k_scan.hip", "k_chunk_fwd.hip", "k_chunk_bwd.hip", "k_chunk_wide.hip",
            "k_moments.hip", "k_pr.hip", "k_diag.hip", "k_quat.hip", "k_step.hip",
            "noalloc_scratch.hip", "k_stream.hip", "k_delta.hip", "k_delta_bwd.hip",
-           "k_delta_step.hip", "k_norm.hip", "k_linear.hip", "k_linear_step.hip",
+           "k_delta_step.hip", "k_norm.hip", "k_linear.hip", "k_linear_bwd.hip", "k_linear_step.hip",
            "k_group_norm.hip"]
 ARCH = "gfx950"
 

@@ -508,20 +508,20 @@ int validate_linear(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape
     return validate_heads(who, dims, d, [](const ssd_delta_dims&) { return 512.0; });
 }
 
-ssd::LinearShape linear_shape(const ssd::DeltaShape& d, const float* log_decay, int jobs) {
-    const int c = ssd::linear_chunk(d.io);
+ssd::LinearShape linear_shape(const ssd::DeltaShape& d, const float* log_decay, bool bwd) {
+    const int c = ssd::kLinearChunk;
     ssd::LinearShape s{d.B, d.S, d.H, d.P, d.R, d.io, (d.S + c - 1) / c, 1, 0, nullptr, log_decay};
-    s.segs = ssd::linear_segments(s, jobs);
+    s.segs = ssd::linear_segments(s, bwd);
     s.seg_chunks = (s.N + s.segs - 1) / s.segs;
     return s;
 }
 
 // Workspace of linear attention: the lengths; in segments their entry states (the backward: of both
 // directions, and of the derivative along the decay); the backward's per-head d_q and d_k where
-// key heads are shared, and the sums of the decay's gradient.
+// key heads are shared, the sums of the decay's gradient, and d_final where d_init takes its place.
 struct LinearBufs {
     int64_t* len;
-    float *H, *G, *dq, *dk;
+    float *H, *G, *dq, *dk, *d_final;
     double* dots;
 };
 size_t linear_plan(const ssd::DeltaShape& d, const ssd::LinearShape& s, bool bwd, void* ws, LinearBufs* f) {
@@ -540,6 +540,7 @@ size_t linear_plan(const ssd::DeltaShape& d, const ssd::LinearShape& s, bool bwd
         f->dq = reinterpret_cast<float*>(take(d.H != d.HK ? rows : 0));
         f->dk = reinterpret_cast<float*>(take(d.H != d.HK ? rows : 0));
         f->dots = reinterpret_cast<double*>(take(8 * static_cast<size_t>(s.H) * ssd::linear_dots(s)));
+        f->d_final = reinterpret_cast<float*>(take(4 * static_cast<size_t>(s.B) * s.H * s.P * s.R));
     }
     return off;
 }
@@ -1321,7 +1322,7 @@ int ssd_linear_workspace_size(const ssd_delta_dims* dims, int bwd, size_t* bytes
     if (int rc = validate_linear("ssd_linear_workspace_size", dims, &d)) return rc;
     if (!bytes) return fail(SSD_ERR_NULL, "ssd_linear_workspace_size: bytes is NULL");
     LinearBufs f{};
-    *bytes = linear_plan(d, linear_shape(d, nullptr, bwd ? 2 : 1), bwd != 0, nullptr, &f);
+    *bytes = linear_plan(d, linear_shape(d, nullptr, bwd != 0), bwd != 0, nullptr, &f);
     return ok();
 }
 
@@ -1338,7 +1339,7 @@ int ssd_linear_fwd(const ssd_delta_dims* dims, const void* q, const void* k, con
     if (overlap_unequal(init, final_state, (size_t)d.B * d.H * d.P * d.R))
         return fail(SSD_ERR_UNSUPPORTED, "%s: init and final_state overlap without being equal", who);
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
-    ssd::LinearShape s = linear_shape(d, log_decay, 1);
+    ssd::LinearShape s = linear_shape(d, log_decay, false);
     LinearBufs f{};
     const size_t need = linear_plan(d, s, false, ws, &f);
     if (tok)
@@ -1397,7 +1398,7 @@ int ssd_linear_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fi
     if (overlap_unequal(d_final, d_init, (size_t)d.B * d.H * d.P * d.R))
         return fail(SSD_ERR_UNSUPPORTED, "%s: d_final and d_init overlap without being equal", who);
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
-    ssd::LinearShape s = linear_shape(d, log_decay, 2);
+    ssd::LinearShape s = linear_shape(d, log_decay, true);
     LinearBufs f{};
     const size_t need = linear_plan(d, s, true, ws, &f);
     if (tok)
@@ -1415,6 +1416,10 @@ int ssd_linear_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fi
     }
     const int grp = d.H / d.HK;
     const int64_t size = static_cast<int64_t>(d.P) * d.R;
+    if (d_init && d_init == d_final) {  // one scan writes what others of its launch read
+        SSD_HIP(ssd::launch_copy_or_zero(f.d_final, d_final, static_cast<int64_t>(d.B) * d.H * size, st), "copy d_final");
+        d_final = f.d_final;
+    }
     // what all of them share, and the states in the forward's order: columns p, rows r
     ssd::LinearJob fwd{}, rev{};
     fwd.init = init;
@@ -1455,21 +1460,15 @@ int ssd_linear_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fi
     dv.in = d.scale;
     dv.qdiv = dv.kdiv = grp;
     // d_q and d_k: rows of the state are p, its columns r
-    ssd::LinearShape t = s;
-    t.P = d.R;
-    t.R = d.P;
-    ssd::LinearJobs two{};
-    two.n = 2;
-    two.job[0] = fwd;
-    two.job[1] = rev;
-    for (ssd::LinearJob& j : two.job) {
-        j.csc = 1;
-        j.csr = d.R;
-        j.vdiv = grp;
-        j.wide = grp > 1;
-        dense_strides(j.os, d, d.H, d.R);
+    ssd::LinearGrads all{tan, fwd, rev, dv};
+    ssd::LinearJob &dq = all.q, &dk = all.k;
+    for (ssd::LinearJob* j : {&dq, &dk}) {
+        j->csc = 1;
+        j->csr = d.R;
+        j->vdiv = grp;
+        j->wide = grp > 1;
+        dense_strides(j->os, d, d.H, d.R);
     }
-    ssd::LinearJob &dq = two.job[0], &dk = two.job[1];
     dq.q = dy;
     dq.k = v;
     dq.v = k;
@@ -1486,33 +1485,24 @@ int ssd_linear_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fi
     dense_strides(dk.ks, d, d.H, d.P);
     set_strides(dk.vs, d.qs);
     dk.in = d.scale;
-    ssd::LinearJobs one{};
-    one.n = 1;
     if (s.segs > 1) {
-        ssd::LinearJobs both{};
-        both.n = 2;
-        both.job[0] = tan;
-        both.job[1] = dv;
+        ssd::LinearJobs states{};
         if (d_decay) {
-            one.job[0] = tan;
-            SSD_HIP(ssd::launch_linear_carry(s, one, true, st), "k_linear_carry");
-            SSD_HIP(ssd::launch_linear_join(s, one, true, st), "k_linear_join");
-            one.job[0] = dv;
-            SSD_HIP(ssd::launch_linear_carry(s, one, false, st), "k_linear_carry");
-            SSD_HIP(ssd::launch_linear_join(s, one, false, st), "k_linear_join");
+            states.n = 1;
+            states.job[0] = tan;
+            SSD_HIP(ssd::launch_linear_carry(s, states, true, st), "k_linear_carry");
+            SSD_HIP(ssd::launch_linear_join(s, states, true, st), "k_linear_join");
+            states.job[0] = dv;
         } else {
-            SSD_HIP(ssd::launch_linear_carry(s, both, false, st), "k_linear_carry");
-            SSD_HIP(ssd::launch_linear_join(s, both, false, st), "k_linear_join");
+            states.n = 2;
+            states.job[0] = tan;
+            states.job[1] = dv;
         }
+        SSD_HIP(ssd::launch_linear_carry(s, states, false, st), "k_linear_carry");
+        SSD_HIP(ssd::launch_linear_join(s, states, false, st), "k_linear_join");
     }
-    if (d_decay) {  // before d_init, which may lie in d_final's place
-        one.job[0] = tan;
-        SSD_HIP(ssd::launch_linear_tangent(s, one, st), "k_linear_tangent");
-        SSD_HIP(ssd::launch_linear_decay(s, f.dots, d_decay, st), "k_linear_decay");
-    }
-    SSD_HIP(ssd::launch_linear_scan(t, two, st), "k_linear");
-    one.job[0] = dv;
-    SSD_HIP(ssd::launch_linear_scan(s, one, st), "k_linear");
+    SSD_HIP(ssd::launch_linear_grad(s, all, d_decay != nullptr, st), "k_linear_grad");
+    if (d_decay) SSD_HIP(ssd::launch_linear_decay(s, f.dots, d_decay, st), "k_linear_decay");
     if (grp > 1) {
         SSD_HIP(ssd::launch_linear_share(s, d.HK, d.R, f.dq, d_q, st), "k_linear_share");
         SSD_HIP(ssd::launch_linear_share(s, d.HK, d.R, f.dk, d_k, st), "k_linear_share");

@@ -338,7 +338,7 @@ hipError_t launch_delta_step(const DeltaShape& d, int nslots, const void* q, con
 struct LinearShape {
     int B, S, H, P, R;  // batch, tokens, heads, widths of the values and of the keys
     int io;             // 0 = fp32, 1 = bf16
-    int N;              // chunks of linear_chunk(io) tokens
+    int N;              // chunks of kLinearChunk tokens
     int segs, seg_chunks;  // segments of the chunk axis, and their chunks
     const int64_t* len;    // device, null: all S
     const float* log_decay;
@@ -363,16 +363,21 @@ struct LinearJobs {
     unsigned n;
     LinearJob job[2];
 };
-int linear_chunk(int io);
+// The scans of a gradient; all read by the forward's names in d.
+struct LinearGrads {
+    LinearJob decay, q, k, v;
+};
+constexpr int kLinearChunk = 32;
 // Segments of the chunk axis to run side by side (1: it runs through).
-int linear_segments(const LinearShape& d, int jobs);
+int linear_segments(const LinearShape& d, bool bwd);
+int linear_grad_blocks(const LinearShape& d);  // workgroups of a head's segment in launch_linear_grad, without the decay's
 // Outputs and final states; what each segment but the last adds to a state (and to its tangent); the
-// states the segments start from; the derivative along the decay, dotted with dst.
+// states the segments start from; the gradients.
 hipError_t launch_linear_scan(const LinearShape& d, const LinearJobs& jobs, hipStream_t st);
 hipError_t launch_linear_carry(const LinearShape& d, const LinearJobs& jobs, bool tangent, hipStream_t st);
 hipError_t launch_linear_join(const LinearShape& d, const LinearJobs& jobs, bool tangent, hipStream_t st);
-hipError_t launch_linear_tangent(const LinearShape& d, const LinearJobs& jobs, hipStream_t st);
-// Sums per head that launch_linear_tangent leaves, and their total.
+hipError_t launch_linear_grad(const LinearShape& d, const LinearGrads& g, bool decay, hipStream_t st);
+// Sums per head that the decay's scan leaves, and their total.
 int linear_dots(const LinearShape& d);
 hipError_t launch_linear_decay(const LinearShape& d, const double* dots, float* d_decay, hipStream_t st);
 // dst [b, s, kheads, r] = src [b, s, h, r] fp32 summed over the heads that share one.

@@ -78,3 +78,38 @@ def test_ragged_rows_and_shared_key_heads(io, hk, h):
         for x in (y, g["d_q"], g["d_k"], g["d_v"]):
             assert not x[row, n:].any()
     assert torch.equal(final[1], d["init"][1]) and torch.equal(g["d_init"][1], d["d_final"][1])
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("p,r", [(64, 128), (128, 64), (32, 16)])
+def test_in_place(io, p, r):
+    """final_state in init's place and d_init in d_final's, long enough to run in segments too."""
+    for s in (70, 700):
+        t = ref.linear_inputs(2, s, 1, 2, p, r, seed=s + p, dtype=io)
+        d = on_gpu(t)
+        lens = torch.tensor([s, s - 37], dtype=torch.int64)
+        y, final = ssd.linear_attention(*(d[k] for k in LEAVES), init=d["init"], valid_len=lens)
+        g = ssd.linear_attention_bwd(d["dy"], *(d[k] for k in LEAVES), init=d["init"], d_final=d["d_final"],
+                                     valid_len=lens)
+        state, y2 = d["init"].clone(), torch.empty_like(y)
+        ws = ssd.linear_workspace(d["q"], d["k"], d["v"], False)
+        assert ssd.ssd_linear_fwd(*(d[k] for k in LEAVES), state, lens, y2, state, ws) == 0
+        assert torch.equal(y, y2) and torch.equal(final, state)
+        d_state, out = d["d_final"].clone(), {k: torch.empty_like(g[k]) for k in ("d_q", "d_k", "d_v", "d_decay")}
+        ws = ssd.linear_workspace(d["q"], d["k"], d["v"], True)
+        assert ssd.ssd_linear_bwd(d["dy"], d_state, *(d[k] for k in LEAVES), d["init"], lens, out["d_q"], out["d_k"],
+                                  out["d_v"], out["d_decay"], d_state, ws) == 0
+        out["d_init"] = d_state
+        for k in g:
+            assert torch.equal(out[k], g[k]), k
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("s,h,hk", [(1100, 2, 1), (2500, 1, 1), (600, 3, 3)])
+def test_segments(io, s, h, hk):
+    """Few heads: the chunks run in segments side by side, rows ending in any of them; slow decays."""
+    t = ref.linear_inputs(3, s, hk, h, 32, 64, seed=s, dtype=io, slowest=-14.0)
+    d = on_gpu(t)
+    lens = [s, s // 2 + 5, 3]
+    forward(t, d, lens)
+    backward(t, d, lens)
