@@ -95,13 +95,26 @@ hipError_t run(const LinearShape& d, const LinearJobs& jobs, hipStream_t st) {
 
 }  // namespace
 
-int linear_segments(const LinearShape& d, bool bwd) {
-    const int64_t wgs = static_cast<int64_t>(d.B) * d.H * (bwd ? linear_grad_blocks(d) : 1);
-    if (d.N < 16 || wgs > 256) return 1;
+// As many segments as give the chip's 512 places (two workgroups a CU) a workgroup each, of at least two
+// chunks.  Whole where heads alone take more than half the places, or where the chunks that a workgroup is
+// spared (2 us each in bf16 and 3.5 in fp32 with r = 128, half of that with narrow keys) do not pay for
+// carrying (half as long a chunk) and for two more launches.  Measured in 1 to 32 segments: bf16, p = 64,
+// r = 128, 160 heads of 4096 tokens 268 us whole, 202 in three, 221 in five; 96 of 1531 107 whole, 66 in five;
+// 32 of 8192 523 whole, 98 in sixteen; fp32 8 of 1024 125 whole, 35 in sixteen.
+// A gradient with the decay's fills the places unevenly: where it takes one to three rounds of them, four
+// segments even that out (fp32, 96 heads of 2048 tokens, 650 -> 594 us; bf16, 160 of 4096, 928 -> 856).
+int linear_segments(const LinearShape& d, bool bwd, bool decay) {
+    const int64_t heads = static_cast<int64_t>(d.B) * d.H, each = bwd ? linear_grad_blocks(d, decay) : linear_blocks(d);
+    const int64_t wgs = heads * each;
+    if (wgs == 0) return 1;
+    if (wgs > 256) return bwd && decay && wgs > 512 && wgs <= 1536 && d.N >= 32 ? 4 : 1;
     int64_t n = 512 / wgs;
-    if (n > d.N / 8) n = d.N / 8;
-    return n < 2 ? 1 : static_cast<int>(n);
+    if (n > d.N / 2) n = d.N / 2;
+    if (n < 2) return 1;
+    const double chunk = (d.io == 1 ? 1.0 : 1.75) * (1.0 + d.R / 128.0), left = static_cast<double>((d.N + n - 1) / n);
+    return chunk * d.N < 1.5 * chunk * left + 15.0 ? 1 : static_cast<int>(n);
 }
+int linear_blocks(const LinearShape& d) { return d.P == 128 && d.io == 0 ? 2 : 1; }
 
 hipError_t launch_linear_scan(const LinearShape& d, const LinearJobs& jobs, hipStream_t st) {
     return run<kOutputs>(d, jobs, st);

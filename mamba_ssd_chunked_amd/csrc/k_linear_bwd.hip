@@ -73,9 +73,9 @@ hipError_t grad(const LinearShape& d, const LinearGrads& g, hipStream_t st) {
 
 }  // namespace
 
-int linear_grad_blocks(const LinearShape& d) {
+int linear_grad_blocks(const LinearShape& d, bool decay) {
     auto of = [&](int width) { return blocks(width, d.io == 1 && width == 128 ? 2 : 1); };
-    return 2 * of(d.R) + of(d.P);
+    return 2 * of(d.R) + of(d.P) + (decay ? blocks(d.P, 1) : 0);
 }
 
 hipError_t launch_linear_grad(const LinearShape& d, const LinearGrads& g, bool decay, hipStream_t st) {

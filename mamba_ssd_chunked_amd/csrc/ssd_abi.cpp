@@ -508,10 +508,10 @@ int validate_linear(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape
     return validate_heads(who, dims, d, [](const ssd_delta_dims&) { return 512.0; });
 }
 
-ssd::LinearShape linear_shape(const ssd::DeltaShape& d, const float* log_decay, bool bwd) {
+ssd::LinearShape linear_shape(const ssd::DeltaShape& d, const float* log_decay, bool bwd, bool decay) {
     const int c = ssd::kLinearChunk;
     ssd::LinearShape s{d.B, d.S, d.H, d.P, d.R, d.io, (d.S + c - 1) / c, 1, 0, nullptr, log_decay};
-    s.segs = ssd::linear_segments(s, bwd);
+    s.segs = ssd::linear_segments(s, bwd, decay);
     s.seg_chunks = (s.N + s.segs - 1) / s.segs;
     return s;
 }
@@ -1322,7 +1322,8 @@ int ssd_linear_workspace_size(const ssd_delta_dims* dims, int bwd, size_t* bytes
     if (int rc = validate_linear("ssd_linear_workspace_size", dims, &d)) return rc;
     if (!bytes) return fail(SSD_ERR_NULL, "ssd_linear_workspace_size: bytes is NULL");
     LinearBufs f{};
-    *bytes = linear_plan(d, linear_shape(d, nullptr, bwd != 0), bwd != 0, nullptr, &f);
+    *bytes = linear_plan(d, linear_shape(d, nullptr, bwd != 0, false), bwd != 0, nullptr, &f);
+    if (bwd) *bytes = std::max(*bytes, linear_plan(d, linear_shape(d, nullptr, true, true), true, nullptr, &f));
     return ok();
 }
 
@@ -1339,7 +1340,7 @@ int ssd_linear_fwd(const ssd_delta_dims* dims, const void* q, const void* k, con
     if (overlap_unequal(init, final_state, (size_t)d.B * d.H * d.P * d.R))
         return fail(SSD_ERR_UNSUPPORTED, "%s: init and final_state overlap without being equal", who);
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
-    ssd::LinearShape s = linear_shape(d, log_decay, false);
+    ssd::LinearShape s = linear_shape(d, log_decay, false, false);
     LinearBufs f{};
     const size_t need = linear_plan(d, s, false, ws, &f);
     if (tok)
@@ -1398,7 +1399,7 @@ int ssd_linear_bwd(const ssd_delta_dims* dims, const void* dy, const float* d_fi
     if (overlap_unequal(d_final, d_init, (size_t)d.B * d.H * d.P * d.R))
         return fail(SSD_ERR_UNSUPPORTED, "%s: d_final and d_init overlap without being equal", who);
     if (int rc = check_delta_lens(who, d, valid_len)) return rc;
-    ssd::LinearShape s = linear_shape(d, log_decay, true);
+    ssd::LinearShape s = linear_shape(d, log_decay, true, d_decay != nullptr);
     LinearBufs f{};
     const size_t need = linear_plan(d, s, true, ws, &f);
     if (tok)

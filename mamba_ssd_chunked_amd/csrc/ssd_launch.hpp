@@ -369,8 +369,10 @@ struct LinearGrads {
 };
 constexpr int kLinearChunk = 32;
 // Segments of the chunk axis to run side by side (1: it runs through).
-int linear_segments(const LinearShape& d, bool bwd);
-int linear_grad_blocks(const LinearShape& d);  // workgroups of a head's segment in launch_linear_grad, without the decay's
+int linear_segments(const LinearShape& d, bool bwd, bool decay);
+// Workgroups of a head's segment in launch_linear_scan and in launch_linear_grad.
+int linear_blocks(const LinearShape& d);
+int linear_grad_blocks(const LinearShape& d, bool decay);
 // Outputs and final states; what each segment but the last adds to a state (and to its tangent); the
 // states the segments start from; the gradients.
 hipError_t launch_linear_scan(const LinearShape& d, const LinearJobs& jobs, hipStream_t st);

@@ -632,30 +632,37 @@ def ssd_linear_workspace_size(dims: ssd_delta_dims, bwd: bool) -> int:
                         dims.headdim, dims.dstate, dims.io_dtype, int(bool(bwd)))
 
 
+def _linear_leaves(d, at, v, state, log_decay, init, valid_len):
+    """Addresses of what both directions read besides q, k and v."""
+    f = torch.float32
+    return (_address(log_decay, "log_decay", f, v.shape[-2:-1], at), _address(init, "init", f, state, at, False),
+            _host_lengths(valid_len, d.batch))
+
+
 def ssd_linear_fwd(q, k, v, log_decay, init, valid_len, y, final_state, ws, scale=None, stream=None) -> int:
     """q, k ``[b, s, hk, r]``, v ``[b, s, h, p]`` (last axis contiguous), log_decay ``[h]``; scale None is
     ``1 / sqrt(r)``."""
     d, qkv, at = _delta_args(q, k, v, scale)
     f, (_, state) = torch.float32, _delta_shapes(q, v)
-    args = (_address(log_decay, "log_decay", f, v.shape[-2:-1], at),
-            _address(init, "init", f, state, at, False), _host_lengths(valid_len, d.batch),
-            _address(y, "y", q.dtype, v.shape, at), _address(final_state, "final_state", f, state, at, False))
+    leaves = _linear_leaves(d, at, v, state, log_decay, init, valid_len)
     wp, wb = _workspace(ws, at)
-    return _launch(load_library().ssd_linear_fwd, at, ctypes.byref(d), *qkv, *args, wp, wb, _raw_stream(stream, at))
+    return _launch(load_library().ssd_linear_fwd, at, ctypes.byref(d), *qkv, *leaves,
+                   _address(y, "y", q.dtype, v.shape, at),
+                   _address(final_state, "final_state", f, state, at, False), wp, wb, _raw_stream(stream, at))
 
 
 def ssd_linear_bwd(dy, d_final, q, k, v, log_decay, init, valid_len, d_q, d_k, d_v, d_decay, d_init, ws,
                    scale=None, stream=None) -> int:
     d, qkv, at = _delta_args(q, k, v, scale)
-    f, (_, state), io, h = torch.float32, _delta_shapes(q, v), q.dtype, v.shape[-2:-1]
-    args = (_address(log_decay, "log_decay", f, h, at),
-            _address(init, "init", f, state, at, False), _host_lengths(valid_len, d.batch),
-            _address(d_q, "d_q", io, q.shape, at), _address(d_k, "d_k", io, q.shape, at),
-            _address(d_v, "d_v", io, v.shape, at), _address(d_decay, "d_decay", f, h, at, False),
-            _address(d_init, "d_init", f, state, at, False))
+    f, (_, state), io = torch.float32, _delta_shapes(q, v), q.dtype
+    leaves = _linear_leaves(d, at, v, state, log_decay, init, valid_len)
+    out = (_address(d_q, "d_q", io, q.shape, at), _address(d_k, "d_k", io, q.shape, at),
+           _address(d_v, "d_v", io, v.shape, at), _address(d_decay, "d_decay", f, v.shape[-2:-1], at, False),
+           _address(d_init, "d_init", f, state, at, False))
     wp, wb = _workspace(ws, at)
     return _launch(load_library().ssd_linear_bwd, at, ctypes.byref(d), _address(dy, "dy", io, v.shape, at),
-                   _address(d_final, "d_final", f, state, at, False), *qkv, *args, wp, wb, _raw_stream(stream, at))
+                   _address(d_final, "d_final", f, state, at, False), *qkv, *leaves, *out, wp, wb,
+                   _raw_stream(stream, at))
 
 
 def ssd_linear_step(q, k, v, log_decay, state, slots, y, scale=None, stream=None) -> int:
@@ -734,15 +741,16 @@ def _rows(t: torch.Tensor, name: str, dtype, shape, at: int):
 
 def _group_norm_args(x, groups, eps, act, gate):
     """(dims, addresses of x and gate, x's device) for x ``[n, ..., channels]``."""
-    if x.dim() < 2:
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("x must be [n, ..., channels]")
     if act not in _ACT:
         raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
     tag, at = _io_of(x, "x"), _device_of(x, "x")
-    px, sx = _rows(x, "x", x.dtype, x.shape, at)
-    pg, sg = (None, 0) if gate is None else _rows(gate, "gate", x.dtype, x.shape, at)
-    n, *positions, c = x.shape
-    return ssd_group_norm_dims(n, math.prod(positions), c, groups, sx, sg, eps, _ACT[act], tag), px, pg, at
+    px, sx = _rows(x, "x", x.dtype, shape, at)
+    pg, sg = (None, 0) if gate is None else _rows(gate, "gate", x.dtype, shape, at)
+    return (ssd_group_norm_dims(shape[0], math.prod(shape[1:-1]), shape[-1], groups, sx, sg, eps, _ACT[act], tag),
+            px, pg, at)
 
 
 @functools.lru_cache(maxsize=256)
@@ -765,14 +773,17 @@ def _group_stats(x, groups):
     return x.shape[0], groups, 2
 
 
+def _affine(weight, bias, x, at):
+    f, c = torch.float32, x.shape[-1:]
+    return _address(weight, "weight", f, c, at, False), _address(bias, "bias", f, c, at, False)
+
+
 def ssd_group_norm(x, groups, weight, bias, eps, act, gate, y, stats, ws, stream=None) -> int:
     """x, gate ``[n, ..., channels]`` (positions evenly spaced), y like x (contiguous), weight, bias fp32
     ``[channels]`` or None, stats fp32 ``[n, groups, 2]``; act "none" or "silu"."""
     d, px, pg, at = _group_norm_args(x, groups, eps, act, gate)
-    f, c = torch.float32, x.shape[-1:]
-    args = (px, _address(weight, "weight", f, c, at, False), _address(bias, "bias", f, c, at, False), pg,
-            _address(y, "y", x.dtype, x.shape, at, False),
-            _address(stats, "stats", f, _group_stats(x, groups), at, False))
+    args = (px, *_affine(weight, bias, x, at), pg, _address(y, "y", x.dtype, x.shape, at, False),
+            _address(stats, "stats", torch.float32, _group_stats(x, groups), at, False))
     wp, wb = _workspace(ws, at)
     return _launch(load_library().ssd_group_norm, at, ctypes.byref(d), *args, wp, wb, _raw_stream(stream, at))
 
@@ -781,8 +792,7 @@ def ssd_group_norm_bwd(dy, x, groups, weight, bias, eps, act, gate, stats, d_x, 
                        stream=None) -> int:
     d, px, pg, at = _group_norm_args(x, groups, eps, act, gate)
     f, c, io = torch.float32, x.shape[-1:], x.dtype
-    args = (_address(dy, "dy", io, x.shape, at), px, _address(weight, "weight", f, c, at, False),
-            _address(bias, "bias", f, c, at, False), pg,
+    args = (_address(dy, "dy", io, x.shape, at), px, *_affine(weight, bias, x, at), pg,
             _address(stats, "stats", f, _group_stats(x, groups), at), _address(d_x, "d_x", io, x.shape, at),
             _address(d_weight, "d_weight", f, c, at, False), _address(d_bias, "d_bias", f, c, at, False),
             _address(d_gate, "d_gate", io, x.shape, at, False))
@@ -802,6 +812,15 @@ def _allocating_on(stream, like: torch.Tensor):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     return torch.cuda.stream(stream)
+
+
+def _own_workspace(ws, at, like, size):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one of size() bytes."""
+    if ws is None:
+        n = max(size(), 256)
+        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+        return ws.data_ptr(), n, ws
+    return (*_workspace(ws, at), ws)
 
 
 def _check(rc: int, where: str):
@@ -1036,12 +1055,16 @@ def linear_attention(q, k, v, log_decay, init=None, valid_len=None, scale=None, 
     if q.dim() != 4:
         raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
     with _allocating_on(stream, q):
+        # (what is made here needs no looking over)
+        d, qkv, at = _delta_args(q, k, v, scale)
+        state = _delta_shapes(q, v)[1]
+        valid_len = _lengths(valid_len)  # (a list's tensor has to outlive the call)
+        leaves = _linear_leaves(d, at, v, state, log_decay, init, valid_len)
         y = v.new_empty(v.shape)
-        final = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), dtype=torch.float32,
-                            device=q.device) if want_final else None
-        ws = linear_workspace(q, k, v, False) if ws is None else ws
-        _check(ssd_linear_fwd(q, k, v, log_decay, init, _lengths(valid_len), y, final, ws, scale, stream),
-               "ssd_linear_fwd")
+        final = torch.empty(state, dtype=torch.float32, device=q.device) if want_final else None
+        wp, wb, ws = _own_workspace(ws, at, q, lambda: ssd_linear_workspace_size(d, False))
+        _check(_launch(load_library().ssd_linear_fwd, at, ctypes.byref(d), *qkv, *leaves, y.data_ptr(),
+                       None if final is None else final.data_ptr(), wp, wb, _raw_stream(stream, at)), "ssd_linear_fwd")
     return y, final
 
 
@@ -1053,14 +1076,18 @@ def linear_attention_bwd(dy, q, k, v, log_decay, init=None, d_final=None, valid_
     if q.dim() != 4:
         raise ValueError("q and k must be [b, s, hk, r] and v [b, s, h, p]")
     with _allocating_on(stream, q):
-        new = lambda t: t.new_empty(t.shape)  # noqa: E731
-        out = dict(d_q=new(q), d_k=new(k), d_v=new(v), d_decay=new(log_decay) if want_d_decay else None,
-                   d_init=torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]),
-                                      dtype=torch.float32, device=q.device) if want_d_init else None)
-        ws = linear_workspace(q, k, v, True) if ws is None else ws
-        _check(ssd_linear_bwd(dy, d_final, q, k, v, log_decay, init, _lengths(valid_len), out["d_q"],
-                              out["d_k"], out["d_v"], out["d_decay"], out["d_init"], ws, scale, stream),
-               "ssd_linear_bwd")
+        d, qkv, at = _delta_args(q, k, v, scale)
+        state, f = _delta_shapes(q, v)[1], torch.float32
+        valid_len = _lengths(valid_len)  # (a list's tensor has to outlive the call)
+        leaves = _linear_leaves(d, at, v, state, log_decay, init, valid_len)
+        grads = _address(dy, "dy", q.dtype, v.shape, at), _address(d_final, "d_final", f, state, at, False)
+        out = dict(d_q=q.new_empty(q.shape), d_k=k.new_empty(k.shape), d_v=v.new_empty(v.shape),
+                   d_decay=log_decay.new_empty(v.shape[-2:-1]) if want_d_decay else None,
+                   d_init=torch.empty(state, dtype=f, device=q.device) if want_d_init else None)
+        wp, wb, ws = _own_workspace(ws, at, q, lambda: ssd_linear_workspace_size(d, True))
+        _check(_launch(load_library().ssd_linear_bwd, at, ctypes.byref(d), *grads, *qkv, *leaves,
+                       *(None if t is None else t.data_ptr() for t in out.values()), wp, wb,
+                       _raw_stream(stream, at)), "ssd_linear_bwd")
     return out
 
 
@@ -1129,10 +1156,14 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act="none", gate=Non
     slices of wider rows.  Returns a dict of ``y`` (like x, contiguous) and, where wanted, ``stats`` (fp32
     ``[n, groups, 2]``, the mean and 1 / sqrt(var + eps)), which group_norm_bwd takes."""
     with _allocating_on(stream, x):
+        d, px, pg, at = _group_norm_args(x, groups, eps, act, gate)
+        affine = _affine(weight, bias, x, at)
         y = x.new_empty(x.shape) if want_y else None
         stats = torch.empty(_group_stats(x, groups), dtype=torch.float32, device=x.device) if want_stats else None
-        ws = group_norm_workspace(x, groups, gate) if ws is None else ws
-        _check(ssd_group_norm(x, groups, weight, bias, eps, act, gate, y, stats, ws, stream), "ssd_group_norm")
+        wp, wb, ws = _own_workspace(ws, at, x, lambda: ssd_group_norm_workspace_size(d, False))
+        _check(_launch(load_library().ssd_group_norm, at, ctypes.byref(d), px, *affine, pg,
+                       None if y is None else y.data_ptr(), None if stats is None else stats.data_ptr(), wp, wb,
+                       _raw_stream(stream, at)), "ssd_group_norm")
     return {k: t for k, t in (("y", y), ("stats", stats)) if t is not None}
 
 
@@ -1144,12 +1175,15 @@ def group_norm_bwd(dy, x, groups, weight=None, bias=None, eps=1e-5, act="none", 
     with _allocating_on(stream, x):
         if stats is None:
             stats = group_norm(x, groups, eps=eps, want_y=False, want_stats=True, stream=stream)["stats"]
-        c = x.shape[-1:]
-        d_weight, d_bias = (torch.empty(c, dtype=torch.float32, device=x.device) if want_weights else None
-                            for _ in range(2))
+        d, px, pg, at = _group_norm_args(x, groups, eps, act, gate)
+        f, c, io = torch.float32, x.shape[-1:], x.dtype
+        args = (_address(dy, "dy", io, x.shape, at), px, *_affine(weight, bias, x, at), pg,
+                _address(stats, "stats", f, _group_stats(x, groups), at))
+        d_weight, d_bias = (torch.empty(c, dtype=f, device=x.device) if want_weights else None for _ in range(2))
         out = dict(d_x=x.new_empty(x.shape), d_weight=d_weight, d_bias=d_bias,
                    d_gate=None if gate is None else x.new_empty(x.shape))
-        ws = group_norm_workspace(x, groups, gate, True) if ws is None else ws
-        _check(ssd_group_norm_bwd(dy, x, groups, weight, bias, eps, act, gate, stats, out["d_x"], d_weight, d_bias,
-                                  out["d_gate"], ws, stream), "ssd_group_norm_bwd")
+        wp, wb, ws = _own_workspace(ws, at, x, lambda: ssd_group_norm_workspace_size(d, True))
+        _check(_launch(load_library().ssd_group_norm_bwd, at, ctypes.byref(d), *args,
+                       *(None if t is None else t.data_ptr() for t in out.values()), wp, wb,
+                       _raw_stream(stream, at)), "ssd_group_norm_bwd")
     return out
