@@ -603,6 +603,8 @@ __global__ __launch_bounds__(256) void k_group_norm_means(GroupShape d, const fl
     }
 }
 
+// d_x and d_gate of the pieces; the first workgroups have d_weight and d_bias [c], 32 channels each, the sums
+// over samples of chan.
 template <class IO, int EV>
 __global__ __launch_bounds__(256) void k_group_norm_grad(GroupShape d, const typename IO::T* __restrict__ dy,
                                                          const typename IO::T* __restrict__ x,
@@ -612,10 +614,27 @@ __global__ __launch_bounds__(256) void k_group_norm_grad(GroupShape d, const typ
                                                          const float* __restrict__ stats,
                                                          const float2* __restrict__ mean,
                                                          typename IO::T* __restrict__ d_x,
-                                                         typename IO::T* __restrict__ d_gate) {
+                                                         typename IO::T* __restrict__ d_gate,
+                                                         const float* __restrict__ chan, int sums,
+                                                         float* __restrict__ d_weight, float* __restrict__ d_bias) {
+    __shared__ float sh[8][33];
     const Act act{d.act, gate != nullptr};
+    if (static_cast<int>(blockIdx.x) < sums) {
+        const int l = threadIdx.x & 31, run = threadIdx.x >> 5, which = blockIdx.x & 1, col = (blockIdx.x >> 1) * 32 + l;
+        float* to = which ? d_bias : d_weight;
+        float acc = 0.0f;
+        if (col < d.c)
+            for (int64_t n = run; n < d.n; n += 8) acc += chan[(2 * n + which) * d.c + col];
+        sh[run][l] = acc;
+        __syncthreads();
+        if (run == 0 && col < d.c && to) {
+            for (int m = 1; m < 8; ++m) acc += sh[m][l];
+            to[col] = acc;
+        }
+        return;
+    }
     const int64_t items = d.n * d.outs.blocks * d.outs.slabs;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    for (int64_t item = blockIdx.x - sums; item < items; item += gridDim.x - sums) {
         const Piece<EV> p(d, d.outs, item);
         if (!p.on) continue;
         const int ch = p.channel();
@@ -881,14 +900,17 @@ hipError_t launch_group_norm_means(const GroupShape& d, const float* part, const
 
 hipError_t launch_group_norm_grad(const GroupShape& d, const void* dy, const void* x, const float* weight,
                                   const float* bias, const void* gate, const float* stats, const float* mean,
-                                  void* d_x, void* d_gate, hipStream_t st) {
+                                  void* d_x, void* d_gate, const float* chan, float* d_weight, float* d_bias,
+                                  hipStream_t st) {
+    const int sums = d_weight || d_bias ? 2 * ((d.c + 31) / 32) : 0;
     return by_io(d, [&](auto io_) {
         using IO = decltype(io_);
         using T = typename IO::T;
         return by_vector<IO>(d, [&](auto ev) {
-            k_group_norm_grad<IO, decltype(ev)::value><<<grid_of(d.n * d.outs.blocks * d.outs.slabs), 256, 0, st>>>(
+            k_group_norm_grad<IO, decltype(ev)::value><<<sums + grid_of(d.n * d.outs.blocks * d.outs.slabs), 256, 0, st>>>(
                 d, static_cast<const T*>(dy), static_cast<const T*>(x), weight, bias, static_cast<const T*>(gate),
-                stats, reinterpret_cast<const float2*>(mean), static_cast<T*>(d_x), static_cast<T*>(d_gate));
+                stats, reinterpret_cast<const float2*>(mean), static_cast<T*>(d_x), static_cast<T*>(d_gate), chan, sums,
+                d_weight, d_bias);
             return hipGetLastError();
         });
     });

@@ -1649,19 +1649,20 @@ int ssd_group_norm_bwd(const ssd_group_norm_dims* dims, const void* dy, const vo
         if (d_bias) SSD_HIP(ssd::launch_copy_or_zero(d_bias, nullptr, d.c, st), "zero d_bias");
         return ok();
     }
-    const float* sums = d.tokens ? f.part : f.chan;
-    const int64_t parts = d.tokens ? static_cast<int64_t>(d.sums.blocks) * d.sums.lanes : d.n;
     if (d.tokens) {
         SSD_HIP(ssd::launch_group_norm_rows_bwd(d, dy, x, weight, bias, gate, stats, d_x, d_gate, f.part, st),
                 "k_group_norm_rows_bwd");
-    } else {
-        SSD_HIP(ssd::launch_group_norm_sums(d, dy, x, weight, bias, gate, stats, f.part, st), "k_group_norm_sums");
-        SSD_HIP(ssd::launch_group_norm_means(d, f.part, weight, f.chan, f.mean, st), "k_group_norm_means");
-        SSD_HIP(ssd::launch_group_norm_grad(d, dy, x, weight, bias, gate, stats, f.mean, d_x, d_gate, st),
-                "k_group_norm_grad");
+        if (d_weight || d_bias)
+            SSD_HIP(ssd::launch_group_norm_weight(d, f.part, static_cast<int64_t>(d.sums.blocks) * d.sums.lanes, d_weight,
+                                                  d_bias, st),
+                    "k_group_norm_weight");
+        return ok();
     }
-    if (d_weight || d_bias)
-        SSD_HIP(ssd::launch_group_norm_weight(d, sums, parts, d_weight, d_bias, st), "k_group_norm_weight");
+    SSD_HIP(ssd::launch_group_norm_sums(d, dy, x, weight, bias, gate, stats, f.part, st), "k_group_norm_sums");
+    SSD_HIP(ssd::launch_group_norm_means(d, f.part, weight, f.chan, f.mean, st), "k_group_norm_means");
+    SSD_HIP(ssd::launch_group_norm_grad(d, dy, x, weight, bias, gate, stats, f.mean, d_x, d_gate, f.chan, d_weight, d_bias,
+                                        st),
+            "k_group_norm_grad");
     return ok();
 }
 

@@ -434,7 +434,7 @@ hipError_t launch_group_norm_join(const GroupShape& d, const float* rec, float* 
 hipError_t launch_group_norm_apply(const GroupShape& d, const void* x, const float* weight, const float* bias,
                                    const void* gate, const float* stats, void* y, hipStream_t st);
 // tokens: d_x, d_gate and part [blocks * lanes, 2, c] for launch_group_norm_weight; otherwise channel sums of
-// the blocks, their totals chan [n, 2, c] (also for it) and the groups' means, then d_x and d_gate
+// the blocks, their totals chan [n, 2, c] and the groups' means, then all gradients
 hipError_t launch_group_norm_rows_bwd(const GroupShape& d, const void* dy, const void* x, const float* weight,
                                       const float* bias, const void* gate, const float* stats, void* d_x,
                                       void* d_gate, float* part, hipStream_t st);
@@ -445,7 +445,8 @@ hipError_t launch_group_norm_means(const GroupShape& d, const float* part, const
                                    float* mean, hipStream_t st);
 hipError_t launch_group_norm_grad(const GroupShape& d, const void* dy, const void* x, const float* weight,
                                   const float* bias, const void* gate, const float* stats, const float* mean,
-                                  void* d_x, void* d_gate, hipStream_t st);
+                                  void* d_x, void* d_gate, const float* chan, float* d_weight, float* d_bias,
+                                  hipStream_t st);
 hipError_t launch_group_norm_weight(const GroupShape& d, const float* part, int64_t parts, float* d_weight,
                                     float* d_bias, hipStream_t st);
 
