@@ -413,10 +413,12 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
  * gradients of exactly zero.
  * bf16 io: the products take the bf16 inputs as they are and everything else (states, decays, the
  * causal matrix, sums) to 24 bits; y, d_q, d_k, d_v are rounded to nearest even.  Results are bitwise
- * reproducible.  A NaN or an infinity among a row's tokens spreads over its chunk of 64 tokens and on
- * from there (in the gradients of keys and values: back from there), in that head (and d_q, d_k of its
- * key head, d_decay of the head) only, but to no token past the row's length.
- * 512 * batch * nheads < 2^32 (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
+ * reproducible.  A NaN or an infinity among a row's tokens spreads over its chunk of 32 tokens and on
+ * from there (in the gradients of keys and values, whose chunks are counted from the row's end: back
+ * from there), in that head (and d_q, d_k of its key head, d_decay of the head) only, but to no token
+ * past the row's length.  A positive log_decay is taken as it is; its state has to stay finite.
+ * 2048 * batch * nheads < 2^32, and with more than one token at most 2^24 elements from a token to the
+ * next in every operand (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,
  * SSD_ERR_HIP.
  */
@@ -521,7 +523,8 @@ typedef struct ssd_group_norm_dims {
 /* Workspace bytes (256-byte aligned buffer) of ssd_group_norm (bwd == 0) or ssd_group_norm_bwd; may be 0. */
 int ssd_group_norm_workspace_size(const ssd_group_norm_dims* dims, int bwd, size_t* bytes);
 
-/* y and stats are nullable, one of them is required (y NULL: gate, weight and bias are not read). */
+/* y and stats are nullable, one of them is required (y NULL: gate, weight and bias are not read).  Outputs
+ * overlap no input. */
 int ssd_group_norm(const ssd_group_norm_dims* dims, const void* x, const float* weight,
                    const float* bias, const void* gate, void* y, float* stats, void* ws,
                    size_t ws_bytes, void* stream);

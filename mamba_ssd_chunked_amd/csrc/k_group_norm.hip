@@ -84,10 +84,10 @@ __device__ __forceinline__ void ld_chan(const float* p, int64_t at, float none, 
 // channels bf16 53 us.)
 __device__ __forceinline__ float sigmoid(float x) {
     constexpr float kHi = -1.44269502162933349609375f, kLo = -1.92596303e-8f;  // -log2 e
+    x = __builtin_amdgcn_fmed3f(x, -1.0e4f, 1.0e4f);  // 0 and 1 long before; beyond 2^127 / log2 e t would overflow
     const float t = x * kHi, lo = fmaf(x, kHi, -t) + x * kLo;
-    const float e = __builtin_amdgcn_exp2f(t);
-    // 2^lo - 1 = lo ln 2 to first order, |lo| < 2^-16; an infinite e stays infinite
-    return __builtin_amdgcn_rcpf(1.0f + fmaf(e, lo * 0.693147182f, e));
+    // 2^lo = 1 + lo ln 2 to 24 bits: |lo| < 2^-16 where the power is neither 0 nor infinite, and those stay so
+    return __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_exp2f(t), fmaf(lo, 0.693147182f, 1.0f), 1.0f));
 }
 
 // The output for the normalised value m, and what its gradient needs.

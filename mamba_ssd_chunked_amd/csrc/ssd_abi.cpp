@@ -503,9 +503,16 @@ int validate_delta(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape*
     });
 }
 
-// Linear attention: two workgroups of 256 at most for each head (many only where heads are few).
+// Linear attention: eight workgroups of 256 at most for each head (the gradient in fp32 with p = r = 128, the
+// decay's with it).  Rows of a chunk are found by 32-bit byte offsets from its first.
 int validate_linear(const char* who, const ssd_delta_dims* dims, ssd::DeltaShape* d) {
-    return validate_heads(who, dims, d, [](const ssd_delta_dims&) { return 512.0; });
+    if (int rc = validate_heads(who, dims, d, [](const ssd_delta_dims&) { return 2048.0; })) return rc;
+    const int64_t most = 1 << 24, wide = static_cast<int64_t>(d->H) * std::max(d->P, d->R);
+    if (d->S > 1 && (d->qs[1] > most || d->ks[1] > most || d->vs[1] > most || wide > most))
+        return fail(SSD_ERR_UNSUPPORTED, "%s: tokens may be at most 2^24 elements apart (got %lld, %lld, %lld for q, k "
+                    "and v, %lld for outputs)", who, (long long)d->qs[1], (long long)d->ks[1], (long long)d->vs[1],
+                    (long long)wide);
+    return SSD_OK;
 }
 
 ssd::LinearShape linear_shape(const ssd::DeltaShape& d, const float* log_decay, bool bwd, bool decay) {
@@ -664,7 +671,6 @@ int validate_group_norm(const char* who, const ssd_group_norm_dims* n, ssd::Grou
     d->io = n->io_dtype;
     d->act = n->act;
     d->eps = n->eps;
-    d->count = (float)(cg * (double)n->positions);
     d->inv_count = (float)(1.0 / (cg * (double)n->positions));
     if (d->n > 0) ssd::group_norm_plan(d, bwd);
     return SSD_OK;

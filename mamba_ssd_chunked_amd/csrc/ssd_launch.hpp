@@ -416,7 +416,7 @@ struct GroupShape {
     int c, groups, cg;      // channels, groups, channels of a group
     int64_t x_stride, gate_stride;  // elements between positions
     int io, act;
-    float eps, count, inv_count;    // count: values of a group
+    float eps, inv_count;           // inv_count: one over the values of a group
     // the plan: vector width, and its channels sure to share a group; whether each position is a sample of
     // its own (tokens), or one workgroup has a slab of a sample (whole); how sums and outputs are cut up
     int ev, sub, tokens, whole;
