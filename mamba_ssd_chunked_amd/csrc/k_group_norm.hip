@@ -134,21 +134,28 @@ __global__ __launch_bounds__(256) void k_group_norm_rows(GroupShape d, const typ
         const int64_t row = team / d.groups;
         const int ch = static_cast<int>(team % d.groups) * d.cg;
         float v[NV][EV], w[NV][EV], b[NV][EV], z[NV][EV];
-        float sum = 0.0f;
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int col = (lane + m * TS) * EV;
-#pragma unroll
-            for (int e = 0; e < EV; ++e) v[m][e] = 0.0f;
             if (col < d.cg) {
                 ldv<IO, EV>(x + row * d.x_stride + ch + col, v[m]);
                 if (gate) ldv<IO, EV>(gate + row * d.gate_stride + ch + col, z[m]);
                 ld_chan<EV>(weight, ch + col, 1.0f, w[m]);
                 ld_chan<EV>(bias, ch + col, 0.0f, b[m]);
             }
-#pragma unroll
-            for (int e = 0; e < EV; ++e) sum += v[m][e];
         }
+        // about the group's first value: exact for a constant group, and no sum of large means is rounded
+        const float first = __shfl(v[0][0], 0, TS);
+        float sum = 0.0f;
+#pragma unroll
+        for (int m = 0; m < NV; ++m)
+            if ((lane + m * TS) * EV < d.cg) {
+#pragma unroll
+                for (int e = 0; e < EV; ++e) {
+                    v[m][e] -= first;
+                    sum += v[m][e];
+                }
+            }
         const float mean = team_sum<TS>(sum) * d.inv_count;
         float sq = 0.0f;
 #pragma unroll
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(256) void k_group_norm_rows(GroupShape d, const typ
             }
         const float rstd = 1.0f / sqrtf(team_sum<TS>(sq) * d.inv_count + d.eps);
         if (stats && lane == 0) {
-            stats[2 * team] = mean;
+            stats[2 * team] = first + mean;
             stats[2 * team + 1] = rstd;
         }
         if (y) {
