@@ -78,7 +78,7 @@ namespace {
 
 template <class IO, int R, int P, int MODE>
 hipError_t run_p(const LinearShape& d, const LinearJobs& jobs, hipStream_t st) {
-    constexpr int NTILE = MODE == kTangentCarry ? 1 : linear_tiles<IO, P>(), NW = P <= 32 ? 2 : 4, PC = 16 * NTILE * NW;
+    constexpr int NTILE = MODE == kTangentCarry ? 1 : kLinearTiles<IO, P, R>, NW = P <= 32 ? 2 : 4, PC = 16 * NTILE * NW;
     const int64_t per = MODE == kOutputs ? d.segs : d.segs - 1, pbs = P <= PC ? 1 : P / PC;
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * per * pbs), jobs.n);
     k_linear<IO, R, NTILE, NW, MODE><<<grid, 64 * NW, 0, st>>>(d, jobs);
@@ -95,26 +95,54 @@ hipError_t run(const LinearShape& d, const LinearJobs& jobs, hipStream_t st) {
 
 }  // namespace
 
-// As many segments as give the chip's 512 places (two workgroups a CU) a workgroup each, of at least two
-// chunks.  Whole where heads alone take more than half the places, or where the chunks that a workgroup is
+namespace {
+
+// A gradient in n segments, in us, as measured with p = 64 and r = 128 on a chip of 512 places (two workgroups
+// a CU): a chunk of a workgroup takes 5.3 (bf16 3.0), 8.4 (4.8) with the decay's gradient beside it, less alone
+// on its CU; beyond the places a round more and half of one for its uneven end.  A chunk carried takes 2 (1), 6
+// (4) with the state's derivative, and the launches between 15 or 25.  Narrower states take less, to a floor.
+double gradient_time(const LinearShape& d, bool decay, int n) {
+    auto rounds = [](double wgs) { return wgs <= 256.0 ? 0.73 : wgs <= 512.0 ? 1.0 : wgs / 512.0 + 0.5; };
+    const bool bf = d.io == 1;
+    const double heads = static_cast<double>(d.B) * d.H, left = (d.N + n - 1) / n;
+    const double chunk = (decay ? (bf ? 4.8 : 8.4) : (bf ? 3.0 : 5.3)) * (0.25 + (d.P + d.R) / 256.0);
+    const double t = left * chunk * rounds(heads * linear_grad_blocks(d, decay) * n);
+    if (n == 1) return t;
+    const double carried = heads * linear_blocks(d) * (n - 1), wide = left * (0.5 + (d.P + d.R) / 384.0);
+    return t + (decay ? 25.0 + wide * (bf ? 4.0 : 6.0) * rounds(carried) : 15.0 + wide * (bf ? 1.0 : 2.0) * rounds(2.0 * carried));
+}
+
+}  // namespace
+
+// Forwards, as many segments as give the chip's 512 places (two workgroups a CU) a workgroup each, of at least
+// two chunks.  Whole where heads alone take more than half the places, or where the chunks that a workgroup is
 // spared (2 us each in bf16 and 3.5 in fp32 with r = 128, half of that with narrow keys) do not pay for
 // carrying (half as long a chunk) and for two more launches.  Measured in 1 to 32 segments: bf16, p = 64,
 // r = 128, 160 heads of 4096 tokens 268 us whole, 202 in three, 221 in five; 96 of 1531 107 whole, 66 in five;
 // 32 of 8192 523 whole, 98 in sixteen; fp32 8 of 1024 125 whole, 35 in sixteen.
-// A gradient with the decay's fills the places unevenly: where it takes one to three rounds of them, four
-// segments even that out (fp32, 96 heads of 2048 tokens, 650 -> 594 us; bf16, 160 of 4096, 928 -> 856).
+// Backwards, where a head has workgroups of several kinds and the rounds end unevenly, the number of segments
+// of four chunks or more with the least gradient_time.  Measured in 1 to 24 segments, p = 64, r = 128, with the
+// decay's gradient, fp32: 48 heads of 2048 tokens 384 us whole, 421 in two, 309 in eight; 32 of 16384 3007
+// whole, 1629 in four, 1380 in sixteen; 160 of 4096 1842 whole, 1668 in four; without it, bf16: 96 of 2048 191
+// whole, 169 in four; 160 of 4096 439 whole, 528 in four.
 int linear_segments(const LinearShape& d, bool bwd, bool decay) {
-    const int64_t heads = static_cast<int64_t>(d.B) * d.H, each = bwd ? linear_grad_blocks(d, decay) : linear_blocks(d);
-    const int64_t wgs = heads * each;
+    const int64_t heads = static_cast<int64_t>(d.B) * d.H, wgs = heads * (bwd ? linear_grad_blocks(d, decay) : linear_blocks(d));
     if (wgs == 0) return 1;
-    if (wgs > 256) return bwd && decay && wgs > 512 && wgs <= 1536 && d.N >= 32 ? 4 : 1;
+    if (bwd) {
+        int best = 1;
+        double least = gradient_time(d, decay, 1);
+        for (int n = 2; n <= d.N / 4 && n * wgs <= 2560; ++n)
+            if (const double t = gradient_time(d, decay, n); t < least) best = n, least = t;
+        return best;
+    }
+    if (wgs > 256) return 1;
     int64_t n = 512 / wgs;
     if (n > d.N / 2) n = d.N / 2;
     if (n < 2) return 1;
     const double chunk = (d.io == 1 ? 1.0 : 1.75) * (1.0 + d.R / 128.0), left = static_cast<double>((d.N + n - 1) / n);
     return chunk * d.N < 1.5 * chunk * left + 15.0 ? 1 : static_cast<int>(n);
 }
-int linear_blocks(const LinearShape& d) { return d.P == 128 && d.io == 0 ? 2 : 1; }
+int linear_blocks(const LinearShape& d) { return d.P == 128 && linear_tiles(d.io == 1, d.P, d.R) == 1 ? 2 : 1; }
 
 hipError_t launch_linear_scan(const LinearShape& d, const LinearJobs& jobs, hipStream_t st) {
     return run<kOutputs>(d, jobs, st);

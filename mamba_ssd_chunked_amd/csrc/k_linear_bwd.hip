@@ -11,8 +11,8 @@ namespace ssd {
 // each in as many workgroups as its columns take.
 template <class IO, int R, int P, bool WIDE, bool DECAY>
 __global__ __launch_bounds__(256, 2) void k_linear_grad(LinearShape d, LinearGrads g) {
-    using Keys = LinearScan<IO, P, linear_tiles<IO, R>(), 4, WIDE ? kWide : kOutputs>;  // d_q, d_k
-    using Values = LinearScan<IO, R, linear_tiles<IO, P>(), 4, kOutputs>;
+    using Keys = LinearScan<IO, P, kLinearTiles<IO, R, P>, 4, WIDE ? kWide : kOutputs>;  // d_q, d_k
+    using Values = LinearScan<IO, R, kLinearTiles<IO, P, R>, 4, kOutputs>;
     using Tangent = LinearScan<IO, R, 1, 4, kTangent>;
     constexpr int KB = R <= Keys::PC ? 1 : R / Keys::PC, VB = P <= Values::PC ? 1 : P / Values::PC,
                   TB = !DECAY ? 0 : P <= Tangent::PC ? 1 : P / Tangent::PC, PER = TB + 2 * KB + VB;
@@ -65,7 +65,7 @@ int blocks(int width, int tiles) { return width <= 64 * tiles ? 1 : width / (64 
 
 template <class IO, int R, int P, bool WIDE, bool DECAY>
 hipError_t grad(const LinearShape& d, const LinearGrads& g, hipStream_t st) {
-    const int per = (DECAY ? blocks(P, 1) : 0) + 2 * blocks(R, linear_tiles<IO, R>()) + blocks(P, linear_tiles<IO, P>());
+    const int per = (DECAY ? blocks(P, 1) : 0) + 2 * blocks(R, kLinearTiles<IO, R, P>) + blocks(P, kLinearTiles<IO, P, R>);
     k_linear_grad<IO, R, P, WIDE, DECAY>
         <<<dim3(static_cast<unsigned>(static_cast<int64_t>(d.B) * d.H * d.segs * per)), 256, 0, st>>>(d, g);
     return hipGetLastError();
@@ -74,8 +74,8 @@ hipError_t grad(const LinearShape& d, const LinearGrads& g, hipStream_t st) {
 }  // namespace
 
 int linear_grad_blocks(const LinearShape& d, bool decay) {
-    auto of = [&](int width) { return blocks(width, d.io == 1 && width == 128 ? 2 : 1); };
-    return 2 * of(d.R) + of(d.P) + (decay ? blocks(d.P, 1) : 0);
+    auto of = [&](int columns, int rows) { return blocks(columns, linear_tiles(d.io == 1, columns, rows)); };
+    return 2 * of(d.R, d.P) + of(d.P, d.R) + (decay ? blocks(d.P, 1) : 0);
 }
 
 hipError_t launch_linear_grad(const LinearShape& d, const LinearGrads& g, bool decay, hipStream_t st) {

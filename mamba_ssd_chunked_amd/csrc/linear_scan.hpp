@@ -681,10 +681,13 @@ struct LinearScan {
     }
 };
 
-// Tiles of columns of a wave, and waves, for P value columns: two tiles where 128 columns share a
-// workgroup's operands (bf16; fp32's do not fit twice on a CU: two workgroups of 64).
-template <class IO, int P>
-__host__ __device__ constexpr int linear_tiles() { return P == 128 && in_parts<IO>() == 1 ? 2 : 1; }
+// Tiles of columns of a wave for `columns` of a state with `rows`: two where 128 columns share a workgroup's
+// operands (the parts of fp32 rows of 128 do not fit twice on a CU: two workgroups of 64 columns).
+__host__ __device__ constexpr int linear_tiles(bool bf16, int columns, int rows) {
+    return columns == 128 && (bf16 || rows <= 64) ? 2 : 1;
+}
+template <class IO, int COLUMNS, int ROWS>
+constexpr int kLinearTiles = linear_tiles(in_parts<IO>() == 1, COLUMNS, ROWS);
 
 // f(P, R) as constants
 template <class F>
