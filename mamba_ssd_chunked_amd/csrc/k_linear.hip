@@ -16,6 +16,8 @@
 //   T' = a^C (T + C H) + ((C-1-s) a^{C-1-s} V)^T K,
 //   dY = scale (a^{t+1} Q (T + (t+1) H)^T + sum_s (t-s) P_ts V_s),   d_log_decay = <dy, dY> + <d_final, T_end>:
 // every pair of tokens weighs in with its own distance, and nothing of the size of the positions cancels.
+// dY itself is not made: <dy, dY> = <T, W> + <H, W'> + sum_{s<t} (t-s) P_ts (dy_t.v_s) scale, with
+// W = scale sum_t a^{t+1} dy_t q_t^T and W' the same (t+1) times.
 //
 // Tokens past a row's length are zeros in every operand; their memory is not read.
 #include "linear_scan.hpp"
@@ -98,14 +100,14 @@ hipError_t run(const LinearShape& d, const LinearJobs& jobs, hipStream_t st) {
 namespace {
 
 // A gradient in n segments, in us, as measured with p = 64 and r = 128 on a chip of 512 places (two workgroups
-// a CU): a chunk of a workgroup takes 5.3 (bf16 3.0), 8.4 (4.8) with the decay's gradient beside it, less alone
+// a CU): a chunk of a workgroup takes 5.3 (bf16 3.0), 7.4 (4.0) with the decay's gradient beside it, less alone
 // on its CU; beyond the places a round more and half of one for its uneven end.  A chunk carried takes 2 (1), 6
 // (4) with the state's derivative, and the launches between 15 or 25.  Narrower states take less, to a floor.
 double gradient_time(const LinearShape& d, bool decay, int n) {
     auto rounds = [](double wgs) { return wgs <= 256.0 ? 0.73 : wgs <= 512.0 ? 1.0 : wgs / 512.0 + 0.5; };
     const bool bf = d.io == 1;
     const double heads = static_cast<double>(d.B) * d.H, left = (d.N + n - 1) / n;
-    const double chunk = (decay ? (bf ? 4.8 : 8.4) : (bf ? 3.0 : 5.3)) * (0.25 + (d.P + d.R) / 256.0);
+    const double chunk = (decay ? (bf ? 4.0 : 7.4) : (bf ? 3.0 : 5.3)) * (0.25 + (d.P + d.R) / 256.0);
     const double t = left * chunk * rounds(heads * linear_grad_blocks(d, decay) * n);
     if (n == 1) return t;
     const double carried = heads * linear_blocks(d) * (n - 1), wide = left * (0.5 + (d.P + d.R) / 384.0);
@@ -122,8 +124,8 @@ double gradient_time(const LinearShape& d, bool decay, int n) {
 // 32 of 8192 523 whole, 98 in sixteen; fp32 8 of 1024 125 whole, 35 in sixteen.
 // Backwards, where a head has workgroups of several kinds and the rounds end unevenly, the number of segments
 // of four chunks or more with the least gradient_time.  Measured in 1 to 24 segments, p = 64, r = 128, with the
-// decay's gradient, fp32: 48 heads of 2048 tokens 384 us whole, 421 in two, 309 in eight; 32 of 16384 3007
-// whole, 1629 in four, 1380 in sixteen; 160 of 4096 1842 whole, 1668 in four; without it, bf16: 96 of 2048 191
+// decay's gradient, fp32: 48 heads of 2048 tokens 333 us whole, 383 in two, 276 in eight; 32 of 16384 2655
+// whole, 1498 in four, 1202 in sixteen; 160 of 4096 1590 whole, 1507 in four; without it, bf16: 96 of 2048 191
 // whole, 169 in four; 160 of 4096 439 whole, 528 in four.
 int linear_segments(const LinearShape& d, bool bwd, bool decay) {
     const int64_t heads = static_cast<int64_t>(d.B) * d.H, wgs = heads * (bwd ? linear_grad_blocks(d, decay) : linear_blocks(d));

@@ -83,13 +83,14 @@ struct LinearScan {
     static constexpr bool PLAIN = MODE == kOutputs || MODE == kWide, OUT = PLAIN || MODE == kTangent;
     static constexpr bool TAN = MODE == kTangent || MODE == kTangentCarry;
     using Out = typename std::conditional<MODE == kWide, float, T>::type;
+    static constexpr int GT = TAN && NP > 1 ? 1 : 2;  // state tiles at a time (more in parts spill beside two states)
     static constexpr int QT = TT * KJ;  // operand tiles of q or k, a part
     static constexpr int VS = PC + 4;   // floats of a row of v (fp32 io)
     static constexpr int QBYTES = NP * QT * 1024, VBYTES = NP == 1 ? TT * VJ * 1024 : C * VS * 4;
-    static constexpr int PBYTES = OUT ? 3 * TT * 1024 : 0;
+    static constexpr int PBYTES = PLAIN ? 3 * TT * 1024 : MODE == kTangent ? VBYTES : 0;  // (P, or dy like v)
     static constexpr int YS = PC * sizeof(Out) + 16;  // bytes of a row of outputs
     static constexpr int oK = 0, oQ = oK + QBYTES, oV = oQ + (OUT ? QBYTES : 0), oP = oV + VBYTES, oY = oP + PBYTES,
-                         oF = oY + (PLAIN ? C * YS : 0), LDS = oF + 4 * 2 * C;
+                         oF = oY + (PLAIN ? C * YS : 0), LDS = oF + 4 * (MODE == kTangent ? 4 : 2) * C;
     // loads of one wave and of one thread
     static constexpr int PER = (QT + NW - 1) / NW;
     static constexpr int RPP = 16 / NTILE;  // rows of v that the workgroup loads at a time (fp32 io)
@@ -102,7 +103,9 @@ struct LinearScan {
     char* sm;
     const LinearShape d;  // by value: through references the kernel's arguments are read again in every chunk
     const LinearJob a;
-    float *kf, *kft;  // what a token's key adds to the state is scaled by; of the tangent
+    // what a token's key adds to the state is scaled by, and to the tangent; what a token's query reads of the
+    // tangent and of the state (kTangent)
+    float *kf, *kft, *qw, *qwt;
     // scaled a^(t - s) of a lane's places t = i, s = 4 g + v in a tile of P on the diagonal (0 above it)
     // and in the one below
     v4f near, next;
@@ -116,6 +119,8 @@ struct LinearScan {
         : sm(smem), d(dd), a(aa), p0(first), seg(segment), bh(head_) {
         kf = reinterpret_cast<float*>(sm + oF);
         kft = kf + C;
+        qw = kf + 2 * C;
+        qwt = kf + 3 * C;
         lane = threadIdx.x & 63;
         w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         i = lane & 15;
@@ -173,7 +178,7 @@ struct LinearScan {
     // ---------------------------------------------------------------- loads, a chunk ahead
     struct Ahead {
         raw8 k[PER], q[OUT ? PER : 1];
-        rawv v[VPER];
+        rawv v[VPER], dy[MODE == kTangent ? VPER : 1];
     };
     __device__ int64_t token(int u) const {  // of place u of the row; past its end the last one
         u = u < len ? u : len - 1;
@@ -201,7 +206,9 @@ struct LinearScan {
             return reinterpret_cast<const char*>(head(from, stride, div) + r0 * stride[1]);
         };
         const char *kp = base(a.k, a.ks, a.kdiv), *qp = base(a.q, a.qs, a.qdiv), *vp = base(a.v, a.vs, a.vdiv) + p0 * sizeof(T);
-        const uint32_t kt = a.ks[1] * sizeof(T), qt = a.qs[1] * sizeof(T), vt = a.vs[1] * sizeof(T);
+        const char* dp = MODE == kTangent ? base(a.dst, a.os, 1) + p0 * sizeof(T) : nullptr;
+        const uint32_t kt = a.ks[1] * sizeof(T), qt = a.qs[1] * sizeof(T), vt = a.vs[1] * sizeof(T),
+                       dt = a.os[1] * sizeof(T);
         const int is = slot_token();
         const uint32_t col = (8 * (lane & 3) < R ? 8 * (lane & 3) : 0) * sizeof(T);
         auto load = [](const char* at, uint32_t off, auto& to) {
@@ -233,7 +240,9 @@ struct LinearScan {
         for (int m = 0; m < VPER; ++m)
             if (NP != 1 || TT * VJ % NW == 0 || w + NW * m < TT * VJ) {
                 const int vcol = p0 + (NP == 1 ? 32 * ((w + NW * m) % VJ) + 8 * (lane & 3) : 4 * (threadIdx.x % (PC / 4)));
-                load(vp + shared_row(c, v_at(m), VROWS) * vt, vr[m] * vt + (vcol < d.P ? vcol - p0 : 0) * sizeof(T), x.v[m]);
+                const uint32_t to = (vcol < d.P ? vcol - p0 : 0) * sizeof(T), row = shared_row(c, v_at(m), VROWS);
+                load(vp + row * vt, vr[m] * vt + to, x.v[m]);
+                if constexpr (MODE == kTangent) load(dp + row * dt, vr[m] * dt + to, x.dy[m]);
             }
     }
     __device__ static Parts<NP> parts8(const raw8& x) {
@@ -275,18 +284,26 @@ struct LinearScan {
                 }
             }
         }
+        put_values(x.v, oV, n);
+        if constexpr (MODE == kTangent) put_values(x.dy, oP, n);
+    }
+    __device__ void put_values(rawv (&x)[VPER], int base, int n) const {
+        auto blank = [](auto& r, bool on) {
+#pragma unroll
+            for (int e = 0; e < static_cast<int>(sizeof(r) / sizeof(T)); ++e) r[e] = on ? r[e] : T(0);
+        };
 #pragma unroll
         for (int m = 0; m < VPER; ++m) {
             if constexpr (NP == 1) {
                 const int tile = w + NW * m, tau = tile / VJ;
                 if (TT * VJ % NW == 0 || tile < TT * VJ) {
-                    if (part) blank(x.v[m], 16 * tau + is < n);
-                    *reinterpret_cast<raw8*>(sm + oV + tile * 1024 + slot_at()) = x.v[m];
+                    if (n < C) blank(x[m], 16 * tau + slot_token() < n);
+                    *reinterpret_cast<raw8*>(sm + base + tile * 1024 + slot_at()) = x[m];
                 }
             } else {
                 const int row = RPP * m + threadIdx.x / (PC / 4);
-                if (part) blank(x.v[m], row < n);
-                *reinterpret_cast<raw4*>(sm + oV + (row * VS + 4 * (threadIdx.x % (PC / 4))) * 4) = x.v[m];
+                if (n < C) blank(x[m], row < n);
+                *reinterpret_cast<raw4*>(sm + base + (row * VS + 4 * (threadIdx.x % (PC / 4))) * 4) = x[m];
             }
         }
     }
@@ -308,9 +325,9 @@ struct LinearScan {
             o.p[n] = *reinterpret_cast<const b8v*>(sm + base + (n * QT + tau * KJ + j) * 1024 + tile_slot(i, g) * 16);
         return o;
     }
-    __device__ Parts<NP> col_op(int rho) const {  // rows of state tile rho, k over the chunk's tokens
+    __device__ Parts<NP> col_op(int rho, int base = oK) const {  // rows of state tile rho, k over the chunk's tokens
         Parts<NP> o;
-        const int at = oK + (rho >> 1) * 1024 + tile_slot(4 * g + (i >> 2), i & 3) * 16 + (rho & 1) * 8;
+        const int at = base + (rho >> 1) * 1024 + tile_slot(4 * g + (i >> 2), i & 3) * 16 + (rho & 1) * 8;
 #pragma unroll
         for (int n = 0; n < NP; ++n)
             o.p[n] = join8(lds_col4(reinterpret_cast<const uint16_t*>(sm + at + n * QT * 1024)),
@@ -318,16 +335,47 @@ struct LinearScan {
         return o;
     }
     // tokens 16 t + 4 g + v of column col_of(i, e), as they lie (bf16) or as values (fp32)
-    __device__ auto value4(int t, int e) const {
+    __device__ auto value4(int t, int e, int base = oV) const {
         if constexpr (NP == 1) {
             const int col = wc + (NTILE == 1 ? 4 * (i & 3) : 8 * (i & 3) + 4 * e);
             return lds_col4(reinterpret_cast<const uint16_t*>(
-                sm + oV + (t * VJ + (col >> 5)) * 1024 + tile_slot(4 * g + (i >> 2), (col >> 3) & 3) * 16 +
+                sm + base + (t * VJ + (col >> 5)) * 1024 + tile_slot(4 * g + (i >> 2), (col >> 3) & 3) * 16 +
                 ((col >> 2) & 1) * 8));
         } else {
-            const float* x = reinterpret_cast<const float*>(sm + oV) + (16 * t + 4 * g) * VS + wc + col_of(i, e);
+            const float* x = reinterpret_cast<const float*>(sm + base) + (16 * t + 4 * g) * VS + wc + col_of(i, e);
             return v4f{x[0], x[VS], x[2 * VS], x[3 * VS]};
         }
+    }
+    // all 32 tokens of column col_of(i, e), times what each is weighted by
+    __device__ void values(v4f (&val)[2], int e, int base = oV) const {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const auto x = value4(t, e, base);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                if constexpr (NP == 1)
+                    val[t][m] = bf16_to_f32(x[m]);
+                else
+                    val[t][m] = x[m];
+            }
+        }
+    }
+    __device__ Parts<3> weighted(const v4f (&val)[2], const float* by) const {
+        return cut44<3>(val[0] * *reinterpret_cast<const v4f*>(by + 4 * g), val[1] * *reinterpret_cast<const v4f*>(by + 16 + 4 * g));
+    }
+    // rows of the values: tokens 16 tau + i, the workgroup's columns 32 j + 8 g and on (zeros past the last)
+    __device__ Parts<NP> value_row(int base, int tau, int j) const {
+        Parts<NP> o;
+        if (p0 + 32 * j + 8 * g >= d.P) {
+#pragma unroll
+            for (int n = 0; n < NP; ++n) o.p[n] = b8v{};
+        } else if constexpr (NP == 1) {
+            o.p[0] = *reinterpret_cast<const b8v*>(sm + base + (tau * VJ + j) * 1024 + tile_slot(i, g) * 16);
+        } else {
+            const v4f* x = reinterpret_cast<const v4f*>(sm + base + ((16 * tau + i) * VS + 32 * j + 8 * g) * 4);
+            o = __builtin_bit_cast(Parts<NP>, cut44<3>(x[0], x[1]));
+        }
+        return o;
     }
     __device__ static constexpr int terms(int na, int nb) {  // MFMAs of a product
         int n = 0;
@@ -373,7 +421,6 @@ struct LinearScan {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 x[v] *= tau == sg ? near[v] : next[v];
-                if constexpr (TAN) x[v] *= static_cast<float>(16 * (tau - sg) + i - 4 * g - v);
             }
             const auto p = cut44<3>(x, x);
 #pragma unroll
@@ -425,18 +472,66 @@ struct LinearScan {
             }
         }
     }
-    // Outputs times what dst holds, summed (kTangent).
-    __device__ float dot_outputs(const v4f (&y)[NTILE][TT], int c) const {
-        const T* const dst = static_cast<const T*>(a.dst) + b * a.os[0] + h * a.os[2] + p0 + wc;
+    // ---------------------------------------------------------------- the derivative along the decay
+    // <dy, dY> of a chunk without its outputs.  Of the pairs of tokens: sum (t-s) a^(t-s) (q_t.k_s) (dy_t.v_s), the
+    // tiles round the waves like P's.
+    __device__ float pair_dots() const {
+        float sum = 0.0f;
+        constexpr int MY = (3 + NW - 1) / NW;
+#pragma unroll
+        for (int m = 0; m < MY; ++m) {
+            const int tile = w + NW * m, tau = tile > 0, sg = tile > 1;
+            if (tile >= 3) break;
+            v4f x = zero4(), z = zero4();
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                x = mma(row_op(oK, sg, j), row_op(oQ, tau, j), x);
+                fence();  // (all of them at once would spill)
+            }
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) {
+                z = mma(value_row(oV, sg, j), value_row(oP, tau, j), z);
+                fence();
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float by = (tau == sg ? near[v] : next[v]) * static_cast<float>(16 * (tau - sg) + i - 4 * g - v);
+                sum += by * x[v] * z[v];
+            }
+        }
+        return sum;
+    }
+    // Of the entry state: <T, W> + <H, W'> with W = sum a^(t+1) dy_t q_t^T and W' the same (t+1) times, whose tiles lie
+    // as the state's: neither it nor T is cut into parts for it.  (By outputs Q T^T and Q H^T instead: 96 heads of
+    // 2048 tokens, p = 64, r = 128, bf16 299 -> 243 us, fp32 554 -> 535.)
+    __device__ float state_dots(const State& s, const State& ts) const {
+        constexpr int G = GT, STEPS = RT / G;
         float sum = 0.0f;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int u = c * C + 16 * t + i;
-            if (u < len) {
+        for (int e = 0; e < NTILE; ++e) {
+            v4f val[2];
+            values(val, e, oP);
+            const Parts<3> zo = weighted(val, qw), zt = weighted(val, qwt);
+            Parts<NP> op[2][G];
 #pragma unroll
-                for (int e = 0; e < NTILE; ++e) {
-                    const v4f o = io<IO>::ld4(dst + token(u) * a.os[1], col_of(4 * g, e)), z = y[e][t];
-                    sum += o[0] * z[0] + o[1] * z[1] + o[2] * z[2] + o[3] * z[3];
+            for (int m = 0; m < G; ++m) op[0][m] = col_op(m, oQ);
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                if (k + 1 < STEPS) {
+#pragma unroll
+                    for (int m = 0; m < G; ++m) op[(k + 1) & 1][m] = col_op((k + 1) * G + m, oQ);
+                }
+                v4f x[G], xt[G];
+#pragma unroll
+                for (int m = 0; m < G; ++m) x[m] = xt[m] = zero4();
+                fence();
+                mma_a(x, op[k & 1], zo);
+                mma_a(xt, op[k & 1], zt);
+                fence();
+#pragma unroll
+                for (int m = 0; m < G; ++m) {
+                    const v4f y = ts[e][k * G + m] * x[m] + s[e][k * G + m] * xt[m];
+                    sum += (y[0] + y[1]) + (y[2] + y[3]);
                 }
             }
         }
@@ -474,7 +569,13 @@ struct LinearScan {
                 near[v] = gap >= 0 ? a.out * a.in * power(l2, gap) : 0.0f;
                 next[v] = a.out * a.in * power(l2, 16 + gap);
             }
-            if (w == 0) {  // above P's diagonal
+            if (MODE == kTangent && threadIdx.x < C) {
+                const int n = static_cast<int>(threadIdx.x) + 1;
+                const float f = a.out * power(l2, n);
+                qw[threadIdx.x] = f;
+                qwt[threadIdx.x] = static_cast<float>(n) * f;
+            }
+            if (PLAIN && w == 0) {  // above P's diagonal
 #pragma unroll
                 for (int n = 0; n < 3; ++n)
                     *reinterpret_cast<uint2*>(sm + oP + n * TT * 1024 + lane * 16 + 8) = make_uint2(0, 0);
@@ -498,15 +599,24 @@ struct LinearScan {
             wait_barrier<63>();
             if (c + 1 < c1) fetch(x, c + 1);
             v4f y[NTILE][TT];
-            if constexpr (OUT) {
+            if constexpr (PLAIN) {
                 make_p();
-                if (active) read_state(y, s, ts[0], qf);
+                if (active) read_state(y, s, qf);
                 wait_barrier<63>();  // P is here
+            }
+            if constexpr (MODE == kTangent) {
+                // LDS addresses are made anew in every chunk: kept, beside two states and the parts of fp32 they
+                // spill, and a reload waits for all that is being fetched (96 heads of 2048 tokens, r = 128, 535
+                // -> 502 us; bf16, which does not spill, 243 -> 253)
+                if constexpr (NP > 1 && R == 128) asm volatile("" : "+v"(i), "+v"(g));
+                dot += pair_dots();
+                fence();
+                if (active) dot += state_dots(s, ts[0]);
+                fence();
             }
             if (active) {
                 advance(y, s, ts[0], n, keep, keep_lo);
                 if constexpr (PLAIN) keep_outputs(y, c);
-                if constexpr (MODE == kTangent) dot += dot_outputs(y, c);
             }
             mfma_settle();
             wait_barrier<63>();  // everything of this chunk is read
@@ -549,23 +659,16 @@ struct LinearScan {
 
     // y = scaled Q H^T as D[p][t]: lane token 16 t + i, rows columns col_of(4 g + v, e).  The state's parts
     // for a step are made while the matrix cores are at the step before.
-    __device__ void read_state(v4f (&y)[NTILE][TT], const State& s, const State& ts, const float (&qf)[TT]) const {
-        v4f yt[TAN ? NTILE : 1][TT];
+    __device__ void read_state(v4f (&y)[NTILE][TT], const State& s, const float (&qf)[TT]) const {
 #pragma unroll
         for (int e = 0; e < NTILE; ++e)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                y[e][t] = zero4();
-                if constexpr (TAN) yt[e][t] = zero4();
-            }
+            for (int t = 0; t < TT; ++t) y[e][t] = zero4();
         Parts<NP> op[2][TT];
-        Parts<3> hp[2][NTILE], tp[2][TAN ? NTILE : 1];
+        Parts<3> hp[2][NTILE];
         auto parts = [&](int j) {
 #pragma unroll
-            for (int e = 0; e < NTILE; ++e) {
-                hp[j & 1][e] = cut44<3>(s[e][2 * j], s[e][2 * j + 1]);
-                if constexpr (TAN) tp[j & 1][e] = cut44<3>(ts[e][2 * j], ts[e][2 * j + 1]);
-            }
+            for (int e = 0; e < NTILE; ++e) hp[j & 1][e] = cut44<3>(s[e][2 * j], s[e][2 * j + 1]);
         };
 #pragma unroll
         for (int t = 0; t < TT; ++t) op[0][t] = row_op(oQ, t, 0);
@@ -578,23 +681,17 @@ struct LinearScan {
             }
             fence();
 #pragma unroll
-            for (int e = 0; e < NTILE; ++e) {
-                mma_b(y[e], hp[j & 1][e], op[j & 1]);
-                if constexpr (TAN) mma_b(yt[e], tp[j & 1][e], op[j & 1]);
-            }
+            for (int e = 0; e < NTILE; ++e) mma_b(y[e], hp[j & 1][e], op[j & 1]);
             if (j + 1 < KJ) {
                 parts(j + 1);
-                mix<TT * NTILE * terms(3, NP) * (TAN ? 2 : 1), 28 / (TT * terms(3, NP)) + 1>();
+                mix<TT * NTILE * terms(3, NP), 28 / (TT * terms(3, NP)) + 1>();
             }
             fence();
         }
 #pragma unroll
         for (int e = 0; e < NTILE; ++e)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                if constexpr (TAN) y[e][t] = yt[e][t] + static_cast<float>(16 * t + i + 1 - a.rev) * y[e][t];
-                y[e][t] *= qf[t];
-            }
+            for (int t = 0; t < TT; ++t) y[e][t] *= qf[t];
     }
 
     // y <- y + P V, and the state over the chunk's n tokens.
@@ -604,24 +701,14 @@ struct LinearScan {
         v4f val[NTILE][2];
 #pragma unroll
         for (int e = 0; e < NTILE; ++e) {
-            if constexpr (NP == 1) {
-                const s4 lo = value4(0, e), hi = value4(1, e);
-                vo[e].p[0] = join8(lo, hi);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    val[e][0][m] = bf16_to_f32(lo[m]);
-                    val[e][1][m] = bf16_to_f32(hi[m]);
-                }
-            } else {
-                val[e][0] = value4(0, e);
-                val[e][1] = value4(1, e);
-                if constexpr (OUT) vo[e] = __builtin_bit_cast(Parts<NP>, cut44<3>(val[e][0], val[e][1]));
+            values(val[e], e);
+            if constexpr (PLAIN) {
+                if constexpr (NP == 1)
+                    vo[e].p[0] = join8(value4(0, e), value4(1, e));
+                else
+                    vo[e] = __builtin_bit_cast(Parts<NP>, cut44<3>(val[e][0], val[e][1]));
             }
         }
-        auto weighted = [&](const float* by, int e) {
-            return cut44<3>(val[e][0] * *reinterpret_cast<const v4f*>(by + 4 * g),
-                            val[e][1] * *reinterpret_cast<const v4f*>(by + 16 + 4 * g));
-        };
         auto fade = [&](int rho) {  // what the state keeps
 #pragma unroll
             for (int e = 0; e < NTILE; ++e) {
@@ -635,11 +722,11 @@ struct LinearScan {
         auto operands = [&]() {
 #pragma unroll
             for (int e = 0; e < NTILE; ++e) {
-                zo[e] = weighted(kf, e);
-                if constexpr (TAN) zt[e] = weighted(kft, e);
+                zo[e] = weighted(val[e], kf);
+                if constexpr (TAN) zt[e] = weighted(val[e], kft);
             }
         };
-        if constexpr (OUT) {
+        if constexpr (PLAIN) {
             // the vector unit fades the state and makes its operands meanwhile
             Parts<3> p[TT];
 #pragma unroll
@@ -660,7 +747,7 @@ struct LinearScan {
             for (int rho = 0; rho < RT; ++rho) fade(rho);
             operands();
         }
-        constexpr int G = 2, STEPS = RT / G;  // state tiles at a time
+        constexpr int G = GT, STEPS = RT / G;
         Parts<NP> op[2][G];
 #pragma unroll
         for (int m = 0; m < G; ++m) op[0][m] = col_op(m);
