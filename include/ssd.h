@@ -412,8 +412,9 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
  * d_decay = 0); tokens at or past a row's valid_len are not read, leave the state alone, and give y and
  * gradients of exactly zero.
  * bf16 io: the products take the bf16 inputs as they are and everything else (states, decays, the
- * causal matrix, sums) to 24 bits; y, d_q, d_k, d_v are rounded to nearest even.  Results are bitwise
- * reproducible.  A NaN or an infinity among a row's tokens spreads over its chunk of 32 tokens and on
+ * causal matrix, sums) to 24 bits; y, d_q, d_k, d_v are rounded to nearest even.  fp32 values
+ * below 2^-102 may be held to fewer bits.  Results are bitwise reproducible.  Outputs overlap no input
+ * but states as said below.  A NaN or an infinity among a row's tokens spreads over its chunk of 32 tokens and on
  * from there (in the gradients of keys and values, whose chunks are counted from the row's end: back
  * from there), in that head (and d_q, d_k of its key head, d_decay of the head) only, but to no token
  * past the row's length.  A positive log_decay is taken as it is; its state has to stay finite.

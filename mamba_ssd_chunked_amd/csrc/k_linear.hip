@@ -133,7 +133,7 @@ int linear_segments(const LinearShape& d, bool bwd, bool decay) {
     if (bwd) {
         int best = 1;
         double least = gradient_time(d, decay, 1);
-        for (int n = 2; n <= d.N / 4 && n * wgs <= 2560; ++n)
+        for (int n = 2; n <= d.N / 4 && n * wgs <= 2560; n += 1 + n / 8)  // (few: this runs in every call)
             if (const double t = gradient_time(d, decay, n); t < least) best = n, least = t;
         return best;
     }
