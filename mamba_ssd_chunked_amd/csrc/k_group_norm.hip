@@ -393,7 +393,8 @@ __device__ __forceinline__ void piece_moments(const GroupShape& d, const Piece<E
 #pragma unroll
     for (int e = 0; e < EV; ++e) sh[e][threadIdx.x] = make_float2(mean[e], m2[e]);
     __syncthreads();
-    // per group: its records of every row lane, joined by a power of two of lanes
+    // per group: its records of every row lane, joined by a power of two of lanes.  Means are averaged as
+    // differences from one of them: exactly for a constant group, and else without roundings of the mean's size.
     const int per = p.nch / (p.ng * d.sub), R = static_cast<int>(p.r1 - p.r0), base = R / p.lanes, more = R % p.lanes;
     const float total = static_cast<float>(R) * static_cast<float>(per * d.sub);
     int lanes = 64;
@@ -412,7 +413,8 @@ __device__ __forceinline__ void piece_moments(const GroupShape& d, const Piece<E
             }
             return team(sum);
         };
-        const float mu = each([](float2 r, float cnt) { return cnt * r.x; }) / total;
+        const float one = sh[g * per * d.sub % EV][g * per * d.sub / EV].x;  // the group's first record's
+        const float mu = one + each([&](float2 r, float cnt) { return cnt * (r.x - one); }) / total;
         const float sum = each([&](float2 r, float cnt) { return r.y + cnt * (r.x - mu) * (r.x - mu); });
         if (l == 0) f(g, mu, sum);
     }
@@ -490,6 +492,7 @@ __global__ __launch_bounds__(256) void k_group_norm_join(GroupShape d, const flo
     const int K = d.sums.blocks * d.sums.cuts, l = threadIdx.x & 63;
     for (int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); at < d.n * d.groups;
          at += static_cast<int64_t>(gridDim.x) * 4) {
+        const float one = rec[at * K].x;
         float2 r[MAXREC / 64];
         float cnt[MAXREC / 64], sum = 0.0f;
 #pragma unroll
@@ -504,9 +507,9 @@ __global__ __launch_bounds__(256) void k_group_norm_join(GroupShape d, const flo
                 cnt[m] = static_cast<float>((r0 + d.sums.rows < d.s ? d.sums.rows : d.s - r0) *
                                             (d.sums.cuts > 1 && wide > 256 * d.ev ? 256 * d.ev : wide));
             }
-            sum += cnt[m] * r[m].x;
+            sum += cnt[m] * (r[m].x - one);
         }
-        const float mu = team_sum<64>(sum) * d.inv_count;
+        const float mu = one + team_sum<64>(sum) * d.inv_count;
         sum = 0.0f;
 #pragma unroll
         for (int m = 0; m < MAXREC / 64; ++m) sum += r[m].y + cnt[m] * (r[m].x - mu) * (r[m].x - mu);
