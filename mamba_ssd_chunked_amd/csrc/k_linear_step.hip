@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "delta_device.hpp"
+#include "linear_power.hpp"
 #include "ssd_launch.hpp"
 
 namespace ssd {
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(NT) void k_linear_step(DeltaShape d, int nslots, co
     }
     const v4f k4 = io<IO>::ld4(k, b * d.ks[0] + hk * d.ks[2] + 4 * c4);
     const v4f q4 = io<IO>::ld4(q, b * d.qs[0] + hk * d.qs[2] + 4 * c4);
-    const float a = exp2_of(static_cast<double>(log_decay[h]) * kLog2e);
+    const float a = power(log2_decay(log_decay[h]), 1);
     const float kq = sum_over_lanes<R4>(dot4(k4, q4));
 #pragma unroll
     for (int m = 0; m < K; ++m) {

@@ -4,22 +4,12 @@
 #include <type_traits>
 
 #include "delta_device.hpp"
+#include "linear_power.hpp"
 #include "ssd_launch.hpp"
 
 namespace ssd {
 
 constexpr int LC = 32;  // tokens per chunk
-
-// Below this a log decay counts as this: its powers but the zeroth are zero in fp32, and 0 * -inf
-// does not come up.
-constexpr double kMinDecay = -1.0e4;
-
-// Base-2 logarithm of a head's decay.
-__device__ __forceinline__ double log2_decay(float log_decay) {
-    return (log_decay < kMinDecay ? kMinDecay : static_cast<double>(log_decay)) * kLog2e;
-}
-// a^n for the base-2 logarithm of a, in fp64
-__device__ __forceinline__ float power(double log2a, int n) { return exp2_of(log2a * n); }
 
 // The eight XCDs take workgroups in turn and each has its own L2: give each a consecutive run of
 // the work, so that the columns, value heads and gradients that read the same rows meet in one.
