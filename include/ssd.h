@@ -417,7 +417,8 @@ int ssd_delta_step(const ssd_delta_dims* dims, int64_t nslots, const void* q, co
  * but states as said below.  A NaN or an infinity among a row's tokens spreads over its chunk of 32 tokens and on
  * from there (in the gradients of keys and values, whose chunks are counted from the row's end: back
  * from there), in that head (and d_q, d_k of its key head, d_decay of the head) only, but to no token
- * past the row's length.  A positive log_decay is taken as it is; its state has to stay finite.
+ * past the row's length.  A positive log_decay is taken as it is, as long as 32 a^n stays within fp32 over a row's
+ * n tokens, and over 32 of a longer row (log_decay up to 2.5 then); its state has to stay finite.
  * 2048 * batch * nheads < 2^32, and with more than one token at most 2^24 elements from a token to the
  * next in every operand (SSD_ERR_UNSUPPORTED otherwise; split over batch or heads).
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,

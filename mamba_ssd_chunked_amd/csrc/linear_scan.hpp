@@ -464,8 +464,9 @@ struct LinearScan {
     }
     // ---------------------------------------------------------------- the derivative along the decay
     // <dy, dY> of a chunk without its outputs.  Of the pairs of tokens: sum (t-s) a^(t-s) (q_t.k_s) (dy_t.v_s), the
-    // tiles round the waves like P's.
-    __device__ float pair_dots() const {
+    // tiles round the waves like P's.  (Tokens past the n-th left out: zero times what may be no number any more in a
+    // state that grows.)
+    __device__ float pair_dots(int n) const {
         float sum = 0.0f;
         constexpr int MY = (3 + NW - 1) / NW;
 #pragma unroll
@@ -483,11 +484,13 @@ struct LinearScan {
                 z = mma(value_row(oV, sg, j), value_row(oP, tau, j), z);
                 fence();
             }
+            float pairs = 0.0f;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const float by = (tau == sg ? near[v] : next[v]) * static_cast<float>(16 * (tau - sg) + i - 4 * g - v);
-                sum += by * x[v] * z[v];
+                pairs += by * x[v] * z[v];
             }
+            sum += 16 * tau + i < n ? pairs : 0.0f;
         }
         return sum;
     }
@@ -582,6 +585,7 @@ struct LinearScan {
             put(x, n);
             if (n < C) {
                 put_factors(n);
+                if (MODE == kTangent && static_cast<int>(threadIdx.x) >= n && threadIdx.x < C) qw[threadIdx.x] = qwt[threadIdx.x] = 0.0f;
                 kept = exp2(l2 * n);
                 keep = static_cast<float>(kept);
                 keep_lo = static_cast<float>(kept - keep);
@@ -599,7 +603,7 @@ struct LinearScan {
                 // spill, and a reload waits for all that is being fetched (96 heads of 2048 tokens, r = 128, 535
                 // -> 502 us; bf16, which does not spill, 243 -> 253)
                 if constexpr (NP > 1 && R == 128) asm volatile("" : "+v"(i), "+v"(g));
-                dot += pair_dots();
+                dot += pair_dots(n);
                 fence();
                 if (active) dot += state_dots(s, ts[0]);
                 fence();
