@@ -42,6 +42,13 @@ struct DeltaScan {
     int segs, seg_chunks;  // segments of the chunk axis, and their chunks
 };
 
+// A vector from memory on 16 bytes, as the entry points ask for (the type of eight floats alone says 32).
+template <class V>
+__device__ __forceinline__ V load_vec(const void* at) {
+    typedef V there __attribute__((aligned(16)));
+    return *static_cast<const there*>(at);
+}
+
 template <int N>
 struct Parts {
     b8v p[N];

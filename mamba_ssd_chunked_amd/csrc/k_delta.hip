@@ -186,8 +186,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaShape d, const typename
         const T* qb = q + b * d.qs[0] + (t0 + row) * d.qs[1] + hk * d.qs[2] + (R < 32 ? 8 * (g & 1) : 8 * g);
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
-            kr[j] = *reinterpret_cast<const raw8*>(kb + 32 * j);
-            qr[j] = *reinterpret_cast<const raw8*>(qb + 32 * j);
+            kr[j] = load_vec<raw8>(kb + 32 * j);
+            qr[j] = load_vec<raw8>(qb + 32 * j);
         }
     }
     if (w == 0) {
@@ -483,7 +483,7 @@ struct Scan {
     typedef T raw8 __attribute__((ext_vector_type(8)));
     typedef raw8 Ahead[QT / NL];
     __device__ void fetch_qk(Ahead& r, const T* x, const int64_t (&stride)[3], int c) const {
-        each_qk(x, stride, c, [&](int m, int, const T* src) { r[m] = *reinterpret_cast<const raw8*>(src); });
+        each_qk(x, stride, c, [&](int m, int, const T* src) { r[m] = load_vec<raw8>(src); });
     }
     __device__ void put_qk(int at, const Ahead& r) const {
 #pragma unroll

@@ -176,8 +176,8 @@ __global__ __launch_bounds__(GW * 64, in_parts<IO>() == 1 && !SHARED ? 4 : 2) vo
 #pragma unroll
         for (int m = 0; m < KV; ++m) {
             const int t = (tid + m * NTHR) / V, col = 8 * (tid % V), row = t < L ? t : L - 1, from = col < R ? col : 0;
-            kr[m] = *reinterpret_cast<const raw8*>(a.k + b * d.ks[0] + (t0 + row) * d.ks[1] + hk * d.ks[2] + from);
-            qr[m] = *reinterpret_cast<const raw8*>(a.q + b * d.qs[0] + (t0 + row) * d.qs[1] + hk * d.qs[2] + from);
+            kr[m] = load_vec<raw8>(a.k + b * d.ks[0] + (t0 + row) * d.ks[1] + hk * d.ks[2] + from);
+            qr[m] = load_vec<raw8>(a.q + b * d.qs[0] + (t0 + row) * d.qs[1] + hk * d.qs[2] + from);
         }
         if (AHEAD) fetch(0, 0);
 #pragma unroll

@@ -202,7 +202,7 @@ struct LinearScan {
         const int is = slot_token();
         const uint32_t col = (8 * (lane & 3) < R ? 8 * (lane & 3) : 0) * sizeof(T);
         auto load = [](const char* at, uint32_t off, auto& to) {
-            to = *reinterpret_cast<const std::remove_reference_t<decltype(to)>*>(at + off);
+            to = load_vec<std::remove_reference_t<decltype(to)>>(at + off);
         };
         uint32_t kr[PER], vr[VPER];  // rows
         const int vrow = NP == 1 ? is : threadIdx.x / (PC / 4);
