@@ -81,6 +81,35 @@ def roundings(s, r, p):
     return 1.5 * (4 + max(r, p) + 64 + chunks * (32 + 4))
 
 
+# Relative L2 error of whole fp32 outputs: each of the products that an output sums is off by two cuts to 24 bits, the
+# causal matrix's rounding and its cut, two powers and about eight roundings of sums, sixteen half steps if all of
+# them were whole ones to one side; the products' signs are random, so that the sum is off by as much of its size.
+CLOSE = 16 * 2.0 ** -24
+
+
+def decay_size(dy, q, k, v, log_decay, init=None, d_final=None, valid_len=None, scale=None):
+    """The size, by heads, that errors of d_decay = sum_t <dy_t, dY_t> + <d_final, T_end> go by: with dY and T right to
+    CLOSE in lengths, in directions at random, a product is off by its factors' lengths over the root of their p (or
+    p r) elements, and the products as the root of squares."""
+    dy, q, k, v, ld, init, d_final = _f64(dy, q, k, v, log_decay, init, d_final)
+    b, s, h, p = v.shape
+    r = q.shape[-1]
+    scale = r ** -0.5 if scale is None else scale
+    q, k, a = _spread(q, h), _spread(k, h), ld.exp()[:, None, None]
+    size = torch.zeros(h, dtype=torch.float64)
+    for row, n in enumerate(_lens(valid_len, b, s)):
+        H = torch.zeros(h, p, r, dtype=torch.float64) if init is None else init[row].clone()
+        T = torch.zeros_like(H)
+        for t in range(n):
+            T = a * (T + H)
+            H = a * H + v[row, t, :, :, None] * k[row, t, :, None, :]
+            dY = scale * (T * q[row, t, :, None, :]).sum(-1)
+            size += (dy[row, t].norm(dim=-1) * dY.norm(dim=-1)).square() / p
+        if d_final is not None:
+            size += (d_final[row].flatten(1).norm(dim=-1) * T.flatten(1).norm(dim=-1)).square() / (p * r)
+    return size.sqrt()
+
+
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 
 
