@@ -24,9 +24,14 @@
 
 namespace ssd {
 
+// Waves of a SIMD that share its registers: two, but one for the outputs of narrow fp32 heads with wide keys, which
+// take 287 (two waves would have 256 each).
+template <class IO, int R, int NW, int MODE>
+constexpr int kLinearWaves = in_parts<IO>() > 1 && R == 128 && NW == 2 && MODE == kOutputs ? 1 : 2;
+
 // Outputs, or what each segment but the last adds to a state.
 template <class IO, int R, int NTILE, int NW, int MODE>
-__global__ __launch_bounds__(64 * NW, 2) void k_linear(LinearShape d, LinearJobs jobs) {
+__global__ __launch_bounds__(64 * NW, (kLinearWaves<IO, R, NW, MODE>)) void k_linear(LinearShape d, LinearJobs jobs) {
     using Scan = LinearScan<IO, R, NTILE, NW, MODE>;
     __shared__ __align__(16) char sm[Scan::LDS];
     const int pbs = d.P <= Scan::PC ? 1 : d.P / Scan::PC, per = Scan::OUT ? d.segs : d.segs - 1;
