@@ -502,12 +502,15 @@ int ssd_rms_norm_workspace_size(int64_t rows, int64_t width, size_t* bytes);
  *   y, dy, d_x, d_gate   the same, contiguous    weight, bias, d_weight, d_bias  [channels] fp32
  *   stats          [batch, groups, 2] fp32: mean and 1 / sqrt(var + eps)
  * Tokens that are normalised each by itself are samples of one position (the heads of an attention's
- * output as groups: batch = tokens, positions = 1, groups = heads, the gate a slice of the projection).
+ * output as groups: batch = tokens, positions = 1, groups = heads, the gate a slice of the projection); as
+ * positions of one sample they would share their statistics, earlier ones with later ones.
  * batch >= 0, positions > 0, 0 < channels < 2^20, groups dividing channels, at most 32768 channels and
- * fewer than 2^31 values to a group, strides >= 0; batch * positions * (channels or the strides) < 2^60.  Base addresses 16-byte aligned;
- * strides need no alignment, but the loads are as wide as channels / groups and the strides allow.
+ * fewer than 2^31 values to a group, strides >= 0; batch * positions * (channels or the strides) < 2^60.
+ * Base addresses 16-byte aligned; strides need no alignment, but the loads are as wide as channels / groups and
+ * the strides allow.
  * weight (NULL = 1), bias (NULL = 0) and gate are nullable; act must be SSD_ACT_NONE with a gate.
- * Sums are fp32 (variances about a value of the data, joined by the differences of the means) and y is
+ * Sums are fp32 (variances over short runs about a value of the data, joined by the differences of the means,
+ * and means as differences from one of them: a constant group is normalised to exactly zeros) and y is
  * rounded once.  No atomics: bitwise reproducible.  A NaN or an infinity stays in its sample's group
  * (and, in d_weight and d_bias, its channels; d_x and y elsewhere are not touched).
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,

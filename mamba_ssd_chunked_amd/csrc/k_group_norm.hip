@@ -18,8 +18,8 @@
 // EV is the widest vector of 16 bytes or less that a group's channels divide into, or with positions a slab's of
 // whole groups.
 // Measured: 8192 tokens x 80 groups of 64 under a gate bf16 48 us (5.3 TB/s); 4 x 16384 positions x 512 channels with
-// SiLU bf16 16 us for the statistics (4.4 TB/s), 4 to join them, 24 for the outputs (5.6 TB/s); 8192 tokens x 24
-// groups of 64 fp32 under a gate 24 us (6.3 TB/s), their gradient 52 (5.1 TB/s) and 4.
+// SiLU bf16 16 us for the statistics (4.2 TB/s), 3 to join them, 25 for the outputs (5.5 TB/s); 8192 tokens x 24
+// groups of 64 fp32 under a gate 24 us (6.3 TB/s), their gradient 52-54 (5.0 TB/s) and 4.
 #include <type_traits>
 
 #include "ssd_device.hpp"

@@ -107,7 +107,9 @@ namespace {
 // A gradient in n segments, in us, as measured with p = 64 and r = 128 on a chip of 512 places (two workgroups
 // a CU): a chunk of a workgroup takes 5.3 (bf16 3.0), 7.4 (4.0) with the decay's gradient beside it, less alone
 // on its CU; beyond the places a round more and half of one for its uneven end.  A chunk carried takes 2 (1), 6
-// (4) with the state's derivative, and the launches between 15 or 25.  Narrower states take less, to a floor.
+// (4) with the state's derivative, and the launches between 15 or 25.  Narrower states are taken to need less, to a
+// floor, in proportion: at twelve shapes of other widths (16 to 128) the rule was within 7 % of the best of 1 to 16
+// segments eight times and 12 to 24 % above it four times (bf16, 64 heads of 4096 tokens, 128 x 128, 384 us for 321).
 double gradient_time(const LinearShape& d, bool decay, int n) {
     auto rounds = [](double wgs) { return wgs <= 256.0 ? 0.73 : wgs <= 512.0 ? 1.0 : wgs / 512.0 + 0.5; };
     const bool bf = d.io == 1;
@@ -121,17 +123,17 @@ double gradient_time(const LinearShape& d, bool decay, int n) {
 
 }  // namespace
 
-// Forwards, as many segments as give the chip's 512 places (two workgroups a CU) a workgroup each, of at least
-// two chunks.  Whole where heads alone take more than half the places, or where the chunks that a workgroup is
+// Forwards, as many segments as give 512 places (two workgroups a CU, as the registers allow; bf16 with r = 128 three,
+// which does not show in a fourth segment below) a workgroup each, of at least two chunks.  Whole where heads alone take more than half the places, or where the chunks that a workgroup is
 // spared (2 us each in bf16 and 3.5 in fp32 with r = 128, half of that with narrow keys) do not pay for
 // carrying (half as long a chunk) and for two more launches.  Measured in 1 to 32 segments: bf16, p = 64,
-// r = 128, 160 heads of 4096 tokens 268 us whole, 202 in three, 221 in five; 96 of 1531 107 whole, 66 in five;
-// 32 of 8192 523 whole, 98 in sixteen; fp32 8 of 1024 125 whole, 35 in sixteen.
+// r = 128, 160 heads of 4096 tokens 272 us whole, 216 in three, 219 in four, 234 in five; 96 of 1531 105 whole, 67 in
+// five; 32 of 8192 525 whole, 101 in sixteen; fp32 8 of 1024 126 whole, 33 in sixteen.
 // Backwards, where a head has workgroups of several kinds and the rounds end unevenly, the number of segments
 // of four chunks or more with the least gradient_time.  Measured in 1 to 24 segments, p = 64, r = 128, with the
-// decay's gradient, fp32: 48 heads of 2048 tokens 333 us whole, 383 in two, 276 in eight; 32 of 16384 2655
-// whole, 1498 in four, 1202 in sixteen; 160 of 4096 1590 whole, 1507 in four; without it, bf16: 96 of 2048 191
-// whole, 169 in four; 160 of 4096 439 whole, 528 in four.
+// decay's gradient, fp32: 48 heads of 2048 tokens 329 us whole, 391 in two, 291 in eight; 32 of 16384 2509
+// whole, 1489 in four, 1196 in sixteen; 160 of 4096 1513 whole, 1445 in four; without it, bf16: 96 of 2048 192
+// whole, 184 in four; 160 of 4096 411 whole, 526 in four.
 int linear_segments(const LinearShape& d, bool bwd, bool decay) {
     const int64_t heads = static_cast<int64_t>(d.B) * d.H, wgs = heads * (bwd ? linear_grad_blocks(d, decay) : linear_blocks(d));
     if (wgs == 0) return 1;

@@ -4,8 +4,8 @@
 // decay: all in one launch, those of a head side by side, so that what two of them read meets in an L2.
 // (One launch each, 160 heads of 4096 tokens: d_v 275 us on 160 of the 256 CUs, d_q and d_k 421 us.)
 // What bounds it: the LDS reads of operands and the vector unit that cuts fp32 into parts, a chunk's barriers
-// between them.  p = 64, r = 128, 160 heads of 4096 tokens: bf16 414 us, with the decay's gradient 736; fp32
-// 732 and 1499.
+// between them.  A call with p = 64, r = 128, 160 heads of 4096 tokens: bf16 398-414 us, with the decay's gradient
+// 732; fp32 732-756 and 1432.
 #include "linear_scan.hpp"
 
 namespace ssd {

@@ -3,9 +3,9 @@
 // Per (batch row, head) with the state S [p, r] of the row's slot and a = exp(log_decay):
 //   S' = a S + v k^T,   y = scale S' q = scale (a (S q) + v (k.q)).
 // The dot product is taken of the old state, so that a state element is read once and written once:
-// 8 bytes for 5 flops, bound by HBM (64 rows of 80 heads, p = 64, r = 128, bf16 60 us, 5.4 TB/s).  A state row (r / 4 float4s) is held by r / 4 consecutive lanes,
-// which add up S q; a thread's state loads are all issued before their first use.  The state is updated
-// in place: each element is read and written by the same thread.
+// 8 bytes for 5 flops, bound by HBM (64 rows of 80 heads, p = 64, r = 128, bf16 60 us, 5.4 TB/s).  A state row
+// (r / 4 float4s) is held by r / 4 consecutive lanes, which add up S q; a thread's state loads are all issued before
+// their first use.  The state is updated in place: each element is read and written by the same thread.
 #include <type_traits>
 
 #include "delta_device.hpp"

@@ -37,8 +37,9 @@ EXPORTS = ("ssd_workspace_size", "ssd_fwd", "ssd_fwd_noalloc", "ssd_bwd", "ssd_s
            "ssd_step", "ssd_delta_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd",
            "ssd_delta_step", "ssd_linear_workspace_size", "ssd_linear_fwd", "ssd_linear_bwd",
            "ssd_linear_step", "ssd_rms_norm", "ssd_rms_norm_bwd", "ssd_rms_norm_workspace_size",
-           "ssd_group_norm_workspace_size", "ssd_group_norm", "ssd_group_norm_bwd", "ssd_last_error", "ssd_debug_enable", "ssd_timing_enable",
-           "ssd_timing_collect", "ssd_bwd_partial_region", "ssd_stream_probe")
+           "ssd_group_norm_workspace_size", "ssd_group_norm", "ssd_group_norm_bwd",
+           "ssd_last_error", "ssd_debug_enable", "ssd_timing_enable", "ssd_timing_collect",
+           "ssd_bwd_partial_region", "ssd_stream_probe")
 
 
 class ssd_dims(ctypes.Structure):
@@ -1151,7 +1152,9 @@ def group_norm_workspace(x, groups, gate=None, bwd=False) -> torch.Tensor:
 def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act="none", gate=None, want_y=True,
                want_stats=False, ws=None, stream=None):
     """Group norm of x ``[n, ..., channels]`` (fp32 or bf16; see ssd_group_norm): each sample's positions and
-    the channels of a group are normalised together, so tokens ``[n, channels]`` each by itself.  act
+    the channels of a group are normalised together.  Tokens to be normalised each by itself (the heads of an
+    attention's output) are samples ``[b * s, channels]``: as ``[b, s, channels]`` they would be positions of b
+    samples, and an earlier token's output would depend on the later ones.  act
     "silu" is taken of the result; a gate like x multiplies it by its SiLU instead.  x and gate may be
     slices of wider rows.  Returns a dict of ``y`` (like x, contiguous) and, where wanted, ``stats`` (fp32
     ``[n, groups, 2]``, the mean and 1 / sqrt(var + eps)), which group_norm_bwd takes."""
