@@ -510,7 +510,8 @@ int ssd_rms_norm_workspace_size(int64_t rows, int64_t width, size_t* bytes);
  * the strides allow.
  * weight (NULL = 1), bias (NULL = 0) and gate are nullable; act must be SSD_ACT_NONE with a gate.
  * Sums are fp32 (variances over short runs about a value of the data, joined by the differences of the means,
- * and means as differences from one of them: a constant group is normalised to exactly zeros) and y is
+ * and means as differences from one of them: a constant group is normalised to exactly zeros;
+ * the gradients' sums over more than 256 positions or tokens go on in 64 bits) and y is
  * rounded once.  No atomics: bitwise reproducible.  A NaN or an infinity stays in its sample's group
  * (and, in d_weight and d_bias, its channels; d_x and y elsewhere are not touched).
  * Errors: SSD_ERR_NULL, SSD_ERR_SHAPE, SSD_ERR_UNSUPPORTED, SSD_ERR_DTYPE, SSD_ERR_WORKSPACE,

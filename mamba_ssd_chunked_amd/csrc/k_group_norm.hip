@@ -20,6 +20,7 @@
 // Measured: 8192 tokens x 80 groups of 64 under a gate bf16 48 us (5.3 TB/s); 4 x 16384 positions x 512 channels with
 // SiLU bf16 16 us for the statistics (4.2 TB/s), 3 to join them, 25 for the outputs (5.5 TB/s); 8192 tokens x 24
 // groups of 64 fp32 under a gate 24 us (6.3 TB/s), their gradient 52-54 (5.0 TB/s) and 4.
+#include <algorithm>
 #include <type_traits>
 
 #include "ssd_device.hpp"
@@ -584,9 +585,9 @@ __global__ __launch_bounds__(256) void k_group_norm_sums(GroupShape d, const typ
         __syncthreads();
         for (int k = threadIdx.x; k < 2 * p.nch; k += 256) {
             const int which = k >= p.nch, c = k - which * p.nch;
-            float sum = 0.0f;
+            double sum = 0.0;
             for (int l = 0; l < p.lanes; ++l) sum += sh[which * EV + c % EV][l * p.cv + c / EV];
-            part[((p.n * d.sums.blocks + p.block) * 2 + which) * d.c + p.ch0 + c] = sum;
+            part[((p.n * d.sums.blocks + p.block) * 2 + which) * d.c + p.ch0 + c] = static_cast<float>(sum);
         }
     }
 }
@@ -596,7 +597,7 @@ __global__ __launch_bounds__(256) void k_group_norm_sums(GroupShape d, const typ
 __global__ __launch_bounds__(256) void k_group_norm_means(GroupShape d, const float* __restrict__ part,
                                                           const float* __restrict__ weight, float* __restrict__ chan,
                                                           float2* __restrict__ mean) {
-    __shared__ float sh[2][256];
+    __shared__ double sh[2][256];
     int cw = 1;  // channels at a time, as many lanes as are left for each
     while (cw < d.cg && cw < 256) cw *= 2;
     const int lanes = 256 / cw, lc = threadIdx.x % cw, bl = threadIdx.x / cw;
@@ -606,7 +607,7 @@ __global__ __launch_bounds__(256) void k_group_norm_means(GroupShape d, const fl
         float s1 = 0.0f, s2 = 0.0f;
         for (int c0 = 0; c0 < d.cg; c0 += cw) {
             const int c = c0 + lc, ch = g * d.cg + c;
-            float a = 0.0f, b = 0.0f;
+            double a = 0.0, b = 0.0;
             if (c < d.cg) {
 #pragma unroll 4
                 for (int k = bl; k < d.sums.blocks; k += lanes) {
@@ -623,11 +624,11 @@ __global__ __launch_bounds__(256) void k_group_norm_means(GroupShape d, const fl
                     a += sh[0][l * cw + lc];
                     b += sh[1][l * cw + lc];
                 }
-                chan[(2 * n) * d.c + ch] = b;
-                chan[(2 * n + 1) * d.c + ch] = a;
-                const float w = weight ? weight[ch] : 1.0f;
-                s1 += w * a;
-                s2 += w * b;
+                const float w = weight ? weight[ch] : 1.0f, du = static_cast<float>(a), dum = static_cast<float>(b);
+                chan[(2 * n) * d.c + ch] = dum;
+                chan[(2 * n + 1) * d.c + ch] = du;
+                s1 += w * du;
+                s2 += w * dum;
             }
         }
         s1 = team_sum<64>(s1);
@@ -639,8 +640,8 @@ __global__ __launch_bounds__(256) void k_group_norm_means(GroupShape d, const fl
         }
         __syncthreads();
         if (threadIdx.x == 0)
-            mean[item] = make_float2((sh[0][0] + sh[0][1] + sh[0][2] + sh[0][3]) * d.inv_count,
-                                     (sh[1][0] + sh[1][1] + sh[1][2] + sh[1][3]) * d.inv_count);
+            mean[item] = make_float2(static_cast<float>(sh[0][0] + sh[0][1] + sh[0][2] + sh[0][3]) * d.inv_count,
+                                     static_cast<float>(sh[1][0] + sh[1][1] + sh[1][2] + sh[1][3]) * d.inv_count);
     }
 }
 
@@ -658,19 +659,21 @@ __global__ __launch_bounds__(256) void k_group_norm_grad(GroupShape d, const typ
                                                          typename IO::T* __restrict__ d_gate,
                                                          const float* __restrict__ chan, int sums,
                                                          float* __restrict__ d_weight, float* __restrict__ d_bias) {
-    __shared__ float sh[8][33];
+    __shared__ double sh[8][33];
     const Act act{d.act, gate != nullptr};
     if (static_cast<int>(blockIdx.x) < sums) {
         const int l = threadIdx.x & 31, run = threadIdx.x >> 5, which = blockIdx.x & 1, col = (blockIdx.x >> 1) * 32 + l;
         float* to = which ? d_bias : d_weight;
-        float acc = 0.0f;
-        if (col < d.c)
+        double acc = 0.0;
+        if (col < d.c) {
+#pragma unroll 8  // as many loads under way
             for (int64_t n = run; n < d.n; n += 8) acc += chan[(2 * n + which) * d.c + col];
+        }
         sh[run][l] = acc;
         __syncthreads();
         if (run == 0 && col < d.c && to) {
             for (int m = 1; m < 8; ++m) acc += sh[m][l];
-            to[col] = acc;
+            to[col] = static_cast<float>(acc);
         }
         return;
     }
@@ -713,12 +716,12 @@ __global__ __launch_bounds__(256) void k_group_norm_grad(GroupShape d, const typ
 // d_weight, d_bias [c] = sums over parts of part [parts, 2, c]: 32 columns x 32 interleaved runs of parts.
 __global__ __launch_bounds__(1024) void k_group_norm_weight(const float* __restrict__ part, int64_t parts, int c,
                                                             float* __restrict__ d_weight, float* __restrict__ d_bias) {
-    __shared__ float sh[32][33];
+    __shared__ double sh[32][33];
     const int l = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int col = static_cast<int>(blockIdx.x) * 32 + l;
     float* to = blockIdx.y ? d_bias : d_weight;
     if (!to) return;
-    float acc = 0.0f;
+    double acc = 0.0;
     if (col < c) {
 #pragma unroll 8  // as many loads under way
         for (int64_t t = run; t < parts; t += 32) acc += part[(2 * t + blockIdx.y) * c + col];
@@ -726,10 +729,10 @@ __global__ __launch_bounds__(1024) void k_group_norm_weight(const float* __restr
     sh[run][l] = acc;
     __syncthreads();
     if (run == 0 && col < c) {
-        acc = 0.0f;
+        acc = 0.0;
 #pragma unroll
         for (int m = 0; m < 32; ++m) acc += sh[m][l];
-        to[col] = acc;
+        to[col] = static_cast<float>(acc);
     }
 }
 
@@ -775,8 +778,16 @@ hipError_t by_io(const GroupShape& d, F&& f) {
 
 }  // namespace
 
+// Positions or tokens whose terms a thread of the gradient adds up in fp32: of one sign and size their roundings go to
+// one side, half of such a step for each in the end (1e-5 of the sum over 1000, 4e-5 over 4000).  The rest goes in fp64.
+constexpr int64_t kMaxRun = 256;
+
 // Which way, and how the work is cut up.
 void group_norm_plan(GroupShape* d, bool bwd) {
+    // blocks of `rows` over `lanes` by which a thread has no more than kMaxRun of them (as far as a launch goes)
+    auto short_runs = [](int64_t rows, int64_t lanes, int64_t slabs) {
+        return std::min((rows + kMaxRun * lanes - 1) / (kMaxRun * lanes), std::max<int64_t>(kMaxGroups / slabs, 1));
+    };
     const int V = d->io == 1 ? 8 : 4;
     auto widest = [&](int of) {
         int ev = V;
@@ -796,6 +807,7 @@ void group_norm_plan(GroupShape* d, bool bwd) {
         int64_t b = 2048 / c.slabs;
         const int64_t most = (d->n + c.lanes - 1) / c.lanes;
         if (b > 1024 / c.lanes) b = 1024 / c.lanes;
+        b = std::max(b, short_runs(d->n, c.lanes, c.slabs));
         if (b > most) b = most;
         c.blocks = static_cast<int>(b < 1 ? 1 : b);
         return;
@@ -812,7 +824,7 @@ void group_norm_plan(GroupShape* d, bool bwd) {
     d->sub = 1;
     while (2 * d->sub <= d->ev && d->cg % (2 * d->sub) == 0) d->sub *= 2;
     const int unit_vectors = unit * d->cg / d->ev;
-    auto cut = [&](int units, int each, int most) {
+    auto cut = [&](int units, int each, int most, bool runs) {
         GroupCut c{};
         c.cuts = unit_vectors > 256 ? (unit_vectors + 255) / 256 : 1;
         c.slab_groups = units < 2 ? unit : units * unit;
@@ -826,14 +838,15 @@ void group_norm_plan(GroupShape* d, bool bwd) {
         if (b > most / c.cuts) b = most / c.cuts;
         if (b > whole) b = whole;
         if (b < 1) b = 1;
+        if (runs) b = std::max(b, short_runs(d->s, c.lanes, c.slabs));
         c.rows = (d->s + b - 1) / b;
         c.blocks = static_cast<int>((d->s + c.rows - 1) / c.rows);
         return c;
     };
     // sums: about 256 bytes of neighbouring channels, which leave many positions to a workgroup and few
     // records to a group; outputs: whole rows
-    d->sums = cut((15 + unit_vectors) / unit_vectors, 8, MAXREC);
-    d->outs = cut(256 / unit_vectors, 4, 1 << 20);
+    d->sums = cut((15 + unit_vectors) / unit_vectors, 8, MAXREC, bwd);
+    d->outs = cut(256 / unit_vectors, 4, 1 << 20, false);
     d->whole = d->sums.blocks == 1 && d->sums.cuts == 1;
 }
 
