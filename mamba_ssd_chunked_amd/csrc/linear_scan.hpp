@@ -578,6 +578,7 @@ struct LinearScan {
         double kept = exp2(l2 * C);  // what the state keeps over a chunk, to more than 24 bits: it is raised
         float keep = static_cast<float>(kept), keep_lo = static_cast<float>(kept - keep);  // to the number of chunks
         double dot = 0.0;
+#pragma unroll 1  // (a first chunk of its own, which the compiler makes otherwise, doubles the code: bf16 prompt 182 -> 185 us)
         for (int c = c0; c < c1; ++c) {
             const int n = len - c * C < C ? len - c * C : C;  // tokens of the chunk
             if constexpr (PLAIN)
